@@ -3,11 +3,13 @@
 Thin ctypes binding over libmoe_ep.so (declared in include/moe_ep.h).  The
 Python functions carry the C names and only marshal arguments: torch tensors
 supply device memory and the current HIP stream, every step of the path runs
-in the library's HIP kernels.  Importing this package fails loudly when the
+in the library's HIP kernels.  ``router`` and ``balance_loss`` are the same
+calls as autograd functions.  Importing this package fails loudly when the
 library has not been built; there is no CPU fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import os
@@ -20,12 +22,15 @@ LIB_PATH = os.path.join(_HERE, "libmoe_ep.so")
 
 MOE_OK, MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_ALIGN, MOE_ERR_WORKSPACE, MOE_ERR_HIP = range(6)
 MOE_PAD_NONE, MOE_PAD_MULTIPLE, MOE_PAD_CAPACITY = 0, 1, 2
+MOE_F32, MOE_BF16 = 0, 1
+MOE_ACT_NONE, MOE_ACT_SWIGLU = 0, 1
 MOE_FLAG_BAD_EXPERT, MOE_FLAG_CAPACITY, MOE_FLAG_UNBALANCED = 1, 2, 4
 
 EXPORTED = ("moe_max_recv_rows", "moe_layout_workspace_bytes", "moe_layout", "moe_dispatch",
             "moe_layout_dispatch", "moe_combine", "moe_layout_balanced_workspace_bytes", "moe_layout_balanced",
             "moe_zero_padding", "moe_stream_create_cu_limited", "moe_stream_create_cu_range", "moe_stream_destroy",
-            "moe_status_str", "moe_layout_noalloc")
+            "moe_status_str", "moe_layout_noalloc", "moe_router_workspace_bytes", "moe_router", "moe_balance_loss",
+            "moe_router_backward", "moe_quantize_mx4", "moe_dequantize_mx4", "moe_dispatch_mx4", "moe_expert_gemm_mx4")
 
 
 class MoeError(RuntimeError):
@@ -46,6 +51,15 @@ class moe_layout_bufs(ctypes.Structure):
 
 class moe_balance_bufs(ctypes.Structure):
     _fields_ = [("seg_offset", ctypes.c_void_p), ("slot_expert", ctypes.c_void_p)]
+
+
+class moe_router_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("S", "E", "K", "n_groups", "topk_groups", "renorm", "seq_len")] + \
+               [("alpha", ctypes.c_float)]
+
+
+class moe_router_bufs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("topk_idx", "topk_w", "expert_count", "balance_coef", "balance_loss")]
 
 
 def _load():
@@ -86,6 +100,19 @@ def _load():
     L.moe_status_str.restype = ctypes.c_char_p
     L.moe_layout_noalloc.argtypes = [D, P, B, P]
     L.moe_layout_noalloc.restype = ctypes.c_int
+    I, I64, RD, RB = ctypes.c_int32, ctypes.c_int64, ctypes.POINTER(moe_router_desc), ctypes.POINTER(moe_router_bufs)
+    L.moe_router_workspace_bytes.argtypes = [RD]
+    L.moe_router_workspace_bytes.restype = ctypes.c_size_t
+    L.moe_router.argtypes = [RD, P, I, P, RB, P, ctypes.c_size_t, P]
+    L.moe_balance_loss.argtypes = [RD, P, I, P, P, RB, P, ctypes.c_size_t, P]
+    L.moe_router_backward.argtypes = [RD, P, I, P, P, P, P, P, P, P, P]
+    L.moe_quantize_mx4.argtypes = [P, I64, I, P, P, P, P]
+    L.moe_dequantize_mx4.argtypes = [P, P, I64, I, P, P, P]
+    L.moe_dispatch_mx4.argtypes = [D, B, P, I, P, P, P, P, P]
+    L.moe_expert_gemm_mx4.argtypes = [D, B, ctypes.POINTER(moe_balance_bufs), I, P, P, I, P, P, I, I, P, P]
+    for f in (L.moe_router, L.moe_balance_loss, L.moe_router_backward, L.moe_quantize_mx4, L.moe_dequantize_mx4,
+              L.moe_dispatch_mx4, L.moe_expert_gemm_mx4):
+        f.restype = ctypes.c_int
     return L
 
 
@@ -422,6 +449,374 @@ def moe_zero_padding(desc: LayoutDesc, layout: Layout, recv: torch.Tensor, recv_
 
 
 # ---------------------------------------------------------------------------
+# Router and balance loss
+# ---------------------------------------------------------------------------
+
+def _alloc_on(stream):
+    """Where a call's own outputs come from: memory of the stream that will
+    write them, so that the allocator hands it out again in that stream's order."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _on_device(device):
+    """The C calls launch on the current device: make it the tensors' own."""
+    if device.type != "cuda" or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+@dataclasses.dataclass(frozen=True)
+class RouterDesc:
+    """A router's shape and rule (fields as moe_router_desc; n_groups = 1 and
+    seq_len = 0: no groups, one sequence)."""
+    S: int
+    E: int
+    K: int
+    n_groups: int = 1
+    topk_groups: Optional[int] = None   # None: every group
+    renorm: bool = True
+    seq_len: int = 0
+    alpha: float = 1.0
+
+    @property
+    def sequences(self) -> int:
+        return self.S // self.seq_len if self.seq_len else 1
+
+    def c(self) -> moe_router_desc:
+        return moe_router_desc(self.S, self.E, self.K, self.n_groups,
+                               self.n_groups if self.topk_groups is None else self.topk_groups, 1 if self.renorm else 0,
+                               self.seq_len, self.alpha)
+
+
+@dataclasses.dataclass
+class Router:
+    """Device tensors of one batch's routing.  The last four are None without the loss,
+    the first two without a routing of moe_router's own."""
+    topk_idx: Optional[torch.Tensor]       # [S,K] int32
+    topk_w: Optional[torch.Tensor]         # [S,K] fp32
+    expert_count: Optional[torch.Tensor]   # [G,E] int32
+    balance_coef: Optional[torch.Tensor]   # [G,E] fp32
+    balance_loss: Optional[torch.Tensor]   # [1] fp32
+    workspace: Optional[torch.Tensor] = None
+
+    def c(self) -> moe_router_bufs:
+        return moe_router_bufs(_ptr(self.topk_idx), _ptr(self.topk_w), _ptr(self.expert_count), _ptr(self.balance_coef),
+                               _ptr(self.balance_loss))
+
+
+def moe_router_workspace_bytes(desc: RouterDesc) -> int:
+    return int(_lib.moe_router_workspace_bytes(ctypes.byref(desc.c())))
+
+
+def alloc_router(desc: RouterDesc, device, picks: bool = True, loss: bool = True) -> Router:
+    """Device buffers for moe_router's outputs (``picks``: the routing, ``loss``:
+    counts, coefficients, the loss and its workspace)."""
+    S, E, K, G = desc.S, desc.E, desc.K, desc.sequences
+    i32, f32 = dict(dtype=torch.int32, device=device), dict(dtype=torch.float32, device=device)
+    r = Router(None, None, None, None, None)
+    if picks:
+        r.topk_idx, r.topk_w = torch.empty((S, K), **i32), torch.empty((S, K), **f32)
+    if loss:
+        ws = moe_router_workspace_bytes(desc)
+        if ws == 0:
+            raise MoeError(MOE_ERR_SHAPE, "alloc_router")
+        r.expert_count, r.balance_coef = torch.empty((G, E), **i32), torch.empty((G, E), **f32)
+        r.balance_loss = torch.empty(1, **f32)
+        r.workspace = torch.empty(ws, dtype=torch.uint8, device=device)
+    return r
+
+
+def _logits(desc: RouterDesc, logits: torch.Tensor, token_mask) -> int:
+    """Checks a router call's inputs; the C type of the logits."""
+    _check(logits, "logits", (torch.float32, torch.bfloat16), (desc.S, desc.E))
+    _check(token_mask, "token_mask", (torch.bool, torch.uint8), (desc.S,), logits.device)
+    return MOE_BF16 if logits.dtype == torch.bfloat16 else MOE_F32
+
+
+def _check_router(desc: RouterDesc, r: Router, picks: bool, loss: bool, device):
+    if picks and (r.topk_idx is None or r.topk_w is None):
+        raise ValueError("router has no buffers for the routing")
+    if picks:
+        _check(r.topk_idx, "topk_idx", torch.int32, (desc.S, desc.K), device)
+        _check(r.topk_w, "topk_w", torch.float32, (desc.S, desc.K), device)
+    if loss:
+        if r.balance_loss is None or r.expert_count is None or r.balance_coef is None:
+            raise ValueError("router has no buffers for the loss")
+        _check(r.expert_count, "expert_count", torch.int32, (desc.sequences, desc.E), device)
+        _check(r.balance_coef, "balance_coef", torch.float32, (desc.sequences, desc.E), device)
+        _check(r.balance_loss, "balance_loss", torch.float32, (1,), device)
+        _check(r.workspace, "workspace", torch.uint8, None, device)
+
+
+def moe_router(desc: RouterDesc, logits: torch.Tensor, token_mask=None, loss: bool = True,
+               router: Optional[Router] = None, stream=None) -> Router:
+    """Top-k routing of logits [S,E] (fp32 or bf16), with the balance loss and
+    the counts unless ``loss`` is false (serving: one launch, no workspace).
+    token_mask [S] (bool or uint8): false where a token does not count.
+    Entries without a pick are -1 with weight 0."""
+    dev = logits.device
+    kind = _logits(desc, logits, token_mask)
+    if router is None:
+        with _alloc_on(stream):
+            router = alloc_router(desc, dev, loss=loss)
+    else:
+        _check_router(desc, router, True, loss, dev)
+    ws = router.workspace if loss else None
+    b = router.c()
+    if not loss:
+        b.expert_count = b.balance_coef = b.balance_loss = None
+    with _on_device(dev):
+        rc = _lib.moe_router(ctypes.byref(desc.c()), _ptr(logits), kind, _ptr(token_mask), ctypes.byref(b), _ptr(ws),
+                             0 if ws is None else ws.numel(), _stream(stream, dev))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_router")
+    return router
+
+
+def moe_balance_loss(desc: RouterDesc, logits: torch.Tensor, topk_idx: torch.Tensor, token_mask=None,
+                     router: Optional[Router] = None, stream=None) -> Router:
+    """Balance loss and per-expert counts of the routing topk_idx [S,K] int32
+    that the caller made.  The result holds expert_count, balance_coef and
+    balance_loss; moe_router_backward takes it without d_topk_w."""
+    dev = logits.device
+    kind = _logits(desc, logits, token_mask)
+    _check(topk_idx, "topk_idx", torch.int32, (desc.S, desc.K), dev)
+    if router is None:
+        with _alloc_on(stream):
+            router = alloc_router(desc, dev, picks=False)
+    else:
+        _check_router(desc, router, False, True, dev)
+    ws = router.workspace
+    with _on_device(dev):
+        rc = _lib.moe_balance_loss(ctypes.byref(desc.c()), _ptr(logits), kind, _ptr(topk_idx), _ptr(token_mask),
+                                   ctypes.byref(router.c()), _ptr(ws), 0 if ws is None else ws.numel(),
+                                   _stream(stream, dev))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_balance_loss")
+    return router
+
+
+def moe_router_backward(desc: RouterDesc, logits: torch.Tensor, router: Router, d_topk_w=None, d_loss=None,
+                        token_mask=None, d_logits=None, stream=None) -> torch.Tensor:
+    """d logits, from the gradients of the route weights (d_topk_w [S,K] fp32)
+    and of the balance loss (d_loss, one fp32 value), at least one of them.
+    desc, logits, router and token_mask as moe_router had and returned them."""
+    dev = logits.device
+    kind = _logits(desc, logits, token_mask)
+    _check_router(desc, router, d_topk_w is not None, d_loss is not None, dev)
+    _check(d_topk_w, "d_topk_w", torch.float32, (desc.S, desc.K), dev)
+    _check(d_loss, "d_loss", torch.float32, None, dev)
+    if d_loss is not None and d_loss.numel() != 1:
+        raise ValueError(f"d_loss: {d_loss.numel()} values, expected 1")
+    if d_logits is None:
+        with _alloc_on(stream):
+            d_logits = torch.empty_like(logits)
+    _check(d_logits, "d_logits", logits.dtype, (desc.S, desc.E), dev)
+    with _on_device(dev):
+        rc = _lib.moe_router_backward(ctypes.byref(desc.c()), _ptr(logits), kind, _ptr(token_mask),
+                                      _ptr(router.topk_idx), _ptr(router.topk_w), _ptr(router.balance_coef),
+                                      _ptr(d_topk_w), _ptr(d_loss), _ptr(d_logits), _stream(stream, dev))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_router_backward")
+    return d_logits
+
+
+def _no_capture(what: str):
+    # autograd joins the streams of the leaves that live outside the capture
+    if torch.cuda.is_current_stream_capturing():
+        raise RuntimeError(f"{what} cannot be captured into a graph: capture moe_router / moe_balance_loss and "
+                           "moe_router_backward instead")
+
+
+class _RouterFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, desc, token_mask, topk_idx):
+        ctx.set_materialize_grads(False)
+        given = topk_idx is not None
+        r = moe_balance_loss(desc, logits, topk_idx, token_mask) if given else moe_router(desc, logits, token_mask)
+        loss = r.balance_loss.view(())
+        ctx.desc, ctx.given = desc, given
+        ctx.save_for_backward(logits, token_mask, r.topk_idx, r.topk_w, r.balance_coef)
+        ctx.mark_non_differentiable(*(t for t in (r.topk_idx, r.expert_count) if t is not None))
+        return loss, r.expert_count, r.topk_idx, r.topk_w
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_loss, _count, _idx, d_w):
+        if d_loss is None and d_w is None:
+            return None, None, None, None
+        logits, token_mask, idx, w, coef = ctx.saved_tensors
+        _no_capture("the backward pass of router / balance_loss")
+        G, E = ctx.desc.sequences, ctx.desc.E
+        # the backward call reads balance_coef; the two others stand in for outputs that it does not read
+        r = Router(idx, w, torch.empty((G, E), dtype=torch.int32, device=coef.device), coef,
+                   torch.empty(1, device=coef.device))
+        d = moe_router_backward(ctx.desc, logits, r, None if d_w is None else d_w.contiguous(),
+                                None if d_loss is None else d_loss.contiguous(), token_mask)
+        return d, None, None, None
+
+
+def router(desc: RouterDesc, logits: torch.Tensor, token_mask=None):
+    """moe_router as an autograd function of the logits: (topk_idx, topk_w,
+    balance_loss, expert_count), of which topk_w and balance_loss (a scalar)
+    carry gradients.  Not capturable; moe_router and moe_router_backward are."""
+    _no_capture("router")
+    loss, count, idx, w = _RouterFunction.apply(logits, desc, token_mask, None)
+    return idx, w, loss, count
+
+
+def balance_loss(desc: RouterDesc, logits: torch.Tensor, topk_idx: torch.Tensor, token_mask=None):
+    """moe_balance_loss as an autograd function of the logits: (balance_loss,
+    expert_count).  Not capturable, as router."""
+    _no_capture("balance_loss")
+    return _RouterFunction.apply(logits, desc, token_mask, topk_idx)[:2]
+
+
+# ---------------------------------------------------------------------------
+# MXFP4 rows and the experts' products
+# ---------------------------------------------------------------------------
+
+def _check_mx4(codes, scales, names, rows, H, device):
+    """Packed rows [.., H/2] and their scales [.., H/32], at least `rows` of them."""
+    for t, name, width in ((codes, names[0], H // 2), (scales, names[1], H // 32)):
+        if t is None:
+            raise ValueError(f"{name} is missing")
+        _check(t, name, torch.uint8, None, device)
+        if t.dim() != 2 or t.shape[1] != width or t.shape[0] < rows:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [at least {rows}, {width}]")
+
+
+def _mx4_width(H: int, what: str):
+    if H < 128 or H % 128:
+        raise MoeError(MOE_ERR_SHAPE, what)
+
+
+def _check_src(layout: Optional[Layout], rows: int, device):
+    if layout is None:
+        return None
+    _check(layout.src, "layout.src", torch.int32, None, device)
+    if layout.src.numel() < rows:
+        raise ValueError(f"layout.src: {layout.src.numel()} rows, expected at least {rows}")
+    return layout.src
+
+
+def moe_quantize_mx4(x: torch.Tensor, codes=None, scales=None, layout: Optional[Layout] = None, stream=None):
+    """bf16 rows [rows,H] -> MXFP4: (codes [rows,H/2] uint8, scales [rows,H/32]
+    uint8).  x may have leading dimensions (expert weights [E,N,H]); so have the
+    results then.  With ``layout`` only the rows that hold an entry are converted."""
+    dev, H = x.device, x.shape[-1]
+    _check(x, "x", torch.bfloat16)
+    _mx4_width(H, "moe_quantize_mx4")
+    rows = x.numel() // H
+    src = _check_src(layout, rows, dev)
+    with _alloc_on(stream):
+        if codes is None:
+            codes = torch.empty((*x.shape[:-1], H // 2), dtype=torch.uint8, device=dev)
+        if scales is None:
+            scales = torch.empty((*x.shape[:-1], H // 32), dtype=torch.uint8, device=dev)
+    _check(codes, "codes", torch.uint8, (*x.shape[:-1], H // 2), dev)
+    _check(scales, "scales", torch.uint8, (*x.shape[:-1], H // 32), dev)
+    with _on_device(dev):
+        rc = _lib.moe_quantize_mx4(_ptr(x), rows, H, _ptr(src), _ptr(codes), _ptr(scales), _stream(stream, dev))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_quantize_mx4")
+    return codes, scales
+
+
+def moe_dequantize_mx4(codes: torch.Tensor, scales: torch.Tensor, out=None, layout: Optional[Layout] = None, stream=None):
+    """MXFP4 rows -> bf16 [.., H].  With ``layout`` only the rows that hold an
+    entry are converted; the others keep what they held."""
+    dev, H = codes.device, codes.shape[-1] * 2
+    _check(codes, "codes", torch.uint8)
+    _mx4_width(H, "moe_dequantize_mx4")
+    _check(scales, "scales", torch.uint8, (*codes.shape[:-1], H // 32), dev)
+    rows = codes.numel() // (H // 2)
+    src = _check_src(layout, rows, dev)
+    if out is None:
+        with _alloc_on(stream):
+            out = torch.empty((*codes.shape[:-1], H), dtype=torch.bfloat16, device=dev)
+    _check(out, "out", torch.bfloat16, (*codes.shape[:-1], H), dev)
+    with _on_device(dev):
+        rc = _lib.moe_dequantize_mx4(_ptr(codes), _ptr(scales), rows, H, _ptr(src), _ptr(out), _stream(stream, dev))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_dequantize_mx4")
+    return out
+
+
+def moe_dispatch_mx4(desc: LayoutDesc, layout: Layout, hidden: torch.Tensor, topk_w=None, recv=None, recv_scales=None,
+                     recv_w=None, stream=None):
+    """moe_dispatch in MXFP4.  Returns (recv [max_recv,H/2] uint8, recv_scales
+    [max_recv,H/32] uint8, recv_w or None)."""
+    dev, H, rows = hidden.device, hidden.shape[-1], moe_max_recv_rows(desc)
+    _check(hidden, "hidden", torch.bfloat16, (desc.S, H))
+    _check(topk_w, "topk_w", torch.float32, (desc.S, desc.K), dev)
+    _mx4_width(H, "moe_dispatch_mx4")
+    if rows < 0:
+        raise MoeError(MOE_ERR_SHAPE, "moe_dispatch_mx4")
+    _check(layout.pos, "layout.pos", torch.int32, (desc.S, desc.K), dev)
+    with _alloc_on(stream):
+        if recv is None:
+            recv = torch.empty((rows, H // 2), dtype=torch.uint8, device=dev)
+        if recv_scales is None:
+            recv_scales = torch.empty((rows, H // 32), dtype=torch.uint8, device=dev)
+        if recv_w is None and topk_w is not None:
+            recv_w = torch.empty(rows, dtype=torch.float32, device=dev)
+    _check_mx4(recv, recv_scales, ("recv", "recv_scales"), rows, H, dev)
+    _check(recv_w, "recv_w", torch.float32, None, dev)
+    if recv_w is not None and recv_w.numel() < rows:
+        raise ValueError(f"recv_w: {recv_w.numel()} rows, expected at least {rows}")
+    d, b = desc.c(), layout.c()
+    with _on_device(dev):
+        rc = _lib.moe_dispatch_mx4(ctypes.byref(d), ctypes.byref(b), _ptr(hidden), H, _ptr(topk_w), _ptr(recv),
+                                   _ptr(recv_scales), _ptr(recv_w), _stream(stream, dev))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_dispatch_mx4")
+    return recv, recv_scales, recv_w
+
+
+def moe_expert_gemm_mx4(desc: LayoutDesc, layout: Layout, x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor,
+                        w_scales: torch.Tensor, act: int = MOE_ACT_NONE, out=None, balance: Optional[Balance] = None,
+                        slots_per_rank: int = 0, stream=None) -> torch.Tensor:
+    """Every expert's rows times its weights: out [max_recv,N] bf16.
+
+    x [max_recv,H/2] and x_scales [max_recv,H/32]: the receive buffer in MXFP4;
+    w [E,M,H/2] and w_scales [E,M,H/32]: the experts' weights, M = N, or 2N with
+    MOE_ACT_SWIGLU (N gate rows, then N up rows).  ``balance`` and
+    ``slots_per_rank`` for a layout of moe_layout_balanced.  Rows that hold no
+    entry are neither read nor written."""
+    dev, H, rows = x.device, x.shape[-1] * 2, moe_max_recv_rows(desc)
+    _mx4_width(H, "moe_expert_gemm_mx4")
+    if rows < 0 or act not in (MOE_ACT_NONE, MOE_ACT_SWIGLU):
+        raise MoeError(MOE_ERR_SHAPE, "moe_expert_gemm_mx4")
+    _check_mx4(x, x_scales, ("x", "x_scales"), rows, H, dev)
+    if w.dim() != 3 or (act == MOE_ACT_SWIGLU and w.shape[1] % 2):
+        raise ValueError(f"w: shape {tuple(w.shape)}, expected [E, N or 2N, H/2]")
+    M = w.shape[1]
+    N = M // 2 if act == MOE_ACT_SWIGLU else M
+    _check(w, "w", torch.uint8, (desc.E, M, H // 2), dev)
+    _check(w_scales, "w_scales", torch.uint8, (desc.E, M, H // 32), dev)
+    _check(layout.tokens_per_expert, "layout.tokens_per_expert", torch.int32, (desc.E,), dev)
+    _check(layout.expert_offset, "layout.expert_offset", torch.int32, (desc.E + 1,), dev)
+    if balance is not None:
+        _check(balance.seg_offset, "balance.seg_offset", torch.int32, (desc.E + desc.R * slots_per_rank + 1,), dev)
+        _check(balance.slot_expert, "balance.slot_expert", torch.int32, (max(desc.R * slots_per_rank, 1),), dev)
+    if out is None:
+        with _alloc_on(stream):
+            out = torch.empty((rows, N), dtype=torch.bfloat16, device=dev)
+    _check(out, "out", torch.bfloat16, None, dev)
+    if out.dim() != 2 or out.shape[1] != N or out.shape[0] < rows:
+        raise ValueError(f"out: shape {tuple(out.shape)}, expected [at least {rows}, {N}]")
+    d, b = desc.c(), layout.c()
+    bal = None if balance is None else ctypes.byref(balance.c())
+    with _on_device(dev):
+        rc = _lib.moe_expert_gemm_mx4(ctypes.byref(d), ctypes.byref(b), bal, slots_per_rank, _ptr(x), _ptr(x_scales), H,
+                                      _ptr(w), _ptr(w_scales), N, act, _ptr(out), _stream(stream, dev))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_expert_gemm_mx4")
+    return out
+
+
+# ---------------------------------------------------------------------------
 # Static-shape buffer: validate once, then bare C calls
 # ---------------------------------------------------------------------------
 
@@ -441,24 +836,32 @@ class Buffer:
     going to B replica slots per rank; MoonEP article, section 1); dispatch and
     combine are unchanged.  ``balance.slot_expert`` then tells which expert each
     slot must hold.
+
+    With ``mx4`` the rows travel in MXFP4 (recv [rows,H/2] and recv_scales
+    [rows,H/32], both uint8; moe_dispatch_mx4), and expert_gemm multiplies them
+    with the experts' weights, with either layout.
     """
 
     def __init__(self, S: int, H: int, K: int, E: int, R: int, fp8: bool = False,
                  pad_mode: int = MOE_PAD_NONE, pad_rows: int = 0, device="cuda",
-                 balance_slots: Optional[int] = None):
+                 balance_slots: Optional[int] = None, mx4: bool = False):
         if balance_slots is not None and pad_mode != MOE_PAD_NONE:
             raise MoeError(MOE_ERR_SHAPE, "Buffer: the balanced layout has no padding")
         self.desc = LayoutDesc(S, K, E, R, pad_mode, pad_rows)
         self.rows = moe_max_recv_rows(self.desc)
-        if self.rows < 0 or H < 8 or H % 8 or (fp8 and H % 128):
+        if self.rows < 0 or H < 8 or H % 8 or ((fp8 or mx4) and H % 128) or (fp8 and mx4):
             raise MoeError(MOE_ERR_SHAPE, "Buffer")
         dev = torch.device(device)
         if dev.type == "cuda" and dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
-        self.H, self.fp8, self.device = H, fp8, dev
+        self.H, self.fp8, self.mx4, self.device = H, fp8, mx4, dev
         self.layout = alloc_layout(self.desc, dev)
-        self.recv = torch.empty((self.rows, H), dtype=torch.uint8 if fp8 else torch.bfloat16, device=dev)
-        self.recv_scales = torch.empty((self.rows, H // 128), dtype=torch.float32, device=dev) if fp8 else None
+        if mx4:
+            self.recv = torch.empty((self.rows, H // 2), dtype=torch.uint8, device=dev)
+            self.recv_scales = torch.empty((self.rows, H // 32), dtype=torch.uint8, device=dev)
+        else:
+            self.recv = torch.empty((self.rows, H), dtype=torch.uint8 if fp8 else torch.bfloat16, device=dev)
+            self.recv_scales = torch.empty((self.rows, H // 128), dtype=torch.float32, device=dev) if fp8 else None
         self.recv_w = torch.empty(self.rows, dtype=torch.float32, device=dev)
         self.out = torch.empty((S, H), dtype=torch.bfloat16, device=dev)
         self._d = self.desc.c()
@@ -502,6 +905,12 @@ class Buffer:
     def dispatch_call(self, hidden, topk_idx=None, topk_w=None, stream=None, check=True):
         if check:
             self._inputs(hidden, topk_idx, topk_w)
+        if self.mx4:
+            rc = _lib.moe_dispatch_mx4(self._dp, self._bp, _ptr(hidden), self.H, _ptr(topk_w), self._recv, self._scales,
+                                       self._recv_w if topk_w is not None else None, _stream(stream, self.device))
+            if rc != MOE_OK:
+                raise MoeError(rc, "moe_dispatch_mx4")
+            return
         rc = _lib.moe_dispatch(self._dp, self._bp, _ptr(hidden), self.H, _ptr(topk_idx), _ptr(topk_w),
                                1 if self.fp8 else 0, self._recv, self._scales,
                                self._recv_w if topk_w is not None else None, _stream(stream, self.device))
@@ -510,10 +919,10 @@ class Buffer:
 
     def layout_dispatch_call(self, hidden, topk_idx, topk_w=None, stream=None, check=True):
         """moe_layout_dispatch: one launch for decode-sized batches (with a
-        balanced layout: the balanced layout, then moe_dispatch)."""
+        balanced layout or MXFP4 rows: the layout, then the dispatch)."""
         if check:
             self._inputs(hidden, topk_idx, topk_w)
-        if self.balance is not None:
+        if self.balance is not None or self.mx4:
             self.layout_call(topk_idx, stream, check=False)
             self.dispatch_call(hidden, topk_idx, topk_w, stream, check=False)
             return
@@ -534,7 +943,10 @@ class Buffer:
             raise MoeError(rc, "moe_combine")
 
     def zero_padding_call(self, stream=None):
-        """moe_zero_padding on this buffer's receive rows (after a dispatch)."""
+        """moe_zero_padding on this buffer's receive rows (after a dispatch; not
+        for MXFP4 rows, whose consumers skip padding)."""
+        if self.mx4:
+            raise MoeError(MOE_ERR_SHAPE, "moe_zero_padding")
         rc = _lib.moe_zero_padding(self._dp, self._bp, self.H, 1 if self.fp8 else 0, self._recv, self._scales,
                                    _stream(stream, self.device))
         if rc != MOE_OK:
@@ -549,3 +961,14 @@ class Buffer:
         """Route-weighted gather back to token order.  Returns out [S,H] bf16."""
         self.combine_call(expert_out, w, shared_out, stream)
         return self.out
+
+    def expert_gemm(self, w, w_scales, act: int = MOE_ACT_NONE, x=None, x_scales=None, out=None, stream=None):
+        """moe_expert_gemm_mx4 on the rows of the last dispatch, or on x and
+        x_scales (MXFP4 rows in the same order, such as the previous product's
+        result through moe_quantize_mx4).  Returns [rows,N] bf16."""
+        if x is None:
+            if not self.mx4:
+                raise MoeError(MOE_ERR_SHAPE, "Buffer.expert_gemm: the receive rows are not MXFP4")
+            x, x_scales = self.recv, self.recv_scales
+        return moe_expert_gemm_mx4(self.desc, self.layout, x, x_scales, w, w_scales, act, out, self.balance,
+                                   self.slots or 0, stream)

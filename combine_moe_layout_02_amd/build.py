@@ -20,7 +20,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmoe_ep.so")
-SOURCES = ["api.hip", "layout.hip", "dispatch.hip", "combine.hip", "fused.hip", "balance.hip", "padding.hip"]
+SOURCES = ["api.hip", "layout.hip", "dispatch.hip", "combine.hip", "fused.hip", "balance.hip", "padding.hip", "router.hip",
+           "mx4.hip", "expert_gemm.hip"]
 CEIL_LIB = os.path.join(HERE, "libmoe_ceilings.so")
 CEIL_SOURCES = ["ceilings.hip"]
 ARCH = "gfx950"

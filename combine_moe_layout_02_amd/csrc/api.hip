@@ -4,11 +4,15 @@
 #include <hip/hip_ext.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <atomic>
 #include <vector>
 
+#include "expert_gemm.h"
 #include "moe_ep.h"
 #include "moe_kernels.h"
+#include "mx4.h"
+#include "router.h"
 
 namespace moe {
 hipError_t launch_zero_padding(const int32_t *src, int rows, int row_bytes, void *recv, float *scales, int nsc,
@@ -347,6 +351,209 @@ moe_status moe_stream_create_cu_limited(int32_t num_cus, void **stream_out) {
 moe_status moe_stream_destroy(void *stream) {
     if (stream == nullptr) return MOE_ERR_NULL;
     return hipStreamDestroy(static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+}  // extern "C"
+
+namespace {
+
+bool router_desc_ok(const moe_router_desc *d, bool picks) {
+    if (d->S < 0 || d->E < 1 || d->E > moe::kMaxE || d->K < 1 || d->K > moe::kMaxK) return false;
+    if (picks && d->K > d->E) return false;
+    if (d->n_groups < 1 || d->n_groups > 64 || d->E % d->n_groups != 0) return false;
+    if (d->topk_groups < 1 || d->topk_groups > d->n_groups) return false;
+    if (picks && d->K > d->E / d->n_groups * d->topk_groups) return false;
+    if (d->seq_len < 0 || (d->seq_len > 0 && d->S % d->seq_len != 0)) return false;
+    if (static_cast<int64_t>(d->S) * d->K >= (int64_t(1) << 31)) return false;
+    return true;
+}
+
+int router_sequences(const moe_router_desc *d) { return d->seq_len > 0 ? d->S / d->seq_len : 1; }
+
+moe::RouterArgs router_args(const moe_router_desc *d, const void *logits, int32_t logits_type, const uint8_t *mask) {
+    moe::RouterArgs a{};
+    a.logits = logits;
+    a.bf16 = logits_type == MOE_BF16;
+    a.mask = mask;
+    a.S = d->S;
+    a.E = d->E;
+    a.K = d->K;
+    a.n_groups = d->n_groups;
+    a.topk_groups = d->topk_groups;
+    a.renorm = d->renorm != 0;
+    a.seq = d->seq_len > 0 ? d->seq_len : d->S;
+    a.G = router_sequences(d);
+    a.alpha = d->alpha;
+    return a;
+}
+
+bool logits_type_ok(int32_t t) { return t == MOE_F32 || t == MOE_BF16; }
+
+// moe_router (given_idx null) and moe_balance_loss.
+moe_status router_forward(const moe_router_desc *desc, const void *logits, int32_t logits_type,
+                          const int32_t *given_idx, const uint8_t *token_mask, const moe_router_bufs *out, bool given,
+                          void *workspace, size_t workspace_bytes, void *stream) {
+    if (desc == nullptr || out == nullptr) return MOE_ERR_NULL;
+    if (!router_desc_ok(desc, !given) || !logits_type_ok(logits_type)) return MOE_ERR_SHAPE;
+    const bool loss = out->balance_loss != nullptr;
+    const bool cells = router_sequences(desc) > 0;      // no sequence: no counts and no coefficients
+    if (loss && cells && (out->expert_count == nullptr || out->balance_coef == nullptr)) return MOE_ERR_NULL;
+    if (!loss && (given || out->expert_count != nullptr || out->balance_coef != nullptr)) return MOE_ERR_NULL;
+    if (desc->S > 0 && logits == nullptr) return MOE_ERR_NULL;
+    if (desc->S > 0 && (given ? given_idx == nullptr : (out->topk_idx == nullptr || out->topk_w == nullptr)))
+        return MOE_ERR_NULL;
+    if (!aligned(logits, logits_type == MOE_BF16 ? 2 : 4) || !aligned(given_idx, 4) || !aligned(out->expert_count, 4) ||
+        !aligned(out->balance_coef, 4) || !aligned(out->balance_loss, 4))
+        return MOE_ERR_ALIGN;
+    if (!given && (!aligned(out->topk_idx, 4) || !aligned(out->topk_w, 4))) return MOE_ERR_ALIGN;
+    moe::RouterArgs a = router_args(desc, logits, logits_type, token_mask);
+    a.given_idx = given ? given_idx : nullptr;
+    a.given = given;
+    a.idx = out->topk_idx;
+    a.w = out->topk_w;
+    if (loss) {
+        const size_t need = moe::router_workspace_bytes(a);
+        if (workspace == nullptr || workspace_bytes < need) return MOE_ERR_WORKSPACE;
+        if (!aligned(workspace, 16)) return MOE_ERR_ALIGN;
+        a.count = out->expert_count;
+        a.coef = out->balance_coef;
+        a.loss = out->balance_loss;
+    } else if (desc->S == 0) {
+        return MOE_OK;
+    }
+    return moe::launch_router(a, workspace, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+// Rows an MXFP4 conversion's launch can number: one workgroup per 8192 channels.
+bool mx4_rows_ok(int64_t rows, int32_t H) {
+    return H >= 128 && H % 128 == 0 && rows >= 0 && rows <= (int64_t(INT32_MAX) * 8192) / H;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_router_workspace_bytes(const moe_router_desc *desc) {
+    if (desc == nullptr || !router_desc_ok(desc, false)) return 0;
+    return moe::router_workspace_bytes(router_args(desc, nullptr, MOE_F32, nullptr));
+}
+
+moe_status moe_router(const moe_router_desc *desc, const void *logits, int32_t logits_type, const uint8_t *token_mask,
+                      const moe_router_bufs *out, void *workspace, size_t workspace_bytes, void *stream) {
+    return router_forward(desc, logits, logits_type, nullptr, token_mask, out, false, workspace, workspace_bytes, stream);
+}
+
+moe_status moe_balance_loss(const moe_router_desc *desc, const void *logits, int32_t logits_type,
+                            const int32_t *topk_idx, const uint8_t *token_mask, const moe_router_bufs *out,
+                            void *workspace, size_t workspace_bytes, void *stream) {
+    return router_forward(desc, logits, logits_type, topk_idx, token_mask, out, true, workspace, workspace_bytes, stream);
+}
+
+moe_status moe_router_backward(const moe_router_desc *desc, const void *logits, int32_t logits_type,
+                               const uint8_t *token_mask, const int32_t *topk_idx, const float *topk_w,
+                               const float *balance_coef, const float *d_topk_w, const float *d_loss, void *d_logits,
+                               void *stream) {
+    if (desc == nullptr) return MOE_ERR_NULL;
+    if (!router_desc_ok(desc, d_topk_w != nullptr) || !logits_type_ok(logits_type)) return MOE_ERR_SHAPE;
+    if (d_topk_w == nullptr && d_loss == nullptr) return MOE_ERR_NULL;
+    if (desc->S == 0) return MOE_OK;
+    if (logits == nullptr || d_logits == nullptr) return MOE_ERR_NULL;
+    if (d_loss != nullptr && balance_coef == nullptr) return MOE_ERR_NULL;
+    if (d_topk_w != nullptr && (topk_idx == nullptr || topk_w == nullptr)) return MOE_ERR_NULL;
+    const uintptr_t size = logits_type == MOE_BF16 ? 2 : 4;
+    if (!aligned(logits, size) || !aligned(d_logits, size) || !aligned(topk_idx, 4) || !aligned(topk_w, 4) ||
+        !aligned(balance_coef, 4) || !aligned(d_topk_w, 4) || !aligned(d_loss, 4))
+        return MOE_ERR_ALIGN;
+    moe::RouterArgs a = router_args(desc, logits, logits_type, token_mask);
+    a.picked = topk_idx;
+    a.picked_w = topk_w;
+    a.saved_coef = d_loss != nullptr ? balance_coef : nullptr;
+    a.d_w = d_topk_w;
+    a.d_loss = d_loss;
+    a.d_logits = d_logits;
+    return moe::launch_router_backward(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+moe_status moe_quantize_mx4(const void *x, int64_t rows, int32_t H, const int32_t *src, void *codes, uint8_t *scales,
+                            void *stream) {
+    if (!mx4_rows_ok(rows, H)) return MOE_ERR_SHAPE;
+    if (rows == 0) return MOE_OK;
+    if (x == nullptr || codes == nullptr || scales == nullptr) return MOE_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(src, 4)) return MOE_ERR_ALIGN;
+    const moe::Mx4Args a{x, nullptr, rows, H, src, codes, scales};
+    return moe::launch_quantize_mx4(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+moe_status moe_dequantize_mx4(const void *codes, const uint8_t *scales, int64_t rows, int32_t H, const int32_t *src,
+                              void *out, void *stream) {
+    if (!mx4_rows_ok(rows, H)) return MOE_ERR_SHAPE;
+    if (rows == 0) return MOE_OK;
+    if (codes == nullptr || scales == nullptr || out == nullptr) return MOE_ERR_NULL;
+    if (!aligned(codes, 16) || !aligned(out, 16) || !aligned(src, 4)) return MOE_ERR_ALIGN;
+    const moe::Mx4Args a{codes, scales, rows, H, src, out, nullptr};
+    return moe::launch_dequantize_mx4(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+moe_status moe_dispatch_mx4(const moe_layout_desc *desc, const moe_layout_bufs *layout, const void *hidden, int32_t H,
+                            const float *topk_w, void *recv, uint8_t *recv_scales, float *recv_w, void *stream) {
+    if (desc == nullptr || layout == nullptr) return MOE_ERR_NULL;
+    if (!desc_ok(desc) || max_rows(desc) < 0 || H < 128 || H % 128 != 0) return MOE_ERR_SHAPE;
+    // one single-wave workgroup per (token, 2048-channel chunk)
+    if (static_cast<int64_t>(desc->S) * ((static_cast<int64_t>(H) + moe::kMx4WaveChannels - 1) / moe::kMx4WaveChannels) >
+        INT32_MAX)
+        return MOE_ERR_SHAPE;
+    if (desc->S == 0) return MOE_OK;
+    if (hidden == nullptr || recv == nullptr || recv_scales == nullptr || layout->pos == nullptr) return MOE_ERR_NULL;
+    if (!aligned(hidden, 16) || !aligned(recv, 16) || !aligned(topk_w, 4) || !aligned(recv_w, 4) ||
+        !aligned(layout->pos, 4))
+        return MOE_ERR_ALIGN;
+    const moe::DispatchMx4Args a{hidden, desc->S, H, desc->K, layout->pos, topk_w, recv, recv_scales, recv_w};
+    return moe::launch_dispatch_mx4(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+moe_status moe_expert_gemm_mx4(const moe_layout_desc *desc, const moe_layout_bufs *layout,
+                               const moe_balance_bufs *bal, int32_t slots_per_rank, const void *x,
+                               const uint8_t *x_scales, int32_t H, const void *w, const uint8_t *w_scales, int32_t N,
+                               int32_t act, void *out, void *stream) {
+    if (desc == nullptr || layout == nullptr) return MOE_ERR_NULL;
+    if (!desc_ok(desc) || max_rows(desc) < 0 || H < 128 || H % 128 != 0 || N < 8 || N % 8 != 0) return MOE_ERR_SHAPE;
+    if (act != MOE_ACT_NONE && act != MOE_ACT_SWIGLU) return MOE_ERR_SHAPE;
+    if (bal == nullptr ? slots_per_rank != 0
+                       : (desc->pad_mode != MOE_PAD_NONE || slots_per_rank < 0 || slots_per_rank > moe::kMaxSlotsPerRank ||
+                          static_cast<int64_t>(desc->R) * slots_per_rank > moe::kMaxBalanceSlots))
+        return MOE_ERR_SHAPE;
+    moe::ExpertGemmArgs a{};
+    a.x = static_cast<const uint8_t *>(x);
+    a.xs = x_scales;
+    a.w = static_cast<const uint8_t *>(w);
+    a.ws = w_scales;
+    a.out = out;
+    a.H = H;
+    a.N = N;
+    a.swiglu = act == MOE_ACT_SWIGLU;
+    a.E = desc->E;
+    a.R = desc->R;
+    a.B = slots_per_rank;
+    a.nseg = desc->E + (bal != nullptr ? desc->R * slots_per_rank : 0);
+    a.entries = static_cast<int64_t>(desc->S) * desc->K;
+    a.max_count = desc->pad_mode == MOE_PAD_CAPACITY ? std::min<int64_t>(a.entries, desc->pad_rows) : a.entries;
+    if (!moe::expert_gemm_grid_ok(a)) return MOE_ERR_SHAPE;
+    if (desc->S == 0) return MOE_OK;
+    if (x == nullptr || x_scales == nullptr || w == nullptr || w_scales == nullptr || out == nullptr) return MOE_ERR_NULL;
+    if (bal != nullptr) {
+        if (bal->seg_offset == nullptr || (slots_per_rank > 0 && bal->slot_expert == nullptr)) return MOE_ERR_NULL;
+        if (!aligned(bal->seg_offset, 4) || !aligned(bal->slot_expert, 4)) return MOE_ERR_ALIGN;
+        a.seg_offset = bal->seg_offset;
+        a.slot_expert = bal->slot_expert;
+    } else {
+        if (layout->tokens_per_expert == nullptr || layout->expert_offset == nullptr) return MOE_ERR_NULL;
+        if (!aligned(layout->tokens_per_expert, 4) || !aligned(layout->expert_offset, 4)) return MOE_ERR_ALIGN;
+        a.count = layout->tokens_per_expert;
+        a.offset = layout->expert_offset;
+    }
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(out, 16) || !aligned(x_scales, 4) || !aligned(w_scales, 4))
+        return MOE_ERR_ALIGN;
+    return moe::launch_expert_gemm_mx4(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
 const char *moe_status_str(int32_t status) {

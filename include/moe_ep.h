@@ -14,6 +14,13 @@
  *                 of each token's K rows (fp32 accumulation), plus an optional
  *                 shared-expert output.
  *
+ * Before the layout, moe_router turns a router's logits into the top-k routing
+ * and its weights, with the load-balance loss and the gradients
+ * (moe_balance_loss, moe_router_backward).  Between dispatch and combine,
+ * moe_dispatch_mx4 carries the rows in microscaled 4-bit floating point
+ * (MXFP4), moe_quantize_mx4 / moe_dequantize_mx4 convert rows, and
+ * moe_expert_gemm_mx4 multiplies every expert's rows with its weights.
+ *
  * Around them: moe_layout_dispatch (layout + dispatch in one launch for
  * decode-sized batches), moe_layout_balanced (every rank receives the same
  * number of rows through redundant-expert slots), moe_zero_padding (optional
@@ -58,8 +65,9 @@
  *     Calls on one stream run in order; calls on different streams that share
  *     output buffers race.
  *   - Limits: 0 <= S, 1 <= K <= 16, 1 <= E <= 1024, R divides E,
- *     S*K and every row count below 2^31; dispatch: S*ceil(H/512) (bf16) or
- *     S*ceil(H/1024) (FP8) below 2^31; combine: S*ceil(H/512) below 2^31.
+ *     S*K and every row count below 2^31; dispatch: S*ceil(H/512) (bf16),
+ *     S*ceil(H/1024) (FP8) or S*ceil(H/2048) (MXFP4) below 2^31; combine:
+ *     S*ceil(H/512) below 2^31.  Offsets inside every array are 64-bit.
  */
 #ifndef MOE_EP_H
 #define MOE_EP_H
@@ -268,6 +276,161 @@ moe_status moe_stream_create_cu_limited(int32_t num_cus, void **stream_out);
  * MOE_ERR_SHAPE.  moe_stream_create_cu_limited(n) is the range [0, n). */
 moe_status moe_stream_create_cu_range(int32_t first_cu, int32_t num_cus, void **stream_out);
 moe_status moe_stream_destroy(void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Router: logits -> top-k routing, load-balance loss, gradients
+ * ------------------------------------------------------------------------- */
+
+/* Types of the router's logits and of their gradient. */
+typedef enum {
+    MOE_F32 = 0,
+    MOE_BF16 = 1
+} moe_dtype;
+
+/* A router's shape and rule (host struct). */
+typedef struct {
+    int32_t S;           /* tokens */
+    int32_t E;           /* experts */
+    int32_t K;           /* experts per token, K <= E */
+    int32_t n_groups;    /* experts form n_groups groups of E/n_groups consecutive ids (1..64, divides E) */
+    int32_t topk_groups; /* a token's picks come from its topk_groups best groups (n_groups: from all) */
+    int32_t renorm;      /* 0: weights are the picks' probabilities; 1: the softmax over the picks alone */
+    int32_t seq_len;     /* tokens per sequence of the balance loss (divides S); 0: the whole batch is one */
+    float alpha;         /* factor of the balance loss */
+} moe_router_desc;
+
+/* What moe_router and moe_balance_loss write (host struct of device pointers).
+ * G = number of sequences: S/seq_len, 1 for seq_len = 0.  expert_count,
+ * balance_coef and balance_loss go together: all three, or none of them (a
+ * serving call of moe_router, which then needs no workspace). */
+typedef struct {
+    int32_t *topk_idx;     /* [S,K] expert of each pick, descending logit; -1 where there is none */
+    float *topk_w;         /* [S,K] route weights; 0 where there is no pick */
+    int32_t *expert_count; /* [G,E] picks of each expert, per sequence */
+    float *balance_coef;   /* [G,E] d balance_loss / d (a token's probability of e) */
+    float *balance_loss;   /* [1] */
+} moe_router_bufs;
+
+/* Device workspace bytes of moe_router (when it writes the loss) and of
+ * moe_balance_loss.  Host only; 0 for an invalid shape. */
+size_t moe_router_workspace_bytes(const moe_router_desc *desc);
+
+/* Router: top-k routing of one batch (the gate in front of the layout), in the
+ * group-limited form of the DeepEP analysis, "normal kernels" set-up (a
+ * token's experts come from its best groups), and optionally the balance loss.
+ *   logits      [S,E] fp32 or bf16 (logits_type); computed in fp32.
+ *   token_mask  [S] bytes or NULL: 0 = the token does not count (padding of the
+ *               batch); what its logits hold is not looked at.
+ * A token counts if its mask lets it and some logit is above -inf (a logit of
+ * -inf marks an expert that cannot be picked).  With p = softmax of a counting
+ * token's logits (0 for other tokens):
+ *   picks    the group score is the group's highest logit; of the topk_groups
+ *            best groups' experts the K highest logits, in descending order;
+ *            ties go to the lower index throughout.  Experts at -inf are never
+ *            picked: entries left over are -1 with weight 0, as are all of a
+ *            token that does not count (moe_layout places no row for them).
+ *   weights  renorm != 0: softmax over the token's picks; else p of the pick.
+ *   loss     per sequence, with n counting tokens and c_e picks of expert e:
+ *            alpha * sum_e (E*c_e/(K*n)) * (sum_t p[t,e] / n), averaged over
+ *            the sequences with n > 0 (0 if there is none).  coef_e =
+ *            alpha*E*c_e/(K*n*n*sequences), 0 in a sequence with n = 0.
+ * A counting token with a NaN or +inf logit is not routed (picks -1, weights
+ * 0), and its probabilities are NaN: so is the loss, and its row of the
+ * gradient.  The results do not depend on the order in which work runs.
+ * No alignment beyond the element types' is needed; workspace 16 bytes. */
+moe_status moe_router(const moe_router_desc *desc, const void *logits, int32_t logits_type, const uint8_t *token_mask,
+                      const moe_router_bufs *out, void *workspace, size_t workspace_bytes, void *stream);
+
+/* The balance loss and per-expert counts of a routing that the caller made:
+ *   topk_idx  [S,K] int32; ids outside [0,E) count for nothing, an expert that
+ *             a token names twice counts twice; picks of tokens that do not
+ *             count are not counted.
+ * Writes expert_count, balance_coef and balance_loss as moe_router does
+ * (out->topk_idx and out->topk_w are not looked at); n_groups, topk_groups and
+ * renorm are checked but change nothing, and K may exceed E.  Gradient:
+ * moe_router_backward without d_topk_w. */
+moe_status moe_balance_loss(const moe_router_desc *desc, const void *logits, int32_t logits_type,
+                            const int32_t *topk_idx, const uint8_t *token_mask, const moe_router_bufs *out,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gradient with respect to the logits, in the logits' type; d_logits is
+ * overwritten (0 for tokens that do not count) and may be the logits' own
+ * buffer.  Two parts, at least one given:
+ *   balance_coef, d_loss ([1] fp32)  d_loss * p * (coef - sum_j coef_j p_j)
+ *   topk_idx, topk_w, d_topk_w ([S,K] fp32)  with inner = sum_k d_k w_k over
+ *     the picks: renorm: w_k*(d_k - inner) at each pick; else
+ *     p_e*(d of the pick of e, if any, - inner) at every expert.
+ * logits, token_mask, topk_* and balance_coef as moe_router had and wrote
+ * them; d_topk_w of an entry without a pick is not looked at. */
+moe_status moe_router_backward(const moe_router_desc *desc, const void *logits, int32_t logits_type,
+                               const uint8_t *token_mask, const int32_t *topk_idx, const float *topk_w,
+                               const float *balance_coef, const float *d_topk_w, const float *d_loss, void *d_logits,
+                               void *stream);
+
+/* ---------------------------------------------------------------------------
+ * MXFP4: rows in microscaled 4-bit floating point, and the experts' products
+ * ------------------------------------------------------------------------- */
+
+/* An MXFP4 row of H channels (H % 128 == 0; OCP microscaling formats, E2M1
+ * elements with E8M0 scales for 32 channels):
+ *   codes   H/2 bytes, channel 2i in the low half of byte i; sign bit, then
+ *           magnitude 0, 0.5, 1, 1.5, 2, 3, 4, 6.
+ *   scales  H/32 bytes, 2^(byte - 127) for 32 consecutive channels, 255 = NaN.
+ * Rounding a bf16 row: per block, byte = floor(log2(amax)) - 2 + 127, at least
+ * 0; code = x / 2^(byte - 127) to the nearest magnitude, ties to the even code,
+ * saturating at 6, x's sign kept.  A block of zeros has byte 0 and codes that
+ * are 0 but for the signs; a block with a NaN or an infinity has byte 255 and
+ * codes 0. */
+
+/* bf16 rows -> MXFP4 rows (an activation between two products, or an expert's
+ * weights, laid out once).
+ *   x       [rows,H] bf16, 16-byte aligned.
+ *   src     [rows] or NULL: with a layout's src only the rows that hold an
+ *           entry (src[r] >= 0) are read and written.
+ *   codes   [rows,H/2], 16-byte aligned; scales [rows,H/32] (any alignment). */
+moe_status moe_quantize_mx4(const void *x, int64_t rows, int32_t H, const int32_t *src, void *codes, uint8_t *scales,
+                            void *stream);
+
+/* MXFP4 rows -> bf16 (exact; a block of scale 255 gives NaN).  Arguments as in
+ * moe_quantize_mx4: rows with src[r] < 0 are neither read nor written. */
+moe_status moe_dequantize_mx4(const void *codes, const uint8_t *scales, int64_t rows, int32_t H, const int32_t *src,
+                              void *out, void *stream);
+
+/* moe_dispatch in MXFP4: row pos[t,k] of the receive buffer gets token t's row
+ * as moe_quantize_mx4 rounds it: a little over half of the FP8 dispatch's
+ * bytes per row.  H % 128 == 0; recv [max_recv,H/2] 16-byte aligned;
+ * recv_scales [max_recv,H/32]; other arguments as in moe_dispatch.  Rows that
+ * no entry maps to are not written. */
+moe_status moe_dispatch_mx4(const moe_layout_desc *desc, const moe_layout_bufs *layout, const void *hidden, int32_t H,
+                            const float *topk_w, void *recv, uint8_t *recv_scales, float *recv_w, void *stream);
+
+/* What moe_expert_gemm_mx4 does with the products before it stores them. */
+typedef enum {
+    MOE_ACT_NONE = 0,
+    MOE_ACT_SWIGLU = 1 /* silu(gate) * up */
+} moe_act;
+
+/* The experts' products: for every row r that holds an entry, of expert e,
+ *   MOE_ACT_NONE    out[r,n] = bf16( sum_h x[r,h] * w[e,n,h] ),  n < N
+ *   MOE_ACT_SWIGLU  out[r,n] = bf16( silu(g) * u ), g = sum_h x[r,h] * w[e,n,h],
+ *                   u = sum_h x[r,h] * w[e,N+n,h];  silu(g) = g / (1 + exp(-g))
+ * with fp32 sums and one rounding at the end (nearest even).
+ *   layout    the layout that the rows were dispatched with.
+ *   x         [max_recv,H/2] codes, x_scales [max_recv,H/32]; H % 128 == 0.
+ *   w         [E,M,H/2] codes, w_scales [E,M,H/32], M = N or (SWIGLU) 2*N.
+ *   N         N % 8 == 0.
+ *   bal, slots_per_rank   NULL and 0 for a layout of moe_layout; for one of
+ *             moe_layout_balanced its bal and slots: a replica slot's rows use
+ *             the weights of the expert in slot_expert.
+ *   out       [max_recv,N] bf16, 16-byte aligned, as are x and w; x_scales and
+ *             w_scales 4 bytes.
+ * Rows that hold no entry are neither read nor written: expert_offset,
+ * tokens_per_expert, seg_offset and slot_expert say which rows hold one.  No
+ * workspace; the grid depends on the shape alone, not on the routing. */
+moe_status moe_expert_gemm_mx4(const moe_layout_desc *desc, const moe_layout_bufs *layout,
+                               const moe_balance_bufs *bal, int32_t slots_per_rank, const void *x,
+                               const uint8_t *x_scales, int32_t H, const void *w, const uint8_t *w_scales, int32_t N,
+                               int32_t act, void *out, void *stream);
 
 /* Static string naming a moe_status value. */
 const char *moe_status_str(int32_t status);
