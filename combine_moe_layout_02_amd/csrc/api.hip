@@ -516,7 +516,9 @@ moe_status moe_expert_gemm_mx4(const moe_layout_desc *desc, const moe_layout_buf
                                const uint8_t *x_scales, int32_t H, const void *w, const uint8_t *w_scales, int32_t N,
                                int32_t act, void *out, void *stream) {
     if (desc == nullptr || layout == nullptr) return MOE_ERR_NULL;
-    if (!desc_ok(desc) || max_rows(desc) < 0 || H < 128 || H % 128 != 0 || N < 8 || N % 8 != 0) return MOE_ERR_SHAPE;
+    if (!desc_ok(desc) || max_rows(desc) < 0 || H < 128 || H % 128 != 0 || N < 8 || N % 8 != 0 ||
+        H > moe::kMaxGemmChannels || N > moe::kMaxGemmChannels)
+        return MOE_ERR_SHAPE;
     if (act != MOE_ACT_NONE && act != MOE_ACT_SWIGLU) return MOE_ERR_SHAPE;
     if (bal == nullptr ? slots_per_rank != 0
                        : (desc->pad_mode != MOE_PAD_NONE || slots_per_rank < 0 || slots_per_rank > moe::kMaxSlotsPerRank ||

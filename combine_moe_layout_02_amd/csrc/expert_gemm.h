@@ -5,6 +5,9 @@
 
 namespace moe {
 
+// H and N: a tile's rows have to lie within 32-bit offsets of each other.
+constexpr int32_t kMaxGemmChannels = 1 << 22;
+
 struct ExpertGemmArgs {
     const uint8_t *x;          // [max_recv,H/2] codes
     const uint8_t *xs;         // [max_recv,H/32] scale bytes

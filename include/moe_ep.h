@@ -418,7 +418,7 @@ typedef enum {
  *   layout    the layout that the rows were dispatched with.
  *   x         [max_recv,H/2] codes, x_scales [max_recv,H/32]; H % 128 == 0.
  *   w         [E,M,H/2] codes, w_scales [E,M,H/32], M = N or (SWIGLU) 2*N.
- *   N         N % 8 == 0.
+ *   N         N % 8 == 0.  H and N are at most 2^22.
  *   bal, slots_per_rank   NULL and 0 for a layout of moe_layout; for one of
  *             moe_layout_balanced its bal and slots: a replica slot's rows use
  *             the weights of the expert in slot_expert.

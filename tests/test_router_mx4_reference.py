@@ -216,7 +216,7 @@ def test_mx4_refusals(moe):
                                      P(out), None)
 
     bal = ctypes.byref(moe.moe_balance_bufs(FAKE, FAKE))
-    for kw in (dict(H=64), dict(H=200), dict(N=0), dict(N=12), dict(act=2), dict(slots=1), dict(bal=bal, slots=65),
+    for kw in (dict(H=64), dict(H=200), dict(N=0), dict(N=12), dict(H=(1 << 22) + 128), dict(N=(1 << 22) + 8), dict(act=2), dict(slots=1), dict(bal=bal, slots=65),
                dict(bal=bal, slots=-1), dict(bal=bal, desc=moe.LayoutDesc(64, 2, 8, 2, moe.MOE_PAD_MULTIPLE, 16).c()),
                dict(desc=moe.LayoutDesc(64, 2, 8, 3).c()),
                dict(desc=moe.LayoutDesc(1 << 26, 16, 8, 2).c(), N=1 << 20)):
