@@ -279,20 +279,20 @@ __device__ __forceinline__ void tile_product(const ExpertGemmArgs &a, const RowT
     for (int m = 0; m < TT; ++m)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[m][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    u32x4 w[kSuper][4], x[kTokLoads], sw, sx;
+    u32x4 w[kSuper][4], x[2][kTokLoads], sw, sx;
     const auto load_w = [&](int k, u32x4 (&to)[4]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) to[i] = load16(i < 2 ? w_gate : w_up, wo[i], k * (kStep / 2));
     };
-    const auto load_x = [&](int k) {
+    const auto load_x = [&](int k, u32x4 (&to)[kTokLoads]) {
 #pragma unroll
         for (int i = 0; i < kTokLoads; ++i)
-            x[i] = load16(xb, xo[i], k * (kStep / 2));
+            to[i] = load16(xb, xo[i], k * (kStep / 2));
     };
-    const auto store_x = [&](int k) {
+    const auto store_x = [&](int k, const u32x4 (&from)[kTokLoads]) {
 #pragma unroll
         for (int i = 0; i < kTokLoads; ++i)
-            lds.tok[k & 1][xslot[i]] = x[i];
+            lds.tok[k & 1][xslot[i]] = from[i];
     };
     // Steps past a row's end read whatever follows it: their scale bytes are 0
     // on both sides, and 2^-254 times any two codes is 0 in fp32.
@@ -317,7 +317,7 @@ __device__ __forceinline__ void tile_product(const ExpertGemmArgs &a, const RowT
 #pragma unroll
         for (int s = 0; s < kSuper; ++s) {
             const int k = kSuper * S + s;
-            if (!last || s < 3) load_x(k + 1);
+            if (!last || s < 2) load_x(k + 2, x[s & 1]);
             if (!last || s < 2) load_w(k + 2, w[(s + 2) & 3]);
             if (s == 0) {
                 if (!last) load_s(S + 1);
@@ -346,7 +346,7 @@ __device__ __forceinline__ void tile_product(const ExpertGemmArgs &a, const RowT
             // them, with their operands, for behind the barriers
             __builtin_amdgcn_sched_barrier(0);
             if (!last || s < 3) {
-                store_x(k + 1);
+                store_x(k + 1, x[(s + 1) & 1]);
                 if (s == 3) store_s(S + 1);
                 lds_barrier();
                 __builtin_amdgcn_sched_barrier(0);
@@ -354,11 +354,12 @@ __device__ __forceinline__ void tile_product(const ExpertGemmArgs &a, const RowT
         }
     };
     load_s(0);
-    load_x(0);
+    load_x(0, x[0]);
     load_w(0, w[0]);
+    load_x(1, x[1]);
     load_w(1, w[1]);
     store_s(0);
-    store_x(0);
+    store_x(0, x[0]);
     lds_barrier();
     for (int S = 0; S < supers - 1; ++S) super(S, std::false_type{});
     super(supers - 1, std::true_type{});
