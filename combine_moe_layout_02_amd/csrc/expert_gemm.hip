@@ -28,13 +28,9 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kFp4 = 4;        // operand format code of the scaled matrix instructions: E2M1
+constexpr int kMaxSegments = kMaxE + kMaxBalanceSlots;
 constexpr int kXcds = 8;       // workgroups go round the XCDs in turn
 constexpr int kStep = 128;     // channels of one matrix instruction
-
-// Rows of segment i.
-__device__ __forceinline__ int seg_rows(const ExpertGemmArgs &a, int i) {
-    return a.seg_offset != nullptr ? a.seg_offset[i + 1] - a.seg_offset[i] : a.count[i];
-}
 
 struct RowTile {
     int row0;      // first row of the receive buffer
@@ -42,6 +38,60 @@ struct RowTile {
     int expert;
     int ntile;     // which tile of the weights' rows
 };
+
+// find_tile with PER segments per lane (nseg <= 64 * PER).
+template <int BM, int PER>
+__device__ __forceinline__ bool find_tile_per(const ExpertGemmArgs &a, int block, int tiles_n, RowTile &t) {
+    const int lane = threadIdx.x & (kWave - 1);
+    // every load at once: the whole search waits for memory one time
+    int first[PER], n[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int i = lane * PER + j;
+        const bool in = i < a.nseg;
+        first[j] = in ? (a.seg_offset != nullptr ? a.seg_offset[i] : a.offset[i]) : 0;
+        n[j] = in ? (a.seg_offset != nullptr ? a.seg_offset[i + 1] : a.count[i]) : 0;
+    }
+    int tiles = 0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        if (a.seg_offset != nullptr) n[j] -= first[j];
+        tiles += (n[j] + BM - 1) / BM;
+    }
+    const int upto = wave_inclusive_scan(tiles);
+    const int total = __builtin_amdgcn_readlane(upto, kWave - 1) * tiles_n;
+    const int run = (total + kXcds - 1) / kXcds, at_run = block / kXcds;
+    const int tile = (block % kXcds) * run + at_run;
+    if (at_run >= run || tile >= total) return false;
+    const int row_tile = tile / tiles_n;
+    const int owner = __builtin_ctzll(__ballot(upto > row_tile));
+    // each lane looks among its own segments; the owner's answer counts
+    int seg = 0, seg_first = 0, seg_n = 0, before = 0, at = upto - tiles;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        if (at <= row_tile) {
+            seg = lane * PER + j;
+            seg_first = first[j];
+            seg_n = n[j];
+            before = at;
+        }
+        at += (n[j] + BM - 1) / BM;
+    }
+    seg = __builtin_amdgcn_readlane(seg, owner);
+    seg_first = __builtin_amdgcn_readlane(seg_first, owner);
+    seg_n = __builtin_amdgcn_readlane(seg_n, owner);
+    before = __builtin_amdgcn_readlane(before, owner);
+    const int seg_tiles = (seg_n + BM - 1) / BM, local = tile - before * tiles_n, m = local % seg_tiles;
+    t.ntile = local / seg_tiles;
+    t.rows = min(BM, seg_n - m * BM);
+    t.row0 = seg_first + m * BM;
+    t.expert = seg;
+    if (a.seg_offset != nullptr) {
+        const int epr = a.E / a.R, r = seg / (epr + a.B), j = seg % (epr + a.B);
+        t.expert = j < epr ? r * epr + j : __builtin_amdgcn_readfirstlane(a.slot_expert[r * a.B + j - epr]);
+    }
+    return true;
+}
 
 // Finds what workgroup `block` computes.  Tiles are numbered segment by
 // segment, inside a segment weight tile by weight tile, inside that row tile
@@ -51,45 +101,9 @@ struct RowTile {
 // false for a workgroup without a tile.
 template <int BM>
 __device__ __forceinline__ bool find_tile(const ExpertGemmArgs &a, int block, int tiles_n, RowTile &t) {
-    const int lane = threadIdx.x & (kWave - 1);
-    const int per = (a.nseg + kWave - 1) / kWave;          // <= 24 segments per lane
-    int tiles = 0;
-    for (int i = lane * per; i < min(a.nseg, (lane + 1) * per); ++i) tiles += (seg_rows(a, i) + BM - 1) / BM;
-    int upto = wave_inclusive_scan(tiles);
-    const int total = __builtin_amdgcn_readlane(upto, kWave - 1) * tiles_n;
-    const int run = (total + kXcds - 1) / kXcds, at_run = block / kXcds;
-    const int tile = (block % kXcds) * run + at_run;
-    if (at_run >= run || tile >= total) return false;
-    const int row_tile = tile / tiles_n;
-    const int owner = __builtin_ctzll(__ballot(upto > row_tile));
-    const int before = __builtin_amdgcn_readlane(upto - tiles, owner);
-    // the owner's segments, one per lane
-    const int seg = owner * per + lane;
-    const int n = lane < per && seg < a.nseg ? seg_rows(a, seg) : 0;
-    tiles = (n + BM - 1) / BM;
-    upto = wave_inclusive_scan(tiles);
-    const int at = __builtin_ctzll(__ballot(before + upto > row_tile));
-    const int seg_tiles = __builtin_amdgcn_readlane(tiles, at);
-    const int local = tile - (before + __builtin_amdgcn_readlane(upto - tiles, at)) * tiles_n;
-    const int m = local % seg_tiles;
-    const int s = owner * per + at;
-    t.ntile = local / seg_tiles;
-    t.rows = min(BM, __builtin_amdgcn_readlane(n, at) - m * BM);
-    if (a.seg_offset != nullptr) {
-        const int epr = a.E / a.R, r = s / (epr + a.B), j = s % (epr + a.B);
-        t.row0 = a.seg_offset[s] + m * BM;
-        t.expert = j < epr ? r * epr + j : a.slot_expert[r * a.B + j - epr];
-    } else {
-        t.row0 = a.offset[s] + m * BM;
-        t.expert = s;
-    }
-    // the same in every lane: into scalar registers, where the buffer
-    // descriptors made from them have to be
-    t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
-    t.rows = __builtin_amdgcn_readfirstlane(t.rows);
-    t.expert = __builtin_amdgcn_readfirstlane(t.expert);
-    t.ntile = __builtin_amdgcn_readfirstlane(t.ntile);
-    return true;
+    if (a.nseg <= kWave) return find_tile_per<BM, 1>(a, block, tiles_n, t);
+    if (a.nseg <= 4 * kWave) return find_tile_per<BM, 4>(a, block, tiles_n, t);
+    return find_tile_per<BM, kMaxSegments / kWave>(a, block, tiles_n, t);
 }
 
 __device__ __forceinline__ i32x8 fp4_operand(u32x4 c) {
@@ -196,10 +210,19 @@ __global__ __launch_bounds__(kStreamWaves * kWave) void k_expert_stream(ExpertGe
 // long segments
 // ---------------------------------------------------------------------------
 
-constexpr int kTileRows = 128;    // token rows of a workgroup
-constexpr int kTileWeights = 256; // weight rows of a workgroup: 64 for each wave
+// 128 token rows by 256 weight rows, four waves of 128 x 64 (128 accumulator
+// registers).  A step (128 channels) is 16 KB of weights and 8 KB of tokens,
+// copied to LDS without passing registers, three steps deep: a step's copies
+// are issued two steps before its products.  Each copy instruction reads whole
+// 64-byte runs (16 rows), which the operands' own order, 16 rows to 16
+// neighbouring lanes, would not: loading weights straight into the operands'
+// registers took 396 us at the prompt case (98304 rows, H = 2048, 2 x 1280
+// weight rows of 64 experts) against 336 us here.  The compiler knows each
+// stage as an object of its own and so waits for that stage's copies alone.
+constexpr int kTileRows = 128;
+constexpr int kTileWeights = 256; // 64 for each wave
 constexpr int kTileWaves = 4;
-constexpr int kSuper = 4;         // steps whose scales are staged together: one byte of a word each
+constexpr int kStageVecs = (kTileRows + kTileWeights) * 4;   // 16-byte vectors: token rows, then weight rows
 
 // A row's scale bytes of steps 4S .. 4S+3 (words d0 .. d3, byte g of each the
 // block of lane group g) as one word per lane group, step s in byte s.
@@ -220,23 +243,50 @@ __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t b, unsigned int o
     return __builtin_amdgcn_raw_buffer_load_b128(b, static_cast<int>(offset), uniform_offset, 0);
 }
 
-struct TileLds {
-    u32x4 tok[2][kTileRows * 4];               // one step of every token row, 16-byte chunks
-    u32x4 scale[2][kTileRows + kTileWeights];  // token rows, then weight rows
-};
+typedef __attribute__((address_space(3))) void lds_void;
+
+// Copies 16 bytes per lane to 1 KiB of LDS from `to` (the same in every lane).
+__device__ __forceinline__ void copy_to_lds(__amdgpu_buffer_rsrc_t b, u32x4 *to, unsigned int offset, int uniform_offset) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(b, reinterpret_cast<lds_void *>(reinterpret_cast<uintptr_t>(to)), 16,
+                                             static_cast<int>(offset), uniform_offset, 0, 0);
+}
+
+// Workgroup barrier that first waits until at most N of the wave's global
+// loads and copies are in flight, and for its LDS writes.  A fence would wait
+// for every copy to LDS; here the ones that N leaves are for later steps.
+template <int N>
+__device__ __forceinline__ void barrier_after_copies() {
+    static_assert(N < 16, "the low bits of the count alone");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0x0070 | N);   // vmcnt(N), lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+}
+
+// Orders the wave's own LDS accesses; nothing else uses the memory between.
+__device__ __forceinline__ void wave_lds_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
 
 // TT 16-row token tiles of the workgroup's rows.
 template <int TT, bool SWIGLU>
-__device__ __forceinline__ void tile_product(const ExpertGemmArgs &a, const RowTile &t, TileLds &lds) {
+__device__ __forceinline__ void tile_product(const ExpertGemmArgs &a, const RowTile &t, u32x4 *stage0, u32x4 *stage1,
+                                             u32x4 *stage2, u32x4 *scale) {
     constexpr int kOutPerWave = SWIGLU ? 32 : 64;
     constexpr int kOutRows = kTileWaves * kOutPerWave;
+    constexpr int kTokCopies = TT >= 4 ? TT / 4 : 1;   // a wave's copies of token rows per step
+    constexpr int kCopies = 4 + kTokCopies;
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int r = lane & 15, g = lane >> 4;
     const unsigned int half = a.H / 2, scales = a.H / kMx4Block;
     const size_t M = SWIGLU ? 2 * static_cast<size_t>(a.N) : a.N;
     const int n0 = t.ntile * kOutRows;
-    const int steps = a.H / kStep, supers = (steps + kSuper - 1) / kSuper;
+    const int steps = a.H / kStep;
     // Weight row j of the workgroup: wave j/64, tile (j/16)%4, row j%16 of it;
     // with SWIGLU tiles 2 and 3 are the up rows of tiles 0 and 1.  Rows past
     // the last one read as zeros.
@@ -251,25 +301,23 @@ __device__ __forceinline__ void tile_product(const ExpertGemmArgs &a, const RowT
     const auto weight_row = [&](int j) -> unsigned int {
         return (j / 64) * kOutPerWave + (SWIGLU ? (j / 16) & 1 : (j / 16) & 3) * 16 + (j & 15);
     };
-    unsigned int wo[4];
+    // A copy instruction moves 16 rows: lane l fills vector l of the 64, row
+    // l/4.  Chunk c (32 channels) of row q lies at 4q + (c ^ (q/2 % 4)), so that
+    // eight rows' chunk c are in eight different groups of banks.
+    const int q16 = lane / 4;
+    const unsigned int chunk = ((lane & 3) ^ ((q16 >> 1) & 3)) * 16;
+    unsigned int wo[4], xo[kTokCopies];
+    int xat[kTokCopies];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) wo[i] = weight_row(wave * 64 + i * 16 + r) * half + g * 16;
-    // tokens: four lanes carry the 64 bytes of a row's step; chunk c of row q
-    // lies at 4q + (c ^ (q/2 % 4)), so that eight rows' chunk c are in eight
-    // different groups of banks
-    constexpr int kTokLoads = (TT * 64 + 255) / 256;
-    unsigned int xo[kTokLoads];
-    int xslot[kTokLoads];
+    for (int i = 0; i < 4; ++i) wo[i] = weight_row(wave * 64 + i * 16 + q16) * half + chunk;
 #pragma unroll
-    for (int i = 0; i < kTokLoads; ++i) {
-        const int q = ((i * 256 + tid) & (TT * 64 - 1)) / 4, c = tid & 3;
-        xo[i] = q * half + c * 16;
-        xslot[i] = 4 * q + (c ^ ((q >> 1) & 3));
+    for (int i = 0; i < kTokCopies; ++i) {
+        xat[i] = (wave * kTokCopies + i) & (TT - 1);   // two waves copy the same rows where there are fewer tiles than waves
+        xo[i] = (xat[i] * 16 + q16) * half + chunk;
     }
     // scales: a thread stages a weight row (with SWIGLU the first two waves the
-    // gate rows, the others the up rows) and a token row.  Where there are more
-    // threads than rows some stage the same one: branches around the loads
-    // would let the compiler move products out of the steps.
+    // gate rows, the others the up rows) and a token row; where there are more
+    // threads than rows some stage the same one
     const int wrow = SWIGLU ? (tid & 127) / 32 * 64 + (tid >> 7) * 32 + (tid & 31) : tid;
     const unsigned int wso = weight_row(wrow) * scales, xso = (tid & (TT * 16 - 1)) * scales;
     const auto sb = SWIGLU && wave >= 2 ? s_up : s_gate;
@@ -279,129 +327,156 @@ __device__ __forceinline__ void tile_product(const ExpertGemmArgs &a, const RowT
     for (int m = 0; m < TT; ++m)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[m][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    u32x4 w[kSuper][4], x[2][kTokLoads], sw, sx;
-    const auto load_w = [&](int k, u32x4 (&to)[4]) {
+    u32x4 sw, sx;
+    const auto copy_step = [&](int k, u32x4 *stage) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) to[i] = load16(i < 2 ? w_gate : w_up, wo[i], k * (kStep / 2));
-    };
-    const auto load_x = [&](int k, u32x4 (&to)[kTokLoads]) {
+        for (int i = 0; i < 4; ++i)
+            copy_to_lds(i < 2 ? w_gate : w_up, stage + (kTileRows + wave * 64 + i * 16) * 4, wo[i], k * (kStep / 2));
 #pragma unroll
-        for (int i = 0; i < kTokLoads; ++i)
-            to[i] = load16(xb, xo[i], k * (kStep / 2));
+        for (int i = 0; i < kTokCopies; ++i) copy_to_lds(xb, stage + xat[i] * 64, xo[i], k * (kStep / 2));
     };
-    const auto store_x = [&](int k, const u32x4 (&from)[kTokLoads]) {
-#pragma unroll
-        for (int i = 0; i < kTokLoads; ++i)
-            lds.tok[k & 1][xslot[i]] = from[i];
-    };
-    // Steps past a row's end read whatever follows it: their scale bytes are 0
-    // on both sides, and 2^-254 times any two codes is 0 in fp32.
+    // Words past a row's end are another row's or zeros: nothing uses them.
     const auto load_s = [&](int S) {
         sw = load16(sb, wso, S * 16);
         sx = load16(xsb, xso, S * 16);
     };
-    const auto store_s = [&](int S) {
-#pragma unroll
-        for (int i = 1; i < 4; ++i) {
-            const unsigned int keep = 4 * S + i < steps ? ~0u : 0u;
-            sw[i] &= keep;
-            sx[i] &= keep;
-        }
-        lds.scale[S & 1][kTileRows + wrow] = transpose_scales(sw);
-        lds.scale[S & 1][tid & (TT * 16 - 1)] = transpose_scales(sx);
+    const auto store_s = [&]() {
+        scale[kTileRows + wrow] = transpose_scales(sw);
+        scale[tid & (TT * 16 - 1)] = transpose_scales(sx);
     };
-    // One superstep; the last one requests nothing past the row's end.
-    const auto super = [&](int S, auto is_last) {
-        constexpr bool last = decltype(is_last)::value;
-        unsigned int sca[4], scb[TT];
+    unsigned int sca[4], scb[TT];
+    const auto read_s = [&]() {
+        const unsigned int *p = reinterpret_cast<const unsigned int *>(scale);
 #pragma unroll
-        for (int s = 0; s < kSuper; ++s) {
-            const int k = kSuper * S + s;
-            if (!last || s < 2) load_x(k + 2, x[s & 1]);
-            if (!last || s < 2) load_w(k + 2, w[(s + 2) & 3]);
-            if (s == 0) {
-                if (!last) load_s(S + 1);
-                const unsigned int *p = reinterpret_cast<const unsigned int *>(lds.scale[S & 1]);
+        for (int i = 0; i < 4; ++i) sca[i] = p[(kTileRows + wave * 64 + i * 16 + r) * 4 + g];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sca[i] = p[(kTileRows + wave * 64 + i * 16 + r) * 4 + g];
+        for (int m = 0; m < TT; ++m) scb[m] = p[(m * 16 + r) * 4 + g];
+    };
+    // The products of step k, from `stage`.
+    const auto products = [&](int k, const u32x4 *stage) {
+        if ((k & 3) == 0) {
+            read_s();
+        } else {
 #pragma unroll
-                for (int m = 0; m < TT; ++m) scb[m] = p[(m * 16 + r) * 4 + g];
-            }
-            const u32x4 *tok = lds.tok[s & 1];
+            for (int i = 0; i < 4; ++i) sca[i] >>= 8;
 #pragma unroll
-            for (int m = 0; m < TT; ++m) {
-                const u32x4 b = tok[4 * (m * 16 + r) + (g ^ ((r >> 1) & 3))];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const i32x8 av = fp4_operand(w[s][i]), bv = fp4_operand(b);
-                    const int sa = static_cast<int>(sca[i]), sx4 = static_cast<int>(scb[m]);
-                    // the byte of a step is an immediate
-                    acc[m][i] = s == 0 ? __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, acc[m][i], kFp4, kFp4, 0, sa, 0, sx4)
-                              : s == 1 ? __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, acc[m][i], kFp4, kFp4, 1, sa, 1, sx4)
-                              : s == 2 ? __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, acc[m][i], kFp4, kFp4, 2, sa, 2, sx4)
-                                       : __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, acc[m][i], kFp4, kFp4, 3, sa, 3, sx4);
-                }
-            }
-            // a step's products stay in their step: the scheduler would keep
-            // them, with their operands, for behind the barriers
-            __builtin_amdgcn_sched_barrier(0);
-            if (!last || s < 3) {
-                store_x(k + 1, x[(s + 1) & 1]);
-                if (s == 3) store_s(S + 1);
-                lds_barrier();
-                __builtin_amdgcn_sched_barrier(0);
-            }
+            for (int m = 0; m < TT; ++m) scb[m] >>= 8;
         }
+        u32x4 wv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) wv[i] = stage[(kTileRows + wave * 64 + i * 16 + r) * 4 + (g ^ ((r >> 1) & 3))];
+#pragma unroll
+        for (int m = 0; m < TT; ++m) {
+            const u32x4 b = stage[(m * 16 + r) * 4 + (g ^ ((r >> 1) & 3))];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                acc[m][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fp4_operand(wv[i]), fp4_operand(b), acc[m][i], kFp4,
+                                                                            kFp4, 0, static_cast<int>(sca[i]), 0,
+                                                                            static_cast<int>(scb[m]));
+        }
+        // a step's products stay in their step: the compiler would move them,
+        // with their operands, behind the barrier
+#pragma unroll
+        for (int m = 0; m < TT; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(acc[m][i]));
+    };
+    // Scales of the next four steps: asked for after the first of four, when
+    // every wave has read the last ones, and stored in the third.
+    const auto scales_early = [&](int k) {
+        if ((k & 3) == 0 && k + 4 < steps) load_s(k / 4 + 1);
+    };
+    const auto scales_late = [&](int k) {
+        if ((k & 3) == 2 && k + 2 < steps) store_s();
+    };
+    // A step with two more behind it; `next` gets step k+2.
+    const auto step = [&](int k, const u32x4 *stage, u32x4 *next) {
+        copy_step(k + 2, next);
+        products(k, stage);
+        scales_late(k);
+        barrier_after_copies<kCopies>();   // step k+1 has arrived: only step k+2 is in flight
+        scales_early(k);
+    };
+    const auto last_step = [&](int k, const u32x4 *stage, u32x4 *next) {
+        if (k + 2 < steps) copy_step(k + 2, next);
+        products(k, stage);
+        scales_late(k);
+        barrier_after_copies<0>();
+        scales_early(k);
     };
     load_s(0);
-    load_x(0, x[0]);
-    load_w(0, w[0]);
-    load_x(1, x[1]);
-    load_w(1, w[1]);
-    store_s(0);
-    store_x(0, x[0]);
-    lds_barrier();
-    for (int S = 0; S < supers - 1; ++S) super(S, std::false_type{});
-    super(supers - 1, std::true_type{});
-    // the sums stay where the products left them: without this the compiler
-    // moves the last products behind the stores and keeps their operands
-#pragma unroll
-    for (int m = 0; m < TT; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(acc[m][i]));
-    // Lane: token r of tile m, four channels from 4g of tile i.  Stores outside
-    // the tile's rows fall past the buffer's end, those past N are sent there.
-    constexpr int kOut = SWIGLU ? 2 : 4;
+    copy_step(0, stage0);
+    store_s();
+    if (steps > 1) {
+        copy_step(1, stage1);
+        barrier_after_copies<kCopies>();
+    } else {
+        barrier_after_copies<0>();
+    }
+    int k = 0;
+    for (; k + 5 <= steps; k += 3) {
+        step(k, stage0, stage2);
+        step(k + 1, stage1, stage0);
+        step(k + 2, stage2, stage1);
+    }
+    // one to four steps are left
+    last_step(k, stage0, stage2);
+    if (k + 1 < steps) last_step(k + 1, stage1, stage0);
+    if (k + 2 < steps) last_step(k + 2, stage2, stage1);
+    if (k + 3 < steps) last_step(k + 3, stage0, stage2);
+    // A lane holds token r of tile m, four channels from 4g of tile i.  Two
+    // tiles at a time pass through LDS (4 KB of the wave's own) so that a store
+    // instruction writes runs of 64 channels (32 with SWIGLU) of a row.  Rows of
+    // kChunks 16-byte chunks, chunk c of row q at c ^ (q % kChunks) (SWIGLU: of
+    // q/2), against bank conflicts.  Stores outside the tile's rows fall past
+    // the buffer's end, those past N are sent there.
+    constexpr int kOut = SWIGLU ? 2 : 4, kChunks = 2 * kOut;
     const unsigned int row_bytes = static_cast<unsigned int>(a.N) * 2u;
     const __amdgpu_buffer_rsrc_t ob = __builtin_amdgcn_make_buffer_rsrc(
         static_cast<char *>(a.out) + static_cast<size_t>(t.row0) * row_bytes, 0, static_cast<int>(t.rows * row_bytes),
         kBufferRsrcWord3);
+    u32x4 *const mine = stage0 + wave * 256;
 #pragma unroll
-    for (int m = 0; m < TT; ++m)
+    for (int m0 = 0; m0 < TT; m0 += 2) {
 #pragma unroll
-        for (int i = 0; i < kOut; ++i) {
-            f32x4 v = acc[m][i];
-            if constexpr (SWIGLU) {
+        for (int m = m0; m < m0 + 2; ++m) {
+            const int q = (m - m0) * 16 + r, turn = SWIGLU ? (q >> 1) & 3 : q & 7;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) v[c] = silu(v[c]) * acc[m][i + 2][c];
+            for (int i = 0; i < kOut; ++i) {
+                f32x4 v = acc[m][i];
+                if constexpr (SWIGLU) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) v[c] = silu(v[c]) * acc[m][i + 2][c];
+                }
+                reinterpret_cast<u32x2 *>(mine)[(q * kChunks + ((2 * i + (g >> 1)) ^ turn)) * 2 + (g & 1)] = pack_bf16x4(v);
             }
-            const int n = n0 + wave * kOutPerWave + i * 16 + 4 * g;
-            const unsigned int at = n < a.N ? (m * 16 + r) * row_bytes + 2u * n : ~0u - 7u;
-            __builtin_amdgcn_raw_buffer_store_b64(pack_bf16x4(v), ob, static_cast<int>(at), 0, 0);
         }
+        wave_lds_fence();
+        constexpr int kRowsPerStore = kWave / kChunks;
+#pragma unroll
+        for (int j = 0; j < 32 / kRowsPerStore; ++j) {
+            const int q = j * kRowsPerStore + lane / kChunks, c = lane % kChunks;
+            const u32x4 v = mine[q * kChunks + (c ^ (SWIGLU ? (q >> 1) & 3 : q & 7))];
+            const int n = n0 + wave * kOutPerWave + c * 8;
+            const unsigned int at = n < a.N ? (m0 * 16 + q) * row_bytes + 2u * n : ~0u - 15u;
+            __builtin_amdgcn_raw_buffer_store_b128(v, ob, static_cast<int>(at), 0, 0);
+        }
+        wave_lds_fence();
+    }
 }
 
 template <bool SWIGLU>
 __global__ __launch_bounds__(kTileWaves * kWave, 2) void k_expert_tile(ExpertGemmArgs a, int tiles_n) {
-    __shared__ TileLds lds;
+    __shared__ u32x4 stage0[kStageVecs], stage1[kStageVecs], stage2[kStageVecs];
+    __shared__ u32x4 scale[kTileRows + kTileWeights];
     RowTile t;
     if (!find_tile<kTileRows>(a, blockIdx.x, tiles_n, t)) return;   // the same for every wave
     if (t.rows > 64)
-        tile_product<8, SWIGLU>(a, t, lds);
+        tile_product<8, SWIGLU>(a, t, stage0, stage1, stage2, scale);
     else if (t.rows > 32)
-        tile_product<4, SWIGLU>(a, t, lds);
+        tile_product<4, SWIGLU>(a, t, stage0, stage1, stage2, scale);
     else
-        tile_product<2, SWIGLU>(a, t, lds);
+        tile_product<2, SWIGLU>(a, t, stage0, stage1, stage2, scale);
 }
 
 // Most row tiles of BM rows that any routing of this shape can have.
