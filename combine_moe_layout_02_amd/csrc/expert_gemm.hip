@@ -210,19 +210,31 @@ __global__ __launch_bounds__(kStreamWaves * kWave) void k_expert_stream(ExpertGe
 // long segments
 // ---------------------------------------------------------------------------
 
-// 128 token rows by 256 weight rows, four waves of 128 x 64 (128 accumulator
-// registers).  A step (128 channels) is 16 KB of weights and 8 KB of tokens,
-// copied to LDS without passing registers, three steps deep: a step's copies
-// are issued two steps before its products.  Each copy instruction reads whole
-// 64-byte runs (16 rows), which the operands' own order, 16 rows to 16
-// neighbouring lanes, would not: loading weights straight into the operands'
-// registers took 396 us at the prompt case (98304 rows, H = 2048, 2 x 1280
-// weight rows of 64 experts) against 336 us here.  The compiler knows each
-// stage as an object of its own and so waits for that stage's copies alone.
-constexpr int kTileRows = 128;
-constexpr int kTileWeights = 256; // 64 for each wave
-constexpr int kTileWaves = 4;
-constexpr int kStageVecs = (kTileRows + kTileWeights) * 4;   // 16-byte vectors: token rows, then weight rows
+// A tile is up to 256 token rows by 256 weight rows.  One workgroup of eight
+// waves per CU takes tile after tile: above 128 rows each wave multiplies 128
+// token rows by 64 weight rows (128 accumulator registers), otherwise all (up to
+// 128) by 32.
+//
+// A stage (256 channels, two steps) of both operands, up to 64 KB, is copied
+// to LDS without passing registers while the stage before it is multiplied,
+// across tiles too: the next tile's first stage is on its way during a tile's
+// last products and its stores, so neither the search for a tile nor the first
+// loads' latency is waited for more than once.  A copy instruction reads 8 whole
+// 128-byte lines; the operands' own order, 16 rows to 16 neighbouring lanes,
+// would read 64 pieces of 16 bytes.  The two stage buffers are objects of their
+// own, so that the compiler, which waits for copies into what it reads, knows
+// that the other buffer's copies may stay in flight.
+//
+// Measured at the prompt case (98304 rows, 64 experts, H = 2048, 2 x 1280
+// weight rows, SwiGLU): weights straight to registers 396 us; 128 x 256 tiles
+// of four waves, two workgroups per CU, one step per stage, three stages deep
+// 336 us; this PROMPT_US.
+constexpr int kTileRows = 256;
+constexpr int kTileWeights = 256;
+constexpr int kTileWaves = 8;
+constexpr int kTileThreads = kTileWaves * kWave;
+constexpr int kCus = 256;                    // workgroups that run at once
+constexpr int kStageVecs = (kTileRows + kTileWeights) * 8;   // 16-byte vectors: 128 bytes of every token row, then weight row
 
 // A row's scale bytes of steps 4S .. 4S+3 (words d0 .. d3, byte g of each the
 // block of lane group g) as one word per lane group, step s in byte s.
@@ -233,14 +245,12 @@ __device__ __forceinline__ u32x4 transpose_scales(u32x4 d) {
                  __builtin_amdgcn_perm(b1, a1, 0x05040100u), __builtin_amdgcn_perm(b1, a1, 0x07060302u)};
 }
 
-// A raw buffer over `bytes` bytes: loads take a uniform base and a 32-bit
-// offset per lane, and read zeros past the end.
+// A raw buffer over `bytes` bytes: loads take a 32-bit offset per lane and read
+// zeros, stores write nothing, where it lies past the end.
 constexpr int kBufferRsrcWord3 = 0x00020000;
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const uint8_t *base, unsigned int bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(base), 0, static_cast<int>(bytes), kBufferRsrcWord3);
-}
-__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t b, unsigned int offset, int uniform_offset) {
-    return __builtin_amdgcn_raw_buffer_load_b128(b, static_cast<int>(offset), uniform_offset, 0);
+constexpr unsigned int kPastEnd = ~0u - 15u;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, unsigned int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, static_cast<int>(bytes), kBufferRsrcWord3);
 }
 
 typedef __attribute__((address_space(3))) void lds_void;
@@ -252,14 +262,14 @@ __device__ __forceinline__ void copy_to_lds(__amdgpu_buffer_rsrc_t b, u32x4 *to,
 }
 
 // Workgroup barrier that first waits until at most N of the wave's global
-// loads and copies are in flight, and for its LDS writes.  A fence would wait
-// for every copy to LDS; here the ones that N leaves are for later steps.
+// loads, copies and stores are in flight (63: for none of them), and for its
+// LDS accesses.  A fence would wait for every copy to LDS.
 template <int N>
-__device__ __forceinline__ void barrier_after_copies() {
-    static_assert(N < 16, "the low bits of the count alone");
+__device__ __forceinline__ void barrier_after() {
+    static_assert(N < 64, "the count's six bits");
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(0x0070 | N);   // vmcnt(N), lgkmcnt(0)
+    __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | (N >> 4 << 14));   // vmcnt(N), lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("" ::: "memory");
@@ -272,193 +282,243 @@ __device__ __forceinline__ void wave_lds_fence() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
 }
 
-// TT 16-row token tiles of the workgroup's rows.
-template <int TT, bool SWIGLU>
-__device__ __forceinline__ void tile_product(const ExpertGemmArgs &a, const RowTile &t, u32x4 *stage0, u32x4 *stage1,
-                                             u32x4 *stage2, u32x4 *scale) {
-    constexpr int kOutPerWave = SWIGLU ? 32 : 64;
-    constexpr int kOutRows = kTileWaves * kOutPerWave;
-    constexpr int kTokCopies = TT >= 4 ? TT / 4 : 1;   // a wave's copies of token rows per step
-    constexpr int kCopies = 4 + kTokCopies;
+// Segments with the number of row tiles before each.
+struct SegTable {
+    int before[kMaxSegments + 1], first[kMaxSegments], rows[kMaxSegments];
+};
+
+struct TileLds {
+    u32x4 *stage0, *stage1, *scale;   // scale: token rows, then weight rows
+    SegTable *segs;
+};
+
+// What a tile's copies need besides the tile: this lane's first offsets into
+// the weights' and the tokens' rows, and its row of scales.
+struct TileCopies {
+    unsigned int wo, xo, so;
+    int slot;               // the scales' place in LDS
+};
+
+// Lane l's vector of a copy: row l/8 of the eight, chunk c at place l%8, where
+// chunk c (32 channels) of row q lies at c ^ (q % 8): eight rows' chunk c are
+// then in eight different groups of banks.
+template <bool SWIGLU>
+__device__ __forceinline__ TileCopies tile_copies(const ExpertGemmArgs &a, const RowTile &t) {
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-    const int r = lane & 15, g = lane >> 4;
     const unsigned int half = a.H / 2, scales = a.H / kMx4Block;
-    const size_t M = SWIGLU ? 2 * static_cast<size_t>(a.N) : a.N;
-    const int n0 = t.ntile * kOutRows;
-    const int steps = a.H / kStep;
-    // Weight row j of the workgroup: wave j/64, tile (j/16)%4, row j%16 of it;
-    // with SWIGLU tiles 2 and 3 are the up rows of tiles 0 and 1.  Rows past
-    // the last one read as zeros.
-    const size_t first = t.expert * M + n0;
-    const unsigned int wrows = min(kOutRows, a.N - n0);
-    const size_t up = SWIGLU ? a.N : 0;
-    const auto w_gate = buffer_of(a.w + first * half, wrows * half), w_up = buffer_of(a.w + (first + up) * half, wrows * half);
-    const auto s_gate = buffer_of(a.ws + first * scales, wrows * scales),
-               s_up = buffer_of(a.ws + (first + up) * scales, wrows * scales);
-    const auto xb = buffer_of(a.x + static_cast<size_t>(t.row0) * half, t.rows * half),
-               xsb = buffer_of(a.xs + static_cast<size_t>(t.row0) * scales, t.rows * scales);
-    const auto weight_row = [&](int j) -> unsigned int {
-        return (j / 64) * kOutPerWave + (SWIGLU ? (j / 16) & 1 : (j / 16) & 3) * 16 + (j & 15);
-    };
-    // A copy instruction moves 16 rows: lane l fills vector l of the 64, row
-    // l/4.  Chunk c (32 channels) of row q lies at 4q + (c ^ (q/2 % 4)), so that
-    // eight rows' chunk c are in eight different groups of banks.
-    const int q16 = lane / 4;
-    const unsigned int chunk = ((lane & 3) ^ ((q16 >> 1) & 3)) * 16;
-    unsigned int wo[4], xo[kTokCopies];
-    int xat[kTokCopies];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) wo[i] = weight_row(wave * 64 + i * 16 + q16) * half + chunk;
-#pragma unroll
-    for (int i = 0; i < kTokCopies; ++i) {
-        xat[i] = (wave * kTokCopies + i) & (TT - 1);   // two waves copy the same rows where there are fewer tiles than waves
-        xo[i] = (xat[i] * 16 + q16) * half + chunk;
+    const bool wide = t.rows > 128;
+    const int q8 = lane / 8;
+    const unsigned int chunk = ((lane & 7) ^ q8) * 16;
+    TileCopies c;
+    // Weight row j of the tile belongs to wave j/64 (wide) or j/32, and is row
+    // j%16 of its 16-row tile; with SWIGLU the second half of a wave's tiles are
+    // the up rows of the first.  This wave copies rows 32*wave .. +31.
+    c.wo = ((SWIGLU ? (wide ? wave / 2 * 32 : wave * 16) : wave * 32) + q8) * half + chunk;
+    c.xo = (wave * 8 + q8) * half + chunk;
+    // scales: a row per thread.  Waves 0 to 3 weight rows (SWIGLU: 0 and 1 gate,
+    // 2 and 3 up), 4 to 7 token rows.
+    if (wave >= 4) {
+        c.so = (tid - 256) * scales;
+        c.slot = tid - 256;
+    } else {
+        const int n = SWIGLU ? tid & 127 : tid, up = SWIGLU && wave >= 2 ? 1 : 0;
+        c.so = n * scales;
+        c.slot = kTileRows + (!SWIGLU ? n : (wide ? n / 32 * 64 + (n & 31) + up * 32 : n / 16 * 32 + (n & 15) + up * 16));
     }
-    // scales: a thread stages a weight row (with SWIGLU the first two waves the
-    // gate rows, the others the up rows) and a token row; where there are more
-    // threads than rows some stage the same one
-    const int wrow = SWIGLU ? (tid & 127) / 32 * 64 + (tid >> 7) * 32 + (tid & 31) : tid;
-    const unsigned int wso = weight_row(wrow) * scales, xso = (tid & (TT * 16 - 1)) * scales;
-    const auto sb = SWIGLU && wave >= 2 ? s_up : s_gate;
+    return c;
+}
 
-    f32x4 acc[TT][4];
+// First weight row of a tile, among all experts', and how many there are.
+template <bool SWIGLU>
+__device__ __forceinline__ size_t first_weight_row(const ExpertGemmArgs &a, const RowTile &t, unsigned int &rows) {
+    constexpr int kOutRows = SWIGLU ? kTileWeights / 2 : kTileWeights;
+    const int n0 = t.ntile * kOutRows;
+    rows = min(kOutRows, a.N - n0);
+    return t.expert * (SWIGLU ? 2 * static_cast<size_t>(a.N) : a.N) + n0;
+}
+
+// Copies channels 256*s .. of the tile into `stage`.  A last stage of 128
+// channels leaves the second half of each row alone (the offset is past the
+// end there).
+template <bool SWIGLU>
+__device__ __forceinline__ void copy_stage(const ExpertGemmArgs &a, const RowTile &t, const TileCopies &c, int s, u32x4 *stage) {
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const unsigned int half = a.H / 2;
+    unsigned int rows;
+    const size_t first = first_weight_row<SWIGLU>(a, t, rows);
+    const bool wide = t.rows > 128;
+    const unsigned int gone = 256 * s + 128 >= a.H && (((lane & 7) ^ (lane / 8)) & 4) ? kPastEnd : 0u;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const bool is_up = SWIGLU && (wide ? (wave & 1) != 0 : i == 1);
+        const auto w = buffer_of(a.w + (first + (is_up ? a.N : 0)) * half, rows * half);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const unsigned int down = (SWIGLU && !wide ? 8 * j : 16 * i + 8 * j) * half;
+            copy_to_lds(w, stage + (kTileRows + wave * 32 + i * 16 + j * 8) * 8, (c.wo + down) | gone, s * 128);
+        }
+    }
+    const auto x = buffer_of(a.x + static_cast<size_t>(t.row0) * half, t.rows * half);
+    const int groups = (t.rows + 15) / 16 * 2;   // token rows, in eights
+#pragma unroll
+    for (int i = 0; i < kTileRows / 8 / kTileWaves; ++i) {
+        const int group = i * kTileWaves + wave;
+        if (group < groups) copy_to_lds(x, stage + group * 64, (c.xo + i * kTileWaves * 8 * half) | gone, s * 128);
+    }
+}
+
+// Scale words 4S .. 4S+3 of this thread's row; those past the row's end are
+// not read.
+template <bool SWIGLU>
+__device__ __forceinline__ u32x4 load_scales(const ExpertGemmArgs &a, const RowTile &t, const TileCopies &c, int S) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const unsigned int scales = a.H / kMx4Block;
+    const int steps = a.H / kStep;
+    unsigned int rows;
+    const size_t first = first_weight_row<SWIGLU>(a, t, rows);
+    const bool tokens = wave >= 4;
+    const uint8_t *base = tokens ? a.xs + static_cast<size_t>(t.row0) * scales
+                                 : a.ws + (first + (SWIGLU && wave >= 2 ? a.N : 0)) * scales;
+    const auto b = buffer_of(base, (tokens ? t.rows : rows) * scales);
+    const unsigned int at = c.so + S * 16;
+    if (4 * S + 4 <= steps) return __builtin_amdgcn_raw_buffer_load_b128(b, static_cast<int>(at), 0, 0);
+    u32x4 d = {0u, 0u, 0u, 0u};
+    d[0] = __builtin_amdgcn_raw_buffer_load_b32(b, static_cast<int>(at), 0, 0);
+    if (4 * S + 1 < steps) d[1] = __builtin_amdgcn_raw_buffer_load_b32(b, static_cast<int>(at + 4), 0, 0);
+    if (4 * S + 2 < steps) d[2] = __builtin_amdgcn_raw_buffer_load_b32(b, static_cast<int>(at + 8), 0, 0);
+    return d;
+}
+
+// Row tile number `row_tile` from the table; every lane calls it.
+__device__ __forceinline__ RowTile tile_at(const ExpertGemmArgs &a, const SegTable &segs, int tile, int tiles_n) {
+    const int lane = threadIdx.x & (kWave - 1);
+    const int row_tile = tile / tiles_n, per = (a.nseg + kWave - 1) / kWave;
+    // the last lane, then the last of its segments, with at most row_tile tiles before it
+    int from = segs.before[min(lane * per, a.nseg)];
+    const int owner = kWave - 1 - __builtin_clzll(__ballot(from <= row_tile && lane * per < a.nseg));
+    const int i = owner * per + lane;
+    from = segs.before[min(i, a.nseg)];
+    const int seg = owner * per + kWave - 1 - __builtin_clzll(__ballot(lane < per && i < a.nseg && from <= row_tile));
+    const int n = __builtin_amdgcn_readfirstlane(segs.rows[seg]), before = __builtin_amdgcn_readfirstlane(segs.before[seg]);
+    const int seg_tiles = (n + kTileRows - 1) / kTileRows, local = tile - before * tiles_n, m = local % seg_tiles;
+    RowTile t;
+    t.ntile = local / seg_tiles;
+    t.rows = min(kTileRows, n - m * kTileRows);
+    t.row0 = __builtin_amdgcn_readfirstlane(segs.first[seg]) + m * kTileRows;
+    t.expert = seg;
+    if (a.seg_offset != nullptr) {
+        const int epr = a.E / a.R, r = seg / (epr + a.B), j = seg % (epr + a.B);
+        t.expert = j < epr ? r * epr + j : __builtin_amdgcn_readfirstlane(a.slot_expert[r * a.B + j - epr]);
+    }
+    return t;
+}
+
+// One tile whose first stage is on its way to stage 0 and whose first scales
+// are on their way to `first_scales`.  next_first() asks for the next tile's,
+// into the same places.  TT token tiles of 16 rows and WT weight tiles per wave.
+template <int TT, int WT, bool SWIGLU, typename NextFirst>
+__device__ __forceinline__ void run_tile(const ExpertGemmArgs &a, const RowTile &t, const TileCopies &copies, const TileLds &lds,
+                                         u32x4 &first_scales, NextFirst &&next_first) {
+    constexpr int kWeightWaves = kTileWeights / (16 * WT);
+    constexpr int kOut = SWIGLU ? WT / 2 : WT;                 // 16-channel tiles of output per wave
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int ww = wave % kWeightWaves, q0 = (wave / kWeightWaves) * 128;   // the wave's weight rows and token rows
+    const int r = lane & 15, g = lane >> 4;
+    const int steps = a.H / kStep, stages = (steps + 1) / 2;
+    f32x4 acc[TT][WT];
 #pragma unroll
     for (int m = 0; m < TT; ++m)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[m][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    u32x4 sw, sx;
-    const auto copy_step = [&](int k, u32x4 *stage) {
+        for (int i = 0; i < WT; ++i) acc[m][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    unsigned int sca[WT], scb[TT];
+    // Step h of a stage, the stage's byte b0 + h of the scales' words.
+    const auto products = [&](const u32x4 *stage, auto byte_, int h) {
+        constexpr int byte = decltype(byte_)::value;
+        const int at = (h * 4 + g) ^ (r & 7);
+        u32x4 wv[WT];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            copy_to_lds(i < 2 ? w_gate : w_up, stage + (kTileRows + wave * 64 + i * 16) * 4, wo[i], k * (kStep / 2));
-#pragma unroll
-        for (int i = 0; i < kTokCopies; ++i) copy_to_lds(xb, stage + xat[i] * 64, xo[i], k * (kStep / 2));
-    };
-    // Words past a row's end are another row's or zeros: nothing uses them.
-    const auto load_s = [&](int S) {
-        sw = load16(sb, wso, S * 16);
-        sx = load16(xsb, xso, S * 16);
-    };
-    const auto store_s = [&]() {
-        scale[kTileRows + wrow] = transpose_scales(sw);
-        scale[tid & (TT * 16 - 1)] = transpose_scales(sx);
-    };
-    unsigned int sca[4], scb[TT];
-    const auto read_s = [&]() {
-        const unsigned int *p = reinterpret_cast<const unsigned int *>(scale);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sca[i] = p[(kTileRows + wave * 64 + i * 16 + r) * 4 + g];
-#pragma unroll
-        for (int m = 0; m < TT; ++m) scb[m] = p[(m * 16 + r) * 4 + g];
-    };
-    // The products of step k, from `stage`.
-    const auto products = [&](int k, const u32x4 *stage) {
-        if ((k & 3) == 0) {
-            read_s();
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sca[i] >>= 8;
-#pragma unroll
-            for (int m = 0; m < TT; ++m) scb[m] >>= 8;
-        }
-        u32x4 wv[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) wv[i] = stage[(kTileRows + wave * 64 + i * 16 + r) * 4 + (g ^ ((r >> 1) & 3))];
+        for (int i = 0; i < WT; ++i) wv[i] = stage[(kTileRows + ww * WT * 16 + i * 16 + r) * 8 + at];
 #pragma unroll
         for (int m = 0; m < TT; ++m) {
-            const u32x4 b = stage[(m * 16 + r) * 4 + (g ^ ((r >> 1) & 3))];
+            const u32x4 b = stage[(q0 + m * 16 + r) * 8 + at];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < WT; ++i)
                 acc[m][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fp4_operand(wv[i]), fp4_operand(b), acc[m][i], kFp4,
-                                                                            kFp4, 0, static_cast<int>(sca[i]), 0,
+                                                                            kFp4, byte, static_cast<int>(sca[i]), byte,
                                                                             static_cast<int>(scb[m]));
         }
         // a step's products stay in their step: the compiler would move them,
-        // with their operands, behind the barrier
+        // with their operands, behind the barriers
 #pragma unroll
         for (int m = 0; m < TT; ++m)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(acc[m][i]));
+            for (int i = 0; i < WT; ++i) asm volatile("" : "+v"(acc[m][i]));
     };
-    // Scales of the next four steps: asked for after the first of four, when
-    // every wave has read the last ones, and stored in the third.
-    const auto scales_early = [&](int k) {
-        if ((k & 3) == 0 && k + 4 < steps) load_s(k / 4 + 1);
-    };
-    const auto scales_late = [&](int k) {
-        if ((k & 3) == 2 && k + 2 < steps) store_s();
-    };
-    // A step with two more behind it; `next` gets step k+2.
-    const auto step = [&](int k, const u32x4 *stage, u32x4 *next) {
-        copy_step(k + 2, next);
-        products(k, stage);
-        scales_late(k);
-        barrier_after_copies<kCopies>();   // step k+1 has arrived: only step k+2 is in flight
-        scales_early(k);
-    };
-    const auto last_step = [&](int k, const u32x4 *stage, u32x4 *next) {
-        if (k + 2 < steps) copy_step(k + 2, next);
-        products(k, stage);
-        scales_late(k);
-        barrier_after_copies<0>();
-        scales_early(k);
-    };
-    load_s(0);
-    copy_step(0, stage0);
-    store_s();
-    if (steps > 1) {
-        copy_step(1, stage1);
-        barrier_after_copies<kCopies>();
-    } else {
-        barrier_after_copies<0>();
+    lds.scale[copies.slot] = transpose_scales(first_scales);
+    barrier_after<0>();                                        // stage 0 has arrived
+    for (int s = 0; s < stages; s += 2) {
+        const bool second = s + 1 < stages, more = s + 2 < stages;
+        if (second) copy_stage<SWIGLU>(a, t, copies, s + 1, lds.stage1);
+        u32x4 next_scales = {0u, 0u, 0u, 0u};
+        if (more) next_scales = load_scales<SWIGLU>(a, t, copies, s / 2 + 1);
+        const unsigned int *p = reinterpret_cast<const unsigned int *>(lds.scale);
+#pragma unroll
+        for (int i = 0; i < WT; ++i) sca[i] = p[(kTileRows + ww * WT * 16 + i * 16 + r) * 4 + g];
+#pragma unroll
+        for (int m = 0; m < TT; ++m) scb[m] = p[(q0 + m * 16 + r) * 4 + g];
+        products(lds.stage0, std::integral_constant<int, 0>{}, 0);
+        if (2 * s + 1 < steps) products(lds.stage0, std::integral_constant<int, 1>{}, 1);
+        barrier_after<0>();                                    // stage s + 1 has arrived, stage s and its scales are free
+        if (more)
+            copy_stage<SWIGLU>(a, t, copies, s + 2, lds.stage0);
+        else
+            next_first();
+        if (second) {
+            products(lds.stage1, std::integral_constant<int, 2>{}, 0);
+            if (2 * s + 3 < steps) products(lds.stage1, std::integral_constant<int, 3>{}, 1);
+        }
+        if (more) {
+            lds.scale[copies.slot] = transpose_scales(next_scales);
+            barrier_after<0>();                                // stage s + 2 has arrived, stage s + 1 is free
+        }
     }
-    int k = 0;
-    for (; k + 5 <= steps; k += 3) {
-        step(k, stage0, stage2);
-        step(k + 1, stage1, stage0);
-        step(k + 2, stage2, stage1);
-    }
-    // one to four steps are left
-    last_step(k, stage0, stage2);
-    if (k + 1 < steps) last_step(k + 1, stage1, stage0);
-    if (k + 2 < steps) last_step(k + 2, stage2, stage1);
-    if (k + 3 < steps) last_step(k + 3, stage0, stage2);
-    // A lane holds token r of tile m, four channels from 4g of tile i.  Two
+    barrier_after<63>();                                       // stage 1 is free; the next tile's first stage may be on its way
+    // A lane holds token r of tile m, four channels from 4g of tile i.  Up to two
     // tiles at a time pass through LDS (4 KB of the wave's own) so that a store
-    // instruction writes runs of 64 channels (32 with SWIGLU) of a row.  Rows of
-    // kChunks 16-byte chunks, chunk c of row q at c ^ (q % kChunks) (SWIGLU: of
-    // q/2), against bank conflicts.  Stores outside the tile's rows fall past
-    // the buffer's end, those past N are sent there.
-    constexpr int kOut = SWIGLU ? 2 : 4, kChunks = 2 * kOut;
+    // instruction writes runs of whole rows.  Rows of kChunks 16-byte chunks,
+    // chunk c of row q at c ^ turn(q), against bank conflicts.  Stores outside
+    // the tile's rows fall past the buffer's end, those past N are sent there.
+    constexpr int kChunks = 2 * kOut, kRowsPerStore = kWave / kChunks;
+    const auto turn = [](int q) { return (q * kChunks / 8) & (kChunks - 1); };
     const unsigned int row_bytes = static_cast<unsigned int>(a.N) * 2u;
-    const __amdgpu_buffer_rsrc_t ob = __builtin_amdgcn_make_buffer_rsrc(
-        static_cast<char *>(a.out) + static_cast<size_t>(t.row0) * row_bytes, 0, static_cast<int>(t.rows * row_bytes),
-        kBufferRsrcWord3);
-    u32x4 *const mine = stage0 + wave * 256;
+    const auto ob = buffer_of(static_cast<char *>(a.out) + static_cast<size_t>(t.row0) * row_bytes, t.rows * row_bytes);
+    const int n0 = (t.ntile * kWeightWaves + ww) * (kOut * 16);
+    u32x4 *const mine = lds.stage1 + wave * 256;
 #pragma unroll
     for (int m0 = 0; m0 < TT; m0 += 2) {
 #pragma unroll
         for (int m = m0; m < m0 + 2; ++m) {
-            const int q = (m - m0) * 16 + r, turn = SWIGLU ? (q >> 1) & 3 : q & 7;
+            const int q = (m - m0) * 16 + r;
 #pragma unroll
             for (int i = 0; i < kOut; ++i) {
                 f32x4 v = acc[m][i];
                 if constexpr (SWIGLU) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) v[c] = silu(v[c]) * acc[m][i + 2][c];
+                    for (int c = 0; c < 4; ++c) v[c] = silu(v[c]) * acc[m][i + kOut][c];
                 }
-                reinterpret_cast<u32x2 *>(mine)[(q * kChunks + ((2 * i + (g >> 1)) ^ turn)) * 2 + (g & 1)] = pack_bf16x4(v);
+                reinterpret_cast<u32x2 *>(mine)[(q * kChunks + ((2 * i + (g >> 1)) ^ turn(q))) * 2 + (g & 1)] = pack_bf16x4(v);
             }
         }
         wave_lds_fence();
-        constexpr int kRowsPerStore = kWave / kChunks;
 #pragma unroll
         for (int j = 0; j < 32 / kRowsPerStore; ++j) {
             const int q = j * kRowsPerStore + lane / kChunks, c = lane % kChunks;
-            const u32x4 v = mine[q * kChunks + (c ^ (SWIGLU ? (q >> 1) & 3 : q & 7))];
-            const int n = n0 + wave * kOutPerWave + c * 8;
-            const unsigned int at = n < a.N ? (m0 * 16 + q) * row_bytes + 2u * n : ~0u - 15u;
+            const u32x4 v = mine[q * kChunks + (c ^ turn(q))];
+            const int n = n0 + c * 8;
+            const unsigned int at = n < a.N ? (q0 + m0 * 16 + q) * row_bytes + 2u * n : kPastEnd;
             __builtin_amdgcn_raw_buffer_store_b128(v, ob, static_cast<int>(at), 0, 0);
         }
         wave_lds_fence();
@@ -466,17 +526,77 @@ __device__ __forceinline__ void tile_product(const ExpertGemmArgs &a, const RowT
 }
 
 template <bool SWIGLU>
-__global__ __launch_bounds__(kTileWaves * kWave, 2) void k_expert_tile(ExpertGemmArgs a, int tiles_n) {
-    __shared__ u32x4 stage0[kStageVecs], stage1[kStageVecs], stage2[kStageVecs];
+__global__ __launch_bounds__(kTileThreads, 2) void k_expert_tile(ExpertGemmArgs a, int tiles_n) {
+    __shared__ u32x4 stage0[kStageVecs], stage1[kStageVecs];
     __shared__ u32x4 scale[kTileRows + kTileWeights];
-    RowTile t;
-    if (!find_tile<kTileRows>(a, blockIdx.x, tiles_n, t)) return;   // the same for every wave
-    if (t.rows > 64)
-        tile_product<8, SWIGLU>(a, t, stage0, stage1, stage2, scale);
-    else if (t.rows > 32)
-        tile_product<4, SWIGLU>(a, t, stage0, stage1, stage2, scale);
-    else
-        tile_product<2, SWIGLU>(a, t, stage0, stage1, stage2, scale);
+    __shared__ SegTable segs;
+    __shared__ int2 s_scan[kTileWaves];
+    const int tid = threadIdx.x;
+    // the table: three segments per thread, every load at once
+    constexpr int kPer = kMaxSegments / kTileThreads;
+    int first[kPer], n[kPer], tiles = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int i = tid * kPer + j;
+        const bool in = i < a.nseg;
+        first[j] = in ? (a.seg_offset != nullptr ? a.seg_offset[i] : a.offset[i]) : 0;
+        n[j] = in ? (a.seg_offset != nullptr ? a.seg_offset[i + 1] : a.count[i]) : 0;
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        if (a.seg_offset != nullptr) n[j] -= first[j];
+        tiles += (n[j] + kTileRows - 1) / kTileRows;
+    }
+    int2 all;
+    int at = block_exclusive_scan2<kTileWaves>(make_int2(tiles, 0), s_scan, all).x;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int i = tid * kPer + j;
+        if (i < a.nseg) {
+            segs.before[i] = at;
+            segs.first[i] = first[j];
+            segs.rows[i] = n[j];
+        }
+        at += (n[j] + kTileRows - 1) / kTileRows;
+    }
+    if (tid == 0) segs.before[a.nseg] = all.x;
+    __syncthreads();
+    // Runs of neighbouring tiles go to the workgroups of one XCD, whose L2 then
+    // serves the tiles' common weights and tokens.
+    const int total = __builtin_amdgcn_readfirstlane(all.x) * tiles_n;
+    const int run = min(kCus / kXcds, (total + kXcds - 1) / kXcds);
+    const int place = static_cast<int>(blockIdx.x) / kXcds;
+    int tile = place < run ? (static_cast<int>(blockIdx.x) % kXcds) * run + place : total;
+    if (tile >= total) return;                                 // the same for every wave
+    const TileLds lds{stage0, stage1, scale, &segs};
+    RowTile t = tile_at(a, segs, tile, tiles_n);
+    TileCopies copies = tile_copies<SWIGLU>(a, t);
+    u32x4 scales = load_scales<SWIGLU>(a, t, copies, 0);
+    copy_stage<SWIGLU>(a, t, copies, 0, stage0);
+    while (true) {
+        const int next = tile + kCus;                          // below INT32_MAX: the grid's check leaves room
+        RowTile nt{};
+        TileCopies nc{};
+        const auto next_first = [&]() {
+            if (next >= total) return;
+            nt = tile_at(a, segs, next, tiles_n);
+            nc = tile_copies<SWIGLU>(a, nt);
+            scales = load_scales<SWIGLU>(a, nt, nc, 0);
+            copy_stage<SWIGLU>(a, nt, nc, 0, stage0);
+        };
+        if (t.rows > 128)
+            run_tile<8, 4, SWIGLU>(a, t, copies, lds, scales, next_first);
+        else if (t.rows > 64)
+            run_tile<8, 2, SWIGLU>(a, t, copies, lds, scales, next_first);
+        else if (t.rows > 32)
+            run_tile<4, 2, SWIGLU>(a, t, copies, lds, scales, next_first);
+        else
+            run_tile<2, 2, SWIGLU>(a, t, copies, lds, scales, next_first);
+        if (next >= total) return;
+        tile = next;
+        t = nt;
+        copies = nc;
+    }
 }
 
 // Most row tiles of BM rows that any routing of this shape can have.
@@ -490,25 +610,28 @@ bool long_segments(const ExpertGemmArgs &a) { return a.entries > 16 * std::min<i
 
 struct Grid {
     int tiles_n;
-    int64_t blocks;   // a multiple of the XCD count
+    int64_t tiles;    // at most; a multiple of the XCD count
+    int64_t blocks;
 };
 Grid grid_of(const ExpertGemmArgs &a) {
     const bool tiles = long_segments(a);
     const int weights = tiles ? kTileWeights : kWTiles * 16, out = a.swiglu ? weights / 2 : weights;
     Grid g;
     g.tiles_n = (a.N + out - 1) / out;
-    g.blocks = (most_tiles(a, tiles ? kTileRows : kStreamRows) * g.tiles_n + kXcds - 1) / kXcds * kXcds;
+    const int64_t all = most_tiles(a, tiles ? kTileRows : kStreamRows) * g.tiles_n;
+    g.tiles = (all + kXcds - 1) / kXcds * kXcds;
+    g.blocks = tiles ? std::min<int64_t>(g.tiles, kCus) : g.tiles;
     return g;
 }
 
 }  // namespace
 
-bool expert_gemm_grid_ok(const ExpertGemmArgs &a) { return grid_of(a).blocks <= INT32_MAX; }
+bool expert_gemm_grid_ok(const ExpertGemmArgs &a) { return grid_of(a).tiles <= INT32_MAX - kCus; }
 
 hipError_t launch_expert_gemm_mx4(const ExpertGemmArgs &a, hipStream_t s) {
     const Grid g = grid_of(a);
     if (g.blocks == 0) return hipSuccess;
-    const dim3 grid(static_cast<unsigned>(g.blocks)), stream_block(kStreamWaves * kWave), tile_block(kTileWaves * kWave);
+    const dim3 grid(static_cast<unsigned>(g.blocks)), stream_block(kStreamWaves * kWave), tile_block(kTileThreads);
     if (long_segments(a)) {
         if (a.swiglu)
             hipLaunchKernelGGL(k_expert_tile<true>, grid, tile_block, 0, s, a, g.tiles_n);
