@@ -8,12 +8,11 @@
 // of one token: one 8-byte store.
 //
 // Which rows belong to which expert is known on the device alone.  The grid
-// holds enough workgroups for any routing; a workgroup finds its tile by
-// scanning the segments' row counts (a wave-wide prefix sum), and one past the
-// last tile returns.
+// holds enough workgroups for any routing; they find their tiles by a prefix sum
+// over the segments' row counts.
 //
-// A workgroup takes 16 rows of one segment and 64 weight rows; its four waves
-// split the channels and join their sums in LDS.
+// Two kernels: k_expert_stream for segments of few rows (the weights' bytes are
+// the work), k_expert_tile for longer ones.
 #include "expert_gemm.h"
 #include "mx4.h"
 
@@ -39,6 +38,20 @@ struct RowTile {
     int ntile;     // which tile of the weights' rows
 };
 
+// Segment i's first row, and its number of rows or (balanced layout) the next
+// segment's first row; past the last segment the last one's, without a branch
+// around the loads.
+__device__ __forceinline__ void load_segment(const ExpertGemmArgs &a, int i, int &first, int &rows_or_end) {
+    const int at = min(i, a.nseg - 1);
+    const int32_t *const f = a.seg_offset != nullptr ? a.seg_offset : a.offset;
+    const int32_t *const n = a.seg_offset != nullptr ? a.seg_offset + 1 : a.count;
+    first = f[at];
+    rows_or_end = n[at];
+}
+__device__ __forceinline__ int segment_rows(const ExpertGemmArgs &a, int i, int first, int rows_or_end) {
+    return i < a.nseg ? rows_or_end - (a.seg_offset != nullptr ? first : 0) : 0;
+}
+
 // find_tile with PER segments per lane (nseg <= 64 * PER).
 template <int BM, int PER>
 __device__ __forceinline__ bool find_tile_per(const ExpertGemmArgs &a, int block, int tiles_n, RowTile &t) {
@@ -46,16 +59,11 @@ __device__ __forceinline__ bool find_tile_per(const ExpertGemmArgs &a, int block
     // every load at once: the whole search waits for memory one time
     int first[PER], n[PER];
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        const int i = lane * PER + j;
-        const bool in = i < a.nseg;
-        first[j] = in ? (a.seg_offset != nullptr ? a.seg_offset[i] : a.offset[i]) : 0;
-        n[j] = in ? (a.seg_offset != nullptr ? a.seg_offset[i + 1] : a.count[i]) : 0;
-    }
+    for (int j = 0; j < PER; ++j) load_segment(a, lane * PER + j, first[j], n[j]);
     int tiles = 0;
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
-        if (a.seg_offset != nullptr) n[j] -= first[j];
+        n[j] = segment_rows(a, lane * PER + j, first[j], n[j]);
         tiles += (n[j] + BM - 1) / BM;
     }
     const int upto = wave_inclusive_scan(tiles);
@@ -122,68 +130,182 @@ __device__ __forceinline__ u32x2 pack_bf16x4(f32x4 v) {
     return __builtin_bit_cast(u32x2, __builtin_convertvector(v, bf16x4));
 }
 
-constexpr int kStreamRows = 16;  // token rows of a workgroup
-constexpr int kStreamWaves = 4;
-constexpr int kWTiles = 4;     // 16-row weight tiles of a workgroup (SWIGLU: half gate, half up)
-
-// U channel steps from step s: every load first, then the products.
-template <int U>
-__device__ __forceinline__ void stream_steps(const uint8_t *const (&wp)[kWTiles], const uint8_t *const (&wsp)[kWTiles],
-                                             const uint8_t *xp, const uint8_t *xsp, int s, int shift,
-                                             f32x4 (&acc)[kWTiles]) {
-    u32x4 w[U][kWTiles], x[U];
-    unsigned int ws[U][kWTiles], xs[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-#pragma unroll
-        for (int i = 0; i < kWTiles; ++i) {
-            w[u][i] = *reinterpret_cast<const u32x4 *>(wp[i] + static_cast<size_t>(s + u) * (kStep / 2));
-            ws[u][i] = *reinterpret_cast<const unsigned int *>(wsp[i] + static_cast<size_t>(s + u) * 4);
-        }
-        x[u] = *reinterpret_cast<const u32x4 *>(xp + static_cast<size_t>(s + u) * (kStep / 2));
-        xs[u] = *reinterpret_cast<const unsigned int *>(xsp + static_cast<size_t>(s + u) * 4);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-#pragma unroll
-        for (int i = 0; i < kWTiles; ++i)
-            acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fp4_operand(w[u][i]), fp4_operand(x[u]), acc[i],
-                                                                     kFp4, kFp4, 0, static_cast<int>(ws[u][i] >> shift),
-                                                                     0, static_cast<int>(xs[u] >> shift));
-    }
+// A raw buffer over `bytes` bytes: loads take a 32-bit offset per lane and read
+// zeros, stores write nothing, where it lies past the end.
+constexpr int kBufferRsrcWord3 = 0x00020000;
+constexpr unsigned int kPastEnd = ~0u - 15u;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, unsigned int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, static_cast<int>(bytes), kBufferRsrcWord3);
 }
 
+typedef __attribute__((address_space(3))) void lds_void;
+
+// Copies 16 bytes per lane to 1 KiB of LDS from `to` (the same in every lane).
+__device__ __forceinline__ void copy_to_lds(__amdgpu_buffer_rsrc_t b, u32x4 *to, unsigned int offset, int uniform_offset) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(b, reinterpret_cast<lds_void *>(reinterpret_cast<uintptr_t>(to)), 16,
+                                             static_cast<int>(offset), uniform_offset, 0, 0);
+}
+
+// Orders the wave's own LDS accesses; nothing else uses the memory between.
+__device__ __forceinline__ void wave_lds_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
+// ---------------------------------------------------------------------------
+// short segments
+// ---------------------------------------------------------------------------
+
+// 16 token rows by 64 weight rows; the four waves split the channels and join
+// their sums in LDS.  The weights' bytes are the work, each read once, so what
+// counts is to keep many of them in flight and to ask for whole lines: a unit
+// (256 channels) of the 64 rows, 8 KB, is copied to the wave's own LDS in
+// instructions of 8 whole 128-byte lines while the unit before it is
+// multiplied, two workgroups of four such waves per CU.  (The operands' own
+// order, straight to registers, asks for 64 pieces of 16 bytes per instruction:
+// DECODE_OLD us at the decode case, 1024 rows of 256 experts, H = 7168, 2 x 1024
+// weight rows, against DECODE_US here.)  The wave's channels' weight scales come
+// in parts of 8 units; tokens and their scales, few and shared by every
+// workgroup of the segment, go straight to registers.
+constexpr int kStreamRows = 16;
+constexpr int kStreamWaves = 4;
+constexpr int kWTiles = 4;         // 16-row weight tiles (SWIGLU: half gate, half up)
+constexpr int kUnitVecs = kWTiles * 16 * 8;
+constexpr int kPartUnits = 8;      // units whose scales are in LDS
+
 template <bool SWIGLU>
-__global__ __launch_bounds__(kStreamWaves * kWave) void k_expert_stream(ExpertGemmArgs a, int tiles_n) {
+__global__ __launch_bounds__(kStreamWaves * kWave, 2) void k_expert_stream(ExpertGemmArgs a, int tiles_n) {
     constexpr int kOutTiles = SWIGLU ? kWTiles / 2 : kWTiles;
-    __shared__ f32x4 part[kStreamWaves][kWTiles][kWave];
+    __shared__ u32x4 unit0[kStreamWaves][kUnitVecs], unit1[kStreamWaves][kUnitVecs];
+    __shared__ unsigned int wscale[kStreamWaves][kWTiles * 16 * 2 * kPartUnits];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     RowTile t;
     if (!find_tile<kStreamRows>(a, blockIdx.x, tiles_n, t)) return;   // the same for every wave
-    const int row0 = t.row0, rows = t.rows, expert = t.expert, n0 = t.ntile * (kOutTiles * 16);
+    t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
+    t.rows = __builtin_amdgcn_readfirstlane(t.rows);
+    t.expert = __builtin_amdgcn_readfirstlane(t.expert);
+    t.ntile = __builtin_amdgcn_readfirstlane(t.ntile);
+    const int n0 = t.ntile * (kOutTiles * 16);
     // lane = 16*g + r: row r of each operand, channels 32*g .. 32*g+31 of a step
     const int r = lane & 15, g = lane >> 4;
-    const size_t half = a.H / 2, scales = a.H / kMx4Block;
-    const size_t M = SWIGLU ? 2 * static_cast<size_t>(a.N) : a.N;
-    const uint8_t *wp[kWTiles], *wsp[kWTiles];
+    const unsigned int half = a.H / 2, scales = a.H / kMx4Block;
+    const unsigned int wrows = min(kOutTiles * 16, a.N - n0);           // past them zeros are read
+    const size_t first = t.expert * (SWIGLU ? 2 * static_cast<size_t>(a.N) : a.N) + n0, up = first + (SWIGLU ? a.N : 0);
+    const auto w_gate = buffer_of(a.w + first * half, wrows * half), w_up = buffer_of(a.w + up * half, wrows * half);
+    const auto s_gate = buffer_of(a.ws + first * scales, wrows * scales), s_up = buffer_of(a.ws + up * scales, wrows * scales);
+    const auto xb = buffer_of(a.x + static_cast<size_t>(t.row0) * half, t.rows * half);
+    const auto xsb = buffer_of(a.xs + static_cast<size_t>(t.row0) * scales, t.rows * scales);
+    const int steps = a.H / kStep, units = (steps + 1) / 2;
+    const int begin = units * wave / kStreamWaves, end = units * (wave + 1) / kStreamWaves;
+    // Copies of 8 weight rows: lane l's vector is row l/8, chunk c at place l%8;
+    // chunk c (32 channels) of row q lies at c ^ (q % 8), so that eight rows'
+    // chunk c are in eight different groups of banks.
+    const int q8 = lane / 8;
+    const unsigned int wo = q8 * half + ((lane & 7) ^ q8) * 16;
+    const auto copy_unit = [&](int u, u32x4 *to) {
+        // a last unit of 128 channels leaves the second half of each row alone
+        const unsigned int gone = 2 * u + 1 >= steps && (((lane & 7) ^ q8) & 4) ? kPastEnd : 0u;
 #pragma unroll
-    for (int i = 0; i < kWTiles; ++i) {
-        const int n = min(n0 + (i % kOutTiles) * 16 + r, a.N - 1);        // rows past N repeat the last one
-        const size_t row = expert * M + n + (i >= kOutTiles ? a.N : 0);
-        wp[i] = a.w + row * half + g * 16;
-        wsp[i] = a.ws + row * scales;
-    }
-    const size_t xrow = row0 + min(r, rows - 1);
-    const uint8_t *xp = a.x + xrow * half + g * 16, *xsp = a.xs + xrow * scales;
+        for (int j = 0; j < kWTiles * 2; ++j) {
+            const int row = 8 * j;                                       // of the 64
+            const bool is_up = row >= kOutTiles * 16;
+            copy_to_lds(is_up ? w_up : w_gate, to + row * 8, (wo + (is_up ? row - kOutTiles * 16 : row) * half) | gone, u * 128);
+        }
+    };
+    // Scale words of 8 units from u0: row 16*i + lane/4, words 4*(lane%4) .. +3;
+    // those past the row's end are not read.  Word d of row q lies at
+    // d ^ (q % 16): 16 rows' word d are in 16 different banks.
+    const auto load_part = [&](int u0) {
+        u32x4 v[kWTiles];
+        const int d0 = 4 * (lane & 3);
+#pragma unroll
+        for (int i = 0; i < kWTiles; ++i) {
+            const bool is_up = i >= kOutTiles;
+            const int q = (is_up ? i - kOutTiles : i) * 16 + lane / 4, word = 2 * u0 + d0;
+            const unsigned int at = q * scales + 4u * word;
+            const auto b = is_up ? s_up : s_gate;
+            v[i] = u32x4{0u, 0u, 0u, 0u};
+            if (word + 4 <= steps) {
+                v[i] = __builtin_amdgcn_raw_buffer_load_b128(b, static_cast<int>(at), 0, 0);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 3; ++j)
+                    if (word + j < steps) v[i][j] = __builtin_amdgcn_raw_buffer_load_b32(b, static_cast<int>(at + 4 * j), 0, 0);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kWTiles; ++i) {
+            const int q = i * 16 + lane / 4;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) wscale[wave][q * 16 + ((d0 + j) ^ (q & 15))] = v[i][j];
+        }
+        wave_lds_fence();
+    };
     f32x4 acc[kWTiles];
 #pragma unroll
     for (int i = 0; i < kWTiles; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    const int steps = a.H / kStep;
-    int s = steps * wave / kStreamWaves;
-    const int end = steps * (wave + 1) / kStreamWaves;
-    for (; s + 4 <= end; s += 4) stream_steps<4>(wp, wsp, xp, xsp, s, 8 * g, acc);
-    for (; s < end; ++s) stream_steps<1>(wp, wsp, xp, xsp, s, 8 * g, acc);
+    struct Tokens {
+        u32x4 x[2];
+        u32x2 s;
+    };
+    // a token row's codes and scale words of a unit; a second step past the
+    // row's end is not read
+    const unsigned int xo = r * half + g * 16, xso = r * scales;
+    const auto load_tokens = [&](int u) {
+        const bool both = 2 * u + 1 < steps;
+        Tokens v;
+        v.x[0] = __builtin_amdgcn_raw_buffer_load_b128(xb, static_cast<int>(xo), u * 128, 0);
+        v.s[0] = __builtin_amdgcn_raw_buffer_load_b32(xsb, static_cast<int>(xso), u * 8, 0);
+        v.x[1] = u32x4{0u, 0u, 0u, 0u};
+        v.s[1] = 0u;
+        if (both) {
+            v.x[1] = __builtin_amdgcn_raw_buffer_load_b128(xb, static_cast<int>(xo), u * 128 + 64, 0);
+            v.s[1] = __builtin_amdgcn_raw_buffer_load_b32(xsb, static_cast<int>(xso), u * 8 + 4, 0);
+        }
+        return v;
+    };
+    const auto products = [&](int u, int u0, const u32x4 *from, const Tokens &tok) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (2 * u + h < steps) {
+#pragma unroll
+                for (int i = 0; i < kWTiles; ++i) {
+                    const int q = i * 16 + r;
+                    const u32x4 w = from[q * 8 + ((h * 4 + g) ^ (r & 7))];
+                    const unsigned int s = wscale[wave][q * 16 + ((2 * (u - u0) + h) ^ r)];
+                    acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fp4_operand(w), fp4_operand(tok.x[h]), acc[i], kFp4, kFp4,
+                                                                             0, static_cast<int>(s >> (8 * g)), 0,
+                                                                             static_cast<int>(tok.s[h] >> (8 * g)));
+                }
+            }
+        }
+        // the unit is read before anything is copied over it
+#pragma unroll
+        for (int i = 0; i < kWTiles; ++i) asm volatile("" : "+v"(acc[i]) : : "memory");
+    };
+    for (int u0 = begin; u0 < end; u0 += kPartUnits) {
+        const int stop = min(end, u0 + kPartUnits);
+        copy_unit(u0, unit0[wave]);
+        if (u0 + 1 < stop) copy_unit(u0 + 1, unit1[wave]);
+        Tokens now = load_tokens(u0);
+        load_part(u0);
+        for (int u = u0; u < stop; u += 2) {
+            Tokens next = now;
+            if (u + 1 < stop) next = load_tokens(u + 1);
+            products(u, u0, unit0[wave], now);
+            if (u + 2 < stop) copy_unit(u + 2, unit0[wave]);
+            if (u + 1 < stop) {
+                if (u + 2 < stop) now = load_tokens(u + 2);
+                products(u + 1, u0, unit1[wave], next);
+                if (u + 3 < stop) copy_unit(u + 3, unit1[wave]);
+            }
+        }
+    }
+    // the sums meet where the weights were
+    __syncthreads();
+    f32x4(*const part)[kWTiles][kWave] = reinterpret_cast<f32x4(*)[kWTiles][kWave]>(&unit0[0][0]);
 #pragma unroll
     for (int i = 0; i < kWTiles; ++i) part[wave][i][lane] = acc[i];
     __syncthreads();
@@ -200,8 +322,8 @@ __global__ __launch_bounds__(kStreamWaves * kWave) void k_expert_stream(ExpertGe
             for (int c = 0; c < 4; ++c) v[c] = silu(v[c]) * u[c];
         }
         const int n = n0 + i * 16 + 4 * g;
-        if (r < rows && n < a.N)
-            *reinterpret_cast<u32x2 *>(static_cast<unsigned short *>(a.out) + static_cast<size_t>(row0 + r) * a.N + n) =
+        if (r < t.rows && n < a.N)
+            *reinterpret_cast<u32x2 *>(static_cast<unsigned short *>(a.out) + static_cast<size_t>(t.row0 + r) * a.N + n) =
                 pack_bf16x4(v);
     }
 }
@@ -228,7 +350,7 @@ __global__ __launch_bounds__(kStreamWaves * kWave) void k_expert_stream(ExpertGe
 // Measured at the prompt case (98304 rows, 64 experts, H = 2048, 2 x 1280
 // weight rows, SwiGLU): weights straight to registers 396 us; 128 x 256 tiles
 // of four waves, two workgroups per CU, one step per stage, three stages deep
-// 336 us; this PROMPT_US.
+// 336 us; this 321 us.
 constexpr int kTileRows = 256;
 constexpr int kTileWeights = 256;
 constexpr int kTileWaves = 8;
@@ -245,22 +367,6 @@ __device__ __forceinline__ u32x4 transpose_scales(u32x4 d) {
                  __builtin_amdgcn_perm(b1, a1, 0x05040100u), __builtin_amdgcn_perm(b1, a1, 0x07060302u)};
 }
 
-// A raw buffer over `bytes` bytes: loads take a 32-bit offset per lane and read
-// zeros, stores write nothing, where it lies past the end.
-constexpr int kBufferRsrcWord3 = 0x00020000;
-constexpr unsigned int kPastEnd = ~0u - 15u;
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, unsigned int bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, static_cast<int>(bytes), kBufferRsrcWord3);
-}
-
-typedef __attribute__((address_space(3))) void lds_void;
-
-// Copies 16 bytes per lane to 1 KiB of LDS from `to` (the same in every lane).
-__device__ __forceinline__ void copy_to_lds(__amdgpu_buffer_rsrc_t b, u32x4 *to, unsigned int offset, int uniform_offset) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(b, reinterpret_cast<lds_void *>(reinterpret_cast<uintptr_t>(to)), 16,
-                                             static_cast<int>(offset), uniform_offset, 0, 0);
-}
-
 // Workgroup barrier that first waits until at most N of the wave's global
 // loads, copies and stores are in flight (63: for none of them), and for its
 // LDS accesses.  A fence would wait for every copy to LDS.
@@ -273,13 +379,6 @@ __device__ __forceinline__ void barrier_after() {
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("" ::: "memory");
-}
-
-// Orders the wave's own LDS accesses; nothing else uses the memory between.
-__device__ __forceinline__ void wave_lds_fence() {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
 }
 
 // Segments with the number of row tiles before each.
@@ -536,15 +635,10 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_expert_tile(ExpertGemmArgs 
     constexpr int kPer = kMaxSegments / kTileThreads;
     int first[kPer], n[kPer], tiles = 0;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        const int i = tid * kPer + j;
-        const bool in = i < a.nseg;
-        first[j] = in ? (a.seg_offset != nullptr ? a.seg_offset[i] : a.offset[i]) : 0;
-        n[j] = in ? (a.seg_offset != nullptr ? a.seg_offset[i + 1] : a.count[i]) : 0;
-    }
+    for (int j = 0; j < kPer; ++j) load_segment(a, tid * kPer + j, first[j], n[j]);
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-        if (a.seg_offset != nullptr) n[j] -= first[j];
+        n[j] = segment_rows(a, tid * kPer + j, first[j], n[j]);
         tiles += (n[j] + kTileRows - 1) / kTileRows;
     }
     int2 all;
