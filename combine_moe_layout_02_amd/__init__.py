@@ -140,6 +140,15 @@ class LayoutDesc:
         return moe_layout_desc(self.S, self.K, self.E, self.R, self.pad_mode, self.pad_rows)
 
 
+def _made_once(desc):
+    """A reference to the descriptor's C struct, which its fields, frozen, cannot outlive."""
+    ref = desc.__dict__.get("_ref")
+    if ref is None:
+        ref = ctypes.byref(desc.c())
+        desc.__dict__["_ref"] = ref
+    return ref
+
+
 @dataclasses.dataclass
 class Layout:
     """Device tensors of one batch's layout (outputs of moe_layout)."""
@@ -183,11 +192,11 @@ def _check(t: Optional[torch.Tensor], name: str, dtype, shape=None, device=None)
         return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if dtype is not None and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+    if dtype is not None and t.dtype is not dtype and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
@@ -452,17 +461,19 @@ def moe_zero_padding(desc: LayoutDesc, layout: Layout, recv: torch.Tensor, recv_
 # Router and balance loss
 # ---------------------------------------------------------------------------
 
+_nothing = contextlib.nullcontext()
+_raw_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _alloc_on(stream):
     """Where a call's own outputs come from: memory of the stream that will
     write them, so that the allocator hands it out again in that stream's order."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _nothing if stream is None else torch.cuda.stream(stream)
 
 
 def _on_device(device):
     """The C calls launch on the current device: make it the tensors' own."""
-    if device.type != "cuda" or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+    return _nothing if device.index == _raw_current_device() else torch.cuda.device(device)
 
 
 @dataclasses.dataclass(frozen=True)
@@ -505,47 +516,50 @@ class Router:
 
 
 def moe_router_workspace_bytes(desc: RouterDesc) -> int:
-    return int(_lib.moe_router_workspace_bytes(ctypes.byref(desc.c())))
+    return int(_lib.moe_router_workspace_bytes(_made_once(desc)))
 
 
 def alloc_router(desc: RouterDesc, device, picks: bool = True, loss: bool = True) -> Router:
     """Device buffers for moe_router's outputs (``picks``: the routing, ``loss``:
     counts, coefficients, the loss and its workspace)."""
-    S, E, K, G = desc.S, desc.E, desc.K, desc.sequences
-    i32, f32 = dict(dtype=torch.int32, device=device), dict(dtype=torch.float32, device=device)
-    r = Router(None, None, None, None, None)
+    empty, i32, f32 = torch.empty, torch.int32, torch.float32
+    idx = w = count = coef = value = ws = None
     if picks:
-        r.topk_idx, r.topk_w = torch.empty((S, K), **i32), torch.empty((S, K), **f32)
+        idx = empty((desc.S, desc.K), dtype=i32, device=device)
+        w = empty((desc.S, desc.K), dtype=f32, device=device)
     if loss:
-        ws = moe_router_workspace_bytes(desc)
-        if ws == 0:
+        need = moe_router_workspace_bytes(desc)
+        if need == 0:
             raise MoeError(MOE_ERR_SHAPE, "alloc_router")
-        r.expert_count, r.balance_coef = torch.empty((G, E), **i32), torch.empty((G, E), **f32)
-        r.balance_loss = torch.empty(1, **f32)
-        r.workspace = torch.empty(ws, dtype=torch.uint8, device=device)
-    return r
+        cells = (desc.sequences, desc.E)
+        count, coef = empty(cells, dtype=i32, device=device), empty(cells, dtype=f32, device=device)
+        value, ws = empty(1, dtype=f32, device=device), empty(need, dtype=torch.uint8, device=device)
+    return Router(idx, w, count, coef, value, ws)
 
 
 def _logits(desc: RouterDesc, logits: torch.Tensor, token_mask) -> int:
     """Checks a router call's inputs; the C type of the logits."""
     _check(logits, "logits", (torch.float32, torch.bfloat16), (desc.S, desc.E))
-    _check(token_mask, "token_mask", (torch.bool, torch.uint8), (desc.S,), logits.device)
-    return MOE_BF16 if logits.dtype == torch.bfloat16 else MOE_F32
+    if token_mask is not None:
+        _check(token_mask, "token_mask", (torch.bool, torch.uint8), (desc.S,), logits.device)
+    return MOE_BF16 if logits.dtype is torch.bfloat16 else MOE_F32
 
 
-def _check_router(desc: RouterDesc, r: Router, picks: bool, loss: bool, device):
-    if picks and (r.topk_idx is None or r.topk_w is None):
+def _check_picks(desc: RouterDesc, r: Router, device):
+    if r.topk_idx is None or r.topk_w is None:
         raise ValueError("router has no buffers for the routing")
-    if picks:
-        _check(r.topk_idx, "topk_idx", torch.int32, (desc.S, desc.K), device)
-        _check(r.topk_w, "topk_w", torch.float32, (desc.S, desc.K), device)
-    if loss:
-        if r.balance_loss is None or r.expert_count is None or r.balance_coef is None:
-            raise ValueError("router has no buffers for the loss")
-        _check(r.expert_count, "expert_count", torch.int32, (desc.sequences, desc.E), device)
-        _check(r.balance_coef, "balance_coef", torch.float32, (desc.sequences, desc.E), device)
-        _check(r.balance_loss, "balance_loss", torch.float32, (1,), device)
-        _check(r.workspace, "workspace", torch.uint8, None, device)
+    _check(r.topk_idx, "topk_idx", torch.int32, (desc.S, desc.K), device)
+    _check(r.topk_w, "topk_w", torch.float32, (desc.S, desc.K), device)
+
+
+def _check_loss(desc: RouterDesc, r: Router, device):
+    if r.balance_loss is None or r.expert_count is None or r.balance_coef is None:
+        raise ValueError("router has no buffers for the loss")
+    cells = (desc.sequences, desc.E)
+    _check(r.expert_count, "expert_count", torch.int32, cells, device)
+    _check(r.balance_coef, "balance_coef", torch.float32, cells, device)
+    _check(r.balance_loss, "balance_loss", torch.float32, (1,), device)
+    _check(r.workspace, "workspace", torch.uint8, None, device)
 
 
 def moe_router(desc: RouterDesc, logits: torch.Tensor, token_mask=None, loss: bool = True,
@@ -560,13 +574,16 @@ def moe_router(desc: RouterDesc, logits: torch.Tensor, token_mask=None, loss: bo
         with _alloc_on(stream):
             router = alloc_router(desc, dev, loss=loss)
     else:
-        _check_router(desc, router, True, loss, dev)
+        _check_picks(desc, router, dev)
+        if loss:
+            _check_loss(desc, router, dev)
     ws = router.workspace if loss else None
-    b = router.c()
-    if not loss:
-        b.expert_count = b.balance_coef = b.balance_loss = None
+    if loss:
+        b = router.c()
+    else:
+        b = moe_router_bufs(router.topk_idx.data_ptr(), router.topk_w.data_ptr())
     with _on_device(dev):
-        rc = _lib.moe_router(ctypes.byref(desc.c()), _ptr(logits), kind, _ptr(token_mask), ctypes.byref(b), _ptr(ws),
+        rc = _lib.moe_router(_made_once(desc), logits.data_ptr(), kind, _ptr(token_mask), ctypes.byref(b), _ptr(ws),
                              0 if ws is None else ws.numel(), _stream(stream, dev))
     if rc != MOE_OK:
         raise MoeError(rc, "moe_router")
@@ -585,10 +602,10 @@ def moe_balance_loss(desc: RouterDesc, logits: torch.Tensor, topk_idx: torch.Ten
         with _alloc_on(stream):
             router = alloc_router(desc, dev, picks=False)
     else:
-        _check_router(desc, router, False, True, dev)
+        _check_loss(desc, router, dev)
     ws = router.workspace
     with _on_device(dev):
-        rc = _lib.moe_balance_loss(ctypes.byref(desc.c()), _ptr(logits), kind, _ptr(topk_idx), _ptr(token_mask),
+        rc = _lib.moe_balance_loss(_made_once(desc), logits.data_ptr(), kind, topk_idx.data_ptr(), _ptr(token_mask),
                                    ctypes.byref(router.c()), _ptr(ws), 0 if ws is None else ws.numel(),
                                    _stream(stream, dev))
     if rc != MOE_OK:
@@ -603,19 +620,27 @@ def moe_router_backward(desc: RouterDesc, logits: torch.Tensor, router: Router, 
     desc, logits, router and token_mask as moe_router had and returned them."""
     dev = logits.device
     kind = _logits(desc, logits, token_mask)
-    _check_router(desc, router, d_topk_w is not None, d_loss is not None, dev)
-    _check(d_topk_w, "d_topk_w", torch.float32, (desc.S, desc.K), dev)
-    _check(d_loss, "d_loss", torch.float32, None, dev)
-    if d_loss is not None and d_loss.numel() != 1:
-        raise ValueError(f"d_loss: {d_loss.numel()} values, expected 1")
+    idx = w = coef = None
+    if d_topk_w is not None:
+        _check_picks(desc, router, dev)
+        _check(d_topk_w, "d_topk_w", torch.float32, (desc.S, desc.K), dev)
+        idx, w = router.topk_idx, router.topk_w
+    if d_loss is not None:
+        coef = router.balance_coef
+        if coef is None:
+            raise ValueError("router has no buffers for the loss")
+        _check(coef, "balance_coef", torch.float32, (desc.sequences, desc.E), dev)
+        _check(d_loss, "d_loss", torch.float32, None, dev)
+        if d_loss.numel() != 1:
+            raise ValueError(f"d_loss: {d_loss.numel()} values, expected 1")
     if d_logits is None:
         with _alloc_on(stream):
             d_logits = torch.empty_like(logits)
-    _check(d_logits, "d_logits", logits.dtype, (desc.S, desc.E), dev)
+    else:
+        _check(d_logits, "d_logits", logits.dtype, (desc.S, desc.E), dev)
     with _on_device(dev):
-        rc = _lib.moe_router_backward(ctypes.byref(desc.c()), _ptr(logits), kind, _ptr(token_mask),
-                                      _ptr(router.topk_idx), _ptr(router.topk_w), _ptr(router.balance_coef),
-                                      _ptr(d_topk_w), _ptr(d_loss), _ptr(d_logits), _stream(stream, dev))
+        rc = _lib.moe_router_backward(_made_once(desc), logits.data_ptr(), kind, _ptr(token_mask), _ptr(idx), _ptr(w),
+                                      _ptr(coef), _ptr(d_topk_w), _ptr(d_loss), d_logits.data_ptr(), _stream(stream, dev))
     if rc != MOE_OK:
         raise MoeError(rc, "moe_router_backward")
     return d_logits
@@ -647,11 +672,7 @@ class _RouterFunction(torch.autograd.Function):
             return None, None, None, None
         logits, token_mask, idx, w, coef = ctx.saved_tensors
         _no_capture("the backward pass of router / balance_loss")
-        G, E = ctx.desc.sequences, ctx.desc.E
-        # the backward call reads balance_coef; the two others stand in for outputs that it does not read
-        r = Router(idx, w, torch.empty((G, E), dtype=torch.int32, device=coef.device), coef,
-                   torch.empty(1, device=coef.device))
-        d = moe_router_backward(ctx.desc, logits, r, None if d_w is None else d_w.contiguous(),
+        d = moe_router_backward(ctx.desc, logits, Router(idx, w, None, coef, None), None if d_w is None else d_w.contiguous(),
                                 None if d_loss is None else d_loss.contiguous(), token_mask)
         return d, None, None, None
 
@@ -709,13 +730,16 @@ def moe_quantize_mx4(x: torch.Tensor, codes=None, scales=None, layout: Optional[
     _mx4_width(H, "moe_quantize_mx4")
     rows = x.numel() // H
     src = _check_src(layout, rows, dev)
+    lead = x.shape[:-1]
     with _alloc_on(stream):
         if codes is None:
-            codes = torch.empty((*x.shape[:-1], H // 2), dtype=torch.uint8, device=dev)
+            codes = torch.empty((*lead, H // 2), dtype=torch.uint8, device=dev)
+        else:
+            _check(codes, "codes", torch.uint8, (*lead, H // 2), dev)
         if scales is None:
-            scales = torch.empty((*x.shape[:-1], H // 32), dtype=torch.uint8, device=dev)
-    _check(codes, "codes", torch.uint8, (*x.shape[:-1], H // 2), dev)
-    _check(scales, "scales", torch.uint8, (*x.shape[:-1], H // 32), dev)
+            scales = torch.empty((*lead, H // 32), dtype=torch.uint8, device=dev)
+        else:
+            _check(scales, "scales", torch.uint8, (*lead, H // 32), dev)
     with _on_device(dev):
         rc = _lib.moe_quantize_mx4(_ptr(x), rows, H, _ptr(src), _ptr(codes), _ptr(scales), _stream(stream, dev))
     if rc != MOE_OK:
@@ -735,7 +759,8 @@ def moe_dequantize_mx4(codes: torch.Tensor, scales: torch.Tensor, out=None, layo
     if out is None:
         with _alloc_on(stream):
             out = torch.empty((*codes.shape[:-1], H), dtype=torch.bfloat16, device=dev)
-    _check(out, "out", torch.bfloat16, (*codes.shape[:-1], H), dev)
+    else:
+        _check(out, "out", torch.bfloat16, (*codes.shape[:-1], H), dev)
     with _on_device(dev):
         rc = _lib.moe_dequantize_mx4(_ptr(codes), _ptr(scales), rows, H, _ptr(src), _ptr(out), _stream(stream, dev))
     if rc != MOE_OK:
@@ -747,7 +772,7 @@ def moe_dispatch_mx4(desc: LayoutDesc, layout: Layout, hidden: torch.Tensor, top
                      recv_w=None, stream=None):
     """moe_dispatch in MXFP4.  Returns (recv [max_recv,H/2] uint8, recv_scales
     [max_recv,H/32] uint8, recv_w or None)."""
-    dev, H, rows = hidden.device, hidden.shape[-1], moe_max_recv_rows(desc)
+    dev, H, rows = hidden.device, hidden.shape[-1], int(_lib.moe_max_recv_rows(_made_once(desc)))
     _check(hidden, "hidden", torch.bfloat16, (desc.S, H))
     _check(topk_w, "topk_w", torch.float32, (desc.S, desc.K), dev)
     _mx4_width(H, "moe_dispatch_mx4")
@@ -765,9 +790,9 @@ def moe_dispatch_mx4(desc: LayoutDesc, layout: Layout, hidden: torch.Tensor, top
     _check(recv_w, "recv_w", torch.float32, None, dev)
     if recv_w is not None and recv_w.numel() < rows:
         raise ValueError(f"recv_w: {recv_w.numel()} rows, expected at least {rows}")
-    d, b = desc.c(), layout.c()
+    b = moe_layout_bufs(pos=layout.pos.data_ptr())
     with _on_device(dev):
-        rc = _lib.moe_dispatch_mx4(ctypes.byref(d), ctypes.byref(b), _ptr(hidden), H, _ptr(topk_w), _ptr(recv),
+        rc = _lib.moe_dispatch_mx4(_made_once(desc), ctypes.byref(b), _ptr(hidden), H, _ptr(topk_w), _ptr(recv),
                                    _ptr(recv_scales), _ptr(recv_w), _stream(stream, dev))
     if rc != MOE_OK:
         raise MoeError(rc, "moe_dispatch_mx4")
@@ -784,7 +809,7 @@ def moe_expert_gemm_mx4(desc: LayoutDesc, layout: Layout, x: torch.Tensor, x_sca
     MOE_ACT_SWIGLU (N gate rows, then N up rows).  ``balance`` and
     ``slots_per_rank`` for a layout of moe_layout_balanced.  Rows that hold no
     entry are neither read nor written."""
-    dev, H, rows = x.device, x.shape[-1] * 2, moe_max_recv_rows(desc)
+    dev, H, rows = x.device, x.shape[-1] * 2, int(_lib.moe_max_recv_rows(_made_once(desc)))
     _mx4_width(H, "moe_expert_gemm_mx4")
     if rows < 0 or act not in (MOE_ACT_NONE, MOE_ACT_SWIGLU):
         raise MoeError(MOE_ERR_SHAPE, "moe_expert_gemm_mx4")
@@ -806,10 +831,10 @@ def moe_expert_gemm_mx4(desc: LayoutDesc, layout: Layout, x: torch.Tensor, x_sca
     _check(out, "out", torch.bfloat16, None, dev)
     if out.dim() != 2 or out.shape[1] != N or out.shape[0] < rows:
         raise ValueError(f"out: shape {tuple(out.shape)}, expected [at least {rows}, {N}]")
-    d, b = desc.c(), layout.c()
+    b = moe_layout_bufs(tokens_per_expert=layout.tokens_per_expert.data_ptr(), expert_offset=layout.expert_offset.data_ptr())
     bal = None if balance is None else ctypes.byref(balance.c())
     with _on_device(dev):
-        rc = _lib.moe_expert_gemm_mx4(ctypes.byref(d), ctypes.byref(b), bal, slots_per_rank, _ptr(x), _ptr(x_scales), H,
+        rc = _lib.moe_expert_gemm_mx4(_made_once(desc), ctypes.byref(b), bal, slots_per_rank, _ptr(x), _ptr(x_scales), H,
                                       _ptr(w), _ptr(w_scales), N, act, _ptr(out), _stream(stream, dev))
     if rc != MOE_OK:
         raise MoeError(rc, "moe_expert_gemm_mx4")

@@ -17,6 +17,7 @@
 #include "mx4.h"
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 namespace moe {
@@ -157,25 +158,26 @@ __device__ __forceinline__ void wave_lds_fence() {
 // short segments
 // ---------------------------------------------------------------------------
 
-// 16 token rows by 64 weight rows; the four waves split the channels and join
+// 16 token rows by 32 weight rows; the four waves split the channels and join
 // their sums in LDS.  The weights' bytes are the work, each read once, so what
 // counts is to keep many of them in flight and to ask for whole lines: a unit
-// (256 channels) of the 64 rows, 8 KB, is copied to the wave's own LDS in
+// (256 channels) of the 32 rows, 4 KB, is copied to the wave's own LDS in
 // instructions of 8 whole 128-byte lines while the unit before it is
-// multiplied, two workgroups of four such waves per CU.  (The operands' own
+// multiplied, four workgroups of four such waves per CU.  (The operands' own
 // order, straight to registers, asks for 64 pieces of 16 bytes per instruction:
-// DECODE_OLD us at the decode case, 1024 rows of 256 experts, H = 7168, 2 x 1024
-// weight rows, against DECODE_US here.)  The wave's channels' weight scales come
+// 432 us at the decode case, 1024 rows of 256 experts, H = 7168, 2 x 1024 weight
+// rows, against 328 us = 6.0 TB/s here; 64 weight rows and two workgroups per CU
+// took 350 us, two waves of 32 rows 339, one 348, eight 395.)  The wave's channels' weight scales come
 // in parts of 8 units; tokens and their scales, few and shared by every
 // workgroup of the segment, go straight to registers.
 constexpr int kStreamRows = 16;
 constexpr int kStreamWaves = 4;
-constexpr int kWTiles = 4;         // 16-row weight tiles (SWIGLU: half gate, half up)
+constexpr int kWTiles = 2;         // 16-row weight tiles (SWIGLU: half gate, half up)
 constexpr int kUnitVecs = kWTiles * 16 * 8;
 constexpr int kPartUnits = 8;      // units whose scales are in LDS
 
 template <bool SWIGLU>
-__global__ __launch_bounds__(kStreamWaves * kWave, 2) void k_expert_stream(ExpertGemmArgs a, int tiles_n) {
+__global__ __launch_bounds__(kStreamWaves * kWave, 4) void k_expert_stream(ExpertGemmArgs a, int tiles_n) {
     constexpr int kOutTiles = SWIGLU ? kWTiles / 2 : kWTiles;
     __shared__ u32x4 unit0[kStreamWaves][kUnitVecs], unit1[kStreamWaves][kUnitVecs];
     __shared__ unsigned int wscale[kStreamWaves][kWTiles * 16 * 2 * kPartUnits];
@@ -209,7 +211,7 @@ __global__ __launch_bounds__(kStreamWaves * kWave, 2) void k_expert_stream(Exper
         const unsigned int gone = 2 * u + 1 >= steps && (((lane & 7) ^ q8) & 4) ? kPastEnd : 0u;
 #pragma unroll
         for (int j = 0; j < kWTiles * 2; ++j) {
-            const int row = 8 * j;                                       // of the 64
+            const int row = 8 * j;
             const bool is_up = row >= kOutTiles * 16;
             copy_to_lds(is_up ? w_up : w_gate, to + row * 8, (wo + (is_up ? row - kOutTiles * 16 : row) * half) | gone, u * 128);
         }
@@ -699,8 +701,29 @@ int64_t most_tiles(const ExpertGemmArgs &a, int BM) {
     return std::min(a.entries / BM + used, used * ((a.max_count + BM - 1) / BM));
 }
 
-// The rule between the two kernels: rows per segment in use, on average.
-bool long_segments(const ExpertGemmArgs &a) { return a.entries > 16 * std::min<int64_t>(a.nseg, a.entries); }
+// The rule between the two kernels: the sooner by these estimates, in
+// microseconds, which hold what was measured within about a fifth.
+//   stream: a workgroup's work is one 16-row tile by 32 weight rows, with about 6
+//     steps' worth of its own start and end; 3200 such steps a microsecond, or
+//     the weights at 6.0 TB/s.
+//   tile: a start of 6 us, then each round of 256 workgroups one tile, 0.4 us a
+//     step for few rows to 0.8 us for 128 and more; or the weights at 4.9 TB/s.
+// Measured, stream / tile (us; E experts with m rows each, M weight rows):
+//   E=256 H=7168 M=2048  m=1 214 / 257   m=4 338 / 400   m=8 374 / 406   m=12 445 / 411
+//   E=256 H=2048 M=7168  m=4 421 / 391   m=16 644 / 438
+//   E=64  H=1024 M=4096  m=1 23 / 19     m=12 44 / 30
+//   E=64  H=2048 M=2048  m=1 20 / 21     m=12 33 / 27
+//   E=8   H=7168 M=2048  m=32 26 / 30    m=64 41 / 34    m=256 134 / 51
+//   E=4   H=7168 M=512   m=256 24 / 49
+bool long_segments(const ExpertGemmArgs &a) {
+    const double used = static_cast<double>(std::min<int64_t>(a.nseg, a.entries)), rows = static_cast<double>(a.entries);
+    if (used == 0) return false;
+    const double M = a.swiglu ? 2.0 * a.N : a.N, steps = a.H / kStep, weights = used * M * a.H * (17.0 / 32.0);
+    const double stream_tiles = std::max(used, rows / kStreamRows + used / 2), tiles = std::max(used, rows / kTileRows + used / 2);
+    const double stream = std::max(stream_tiles * (M / (16 * kWTiles)) * (steps + 6) / 3200, weights / 6.0e6);
+    const double rounds = std::ceil(tiles * std::ceil(M / kTileWeights) / kCus), step_us = 0.4 + 0.4 * std::min(1.0, rows / used / 128);
+    return std::max(6 + rounds * steps * step_us, weights / 4.9e6) < stream;
+}
 
 struct Grid {
     int tiles_n;
