@@ -4,8 +4,8 @@
 // l*V .. l*V+V-1 (V = E/64 rounded up to a power of two), so the lowest index
 // among equal logits is the lowest lane, then the lowest register.  Softmax is
 // one maximum and one sum across the wave (DPP); a pick is the wave's maximum,
-// one ballot for its lane, and the owner's register struck out, K times.  All
-// arithmetic is fp32.
+// one ballot for its lane, and the owner's register struck out, K times.
+// Arithmetic is fp32, sums over workgroups fp64.
 //
 // Loss = sum over tokens and experts of coef[sequence][e] * p[t][e], where coef
 // comes from the counts alone.  A workgroup adds up its own tokens'
@@ -15,7 +15,8 @@
 // cleared before a call.
 //
 // Bound: at path sizes (4 MB of logits) launch and latency; beyond, reading
-// the logits.
+// the logits.  4096 x 256, K = 8 of 4 of 8 groups: picks and sums 9.4 us, the
+// finish 7.5, the gradient 5.8; 128 tokens to serve 5.0 us.
 #include <algorithm>
 
 #include "router.h"
@@ -23,9 +24,12 @@
 namespace moe {
 namespace {
 
-constexpr int kRouterWaves = 4;
+constexpr int kRouterWaves = 4;              // tokens of a workgroup without the loss, and of the backward pass
 constexpr int kMaxGroups = 64;
 constexpr int kFinishThreads = 1024;
+constexpr int kMaxParts = 256;               // workgroups per sequence
+constexpr int kMaxLastParts = 1024;          // workgroups whose last one adds up the loss
+constexpr int kMaxCountedSeqs = 8192;        // sequences that k_router_finish counts itself
 
 // Wave-wide reductions: DPP shifts inside rows of 16, then across rows; lane
 // 63 ends with the result and every lane reads it from there.
@@ -194,7 +198,22 @@ __device__ __forceinline__ void pick_top(float (&z)[V], int K, int &my_idx, floa
     }
 }
 
-// LDS of one workgroup's loss sums: [waves][E] fp32 probabilities, [E] counts.
+// Waves of a workgroup that sums for the loss: as many as keep a SIMD busy (a
+// token's picks are one long chain of dependent steps: with 4 waves per
+// workgroup and 4 tokens per wave the 4096 x 256 batch took 16.0 us, with 16
+// waves and one token each 9.4), with LDS for a row of E sums each.
+template <int V>
+constexpr int loss_waves() {
+    return V <= 4 ? 16 : 64 / V;
+}
+
+// What the finishing launch reads, per workgroup and expert: the sum of the
+// probabilities and the picks.
+struct Partial {
+    float p;
+    int32_t c;
+};
+
 struct LossShape {
     int per_seq;   // workgroups per sequence
     int tokens;    // tokens per workgroup
@@ -202,33 +221,32 @@ struct LossShape {
 
 // GIVEN: the routing is the caller's; else the router picks.  LOSS: the
 // workgroup's tokens are a run of one sequence and it writes partial sums.
-template <int V, bool BF16, bool VEC, bool GIVEN, bool LOSS>
-__global__ __launch_bounds__(kRouterWaves * kWave) void k_router(RouterArgs a, LossShape sh, float *part_p,
-                                                                int32_t *part_c, int32_t *part_n) {
-    extern __shared__ __align__(16) unsigned char lds[];
-    __shared__ unsigned int best[kRouterWaves][kMaxGroups];
+template <int V, bool BF16, bool VEC, bool GIVEN, bool LOSS, int WAVES = LOSS ? loss_waves<V>() : kRouterWaves>
+__global__ __launch_bounds__(WAVES * kWave) void k_router(RouterArgs a, LossShape sh, Partial *part, int32_t *part_n,
+                                                         int32_t *counter) {
+    __shared__ float s_p[LOSS ? WAVES * V * kWave : 1];       // [waves][E] probabilities
+    __shared__ int32_t s_c[LOSS ? V * kWave : 1];             // [E] picks
+    __shared__ unsigned int best[GIVEN ? 1 : WAVES][kMaxGroups];
     __shared__ int s_n;
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int E = a.E, K = a.K;
-    float *s_p = reinterpret_cast<float *>(lds);
-    int32_t *s_c = reinterpret_cast<int32_t *>(lds) + kRouterWaves * E;
     int64_t t0, t1;
     if constexpr (LOSS) {
-        const int64_t g = blockIdx.x / sh.per_seq, part = blockIdx.x % sh.per_seq;
-        t0 = g * a.seq + part * sh.tokens;
+        const int64_t g = blockIdx.x / sh.per_seq, at = blockIdx.x % sh.per_seq;
+        t0 = g * a.seq + at * sh.tokens;
         t1 = min(t0 + sh.tokens, (g + 1) * static_cast<int64_t>(a.seq));
-        for (int e = threadIdx.x; e < E; e += kRouterWaves * kWave) s_c[e] = 0;
+        for (int e = threadIdx.x; e < E; e += WAVES * kWave) s_c[e] = 0;
         if (threadIdx.x == 0) s_n = 0;
         __syncthreads();
     } else {
-        t0 = static_cast<int64_t>(blockIdx.x) * kRouterWaves;
-        t1 = min(t0 + kRouterWaves, static_cast<int64_t>(a.S));
+        t0 = static_cast<int64_t>(blockIdx.x) * WAVES;
+        t1 = min(t0 + WAVES, static_cast<int64_t>(a.S));
     }
     float sum[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) sum[j] = 0.0f;
     int n = 0;
-    for (int64_t t = t0 + wave; t < t1; t += kRouterWaves) {
+    for (int64_t t = t0 + wave; t < t1; t += WAVES) {
         float z[V];
         load_logits<V, BF16, VEC>(a.logits, t, E, z);
         const bool masked = a.mask != nullptr && a.mask[t] == 0;
@@ -288,14 +306,14 @@ __global__ __launch_bounds__(kRouterWaves * kWave) void k_router(RouterArgs a, L
         if (lane == 0) atomicAdd(&s_n, n);
         __syncthreads();
         const size_t base = static_cast<size_t>(blockIdx.x) * E;
-        for (int e = threadIdx.x; e < E; e += kRouterWaves * kWave) {
-            float s = 0.0f;
+        for (int e = threadIdx.x; e < E; e += WAVES * kWave) {
+            float v = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kRouterWaves; ++w) s += s_p[w * E + e];
-            part_p[base + e] = s;
-            part_c[base + e] = s_c[e];
+            for (int w = 0; w < WAVES; ++w) v += s_p[w * E + e];
+            part[base + e] = Partial{v, s_c[e]};
         }
         if (threadIdx.x == 0) part_n[blockIdx.x] = s_n;
+        if (blockIdx.x == 0 && threadIdx.x == 0) *counter = 0;   // for k_router_finish, launched behind this
     }
 }
 
@@ -311,7 +329,8 @@ __device__ __forceinline__ double block_sum(double v, double *s_tmp) {
     return s;
 }
 
-// Sequences with a token that counts (one workgroup; only for G > 1).
+// Sequences with a token that counts, for more of them than k_router_finish
+// counts itself (one workgroup).
 __global__ __launch_bounds__(kFinishThreads) void k_router_used(const int32_t *__restrict__ part_n, int G, int per_seq,
                                                                int32_t *used) {
     __shared__ double s_tmp[kFinishThreads / kWave];
@@ -325,64 +344,97 @@ __global__ __launch_bounds__(kFinishThreads) void k_router_used(const int32_t *_
     if (threadIdx.x == 0) *used = static_cast<int32_t>(total);
 }
 
-// One workgroup per sequence: adds the partial rows in order, writes the
-// sequence's counts and coefficients, and its part of the loss (the loss
-// itself where there is one sequence: used == null).
-__global__ __launch_bounds__(kFinishThreads) void k_router_finish(RouterArgs a, int per_seq,
-                                                                 const float *__restrict__ part_p,
-                                                                 const int32_t *__restrict__ part_c,
+// One workgroup per sequence and kFinishCols experts: adds the partial rows in
+// order, writes counts and coefficients, and its part of the loss (the loss
+// itself where it is alone).  used: the number of sequences that count, or null:
+// then it is counted here, a bit in LDS for each.  The rows come from every
+// XCD's workgroups, past this one's L2, so few columns per workgroup: all 256 of
+// the 4096 x 256 batch in one took 23 us, 32 take 7.5.
+constexpr int kFinishCols = 32;
+__global__ __launch_bounds__(kFinishThreads) void k_router_finish(RouterArgs a, int per_seq, int col_blocks,
+                                                                 const Partial *__restrict__ part,
                                                                  const int32_t *__restrict__ part_n,
-                                                                 const int32_t *__restrict__ used, double *part_loss) {
-    __shared__ double s_tmp[kFinishThreads / kWave];
-    __shared__ double s_p[kFinishThreads];
-    __shared__ int32_t s_c[kFinishThreads];
-    const int tid = threadIdx.x, E = a.E;
-    const size_t first = static_cast<size_t>(blockIdx.x) * per_seq;
-    double cnt = 0.0;
-    for (int b = tid; b < per_seq; b += kFinishThreads) cnt += part_n[first + b];
-    const double n = block_sum(cnt, s_tmp);
-    const double seqs = used != nullptr ? static_cast<double>(*used) : 1.0;
-    const double unit = n > 0.0 ? static_cast<double>(a.alpha) * E / (seqs * a.K * n * n) : 0.0;
-    // the threads of a column's slice: slice s adds rows s, s + slices, ...
-    const int slices = max(1, kFinishThreads / E), cols = min(E, kFinishThreads);
-    double loss = 0.0;
-    const int e = tid % cols, s = tid / cols;   // E <= kMaxE = kFinishThreads: one column per thread
+                                                                 const int32_t *__restrict__ used, double *part_loss,
+                                                                 int32_t *counter) {
+    constexpr int kSlices = kFinishThreads / kFinishCols;
+    constexpr int kBatch = kMaxParts / kSlices;   // a thread's rows, all in flight
+    __shared__ int2 s_tmp[kFinishThreads / kWave];
+    __shared__ double s_p[kSlices][kFinishCols];
+    __shared__ int32_t s_c[kSlices][kFinishCols];
+    __shared__ unsigned int s_bits[kMaxCountedSeqs / 32];
+    const int tid = threadIdx.x, E = a.E, g = blockIdx.x / col_blocks;
+    const int col = tid % kFinishCols, slice = tid / kFinishCols, e = (blockIdx.x % col_blocks) * kFinishCols + col;
+    const size_t first = static_cast<size_t>(g) * per_seq;
+    const bool count_here = a.G > 1 && used == nullptr;
+    // slice s adds rows s, s + slices, ...
+    Partial v[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+        const int b = slice + i * kSlices;
+        v[i] = b < per_seq && e < E ? part[(first + b) * E + e] : Partial{0.0f, 0};
+    }
+    int2 mine = make_int2(tid < per_seq ? part_n[first + tid] : 0, 0);   // per_seq <= kMaxParts
+    if (count_here) {
+        for (int i = tid; i < (a.G + 31) / 32; i += kFinishThreads) s_bits[i] = 0u;
+        __syncthreads();
+        for (int i = tid; i < a.G * per_seq; i += kFinishThreads)
+            if (part_n[i] != 0) atomicOr(&s_bits[i / per_seq / 32], 1u << (i / per_seq % 32));
+        __syncthreads();
+        for (int i = tid; i < (a.G + 31) / 32; i += kFinishThreads) mine.y += __popc(s_bits[i]);
+    }
     double p = 0.0;
     int32_t c = 0;
-    if (s < slices) {
-#pragma unroll 4
-        for (int b = s; b < per_seq; b += slices) {
-            p += part_p[(first + b) * E + e];
-            c += part_c[(first + b) * E + e];
-        }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+        p += v[i].p;
+        c += v[i].c;
     }
-    s_p[tid] = p;
-    s_c[tid] = c;
-    __syncthreads();
-    if (s == 0) {
-        for (int i = 1; i < slices; ++i) {
-            p += s_p[i * cols + e];
-            c += s_c[i * cols + e];
+    s_p[slice][col] = p;
+    s_c[slice][col] = c;
+    int2 sums;
+    block_exclusive_scan2<kFinishThreads / kWave>(mine, s_tmp, sums);
+    if (tid >= kWave) return;
+    const double n = sums.x, seqs = count_here ? sums.y : (a.G > 1 ? *used : 1);
+    double loss = 0.0;
+    if (slice == 0 && e < E) {
+#pragma unroll
+        for (int i = 1; i < kSlices; ++i) {
+            p += s_p[i][col];
+            c += s_c[i][col];
         }
-        const size_t cell = static_cast<size_t>(blockIdx.x) * E + e;
-        const double coef = unit * c;
+        const size_t cell = static_cast<size_t>(g) * E + e;
+        const double coef = n > 0.0 ? static_cast<double>(a.alpha) * E / (seqs * a.K * n * n) * c : 0.0;
         a.count[cell] = c;
         a.coef[cell] = static_cast<float>(coef);
         loss = coef * p;
     }
-    loss = block_sum(loss, s_tmp);
-    if (tid == 0) {
-        if (used == nullptr)
-            *a.loss = static_cast<float>(loss);
-        else
-            part_loss[blockIdx.x] = loss;
+    for (int d = kWave / 2; d > 0; d /= 2) loss += __shfl_xor(loss, d, kWave);
+    if (gridDim.x == 1) {
+        if (tid == 0) *a.loss = static_cast<float>(loss);
+        return;
     }
+    // The workgroup that arrives last adds the parts, in their own order: a
+    // launch less than k_router_loss.  Nobody waits.  (The counter is 0: k_router
+    // cleared it.)
+    int arrived = 0;
+    if (tid == 0) {
+        __hip_atomic_store(part_loss + blockIdx.x, loss, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (gridDim.x <= kMaxLastParts)
+            arrived = __hip_atomic_fetch_add(counter, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) + 1;
+    }
+    if (__builtin_amdgcn_readfirstlane(arrived) != static_cast<int>(gridDim.x)) return;
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    loss = 0.0;
+    for (int i = tid; i < static_cast<int>(gridDim.x); i += kWave)
+        loss += __hip_atomic_load(part_loss + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    for (int d = kWave / 2; d > 0; d /= 2) loss += __shfl_xor(loss, d, kWave);
+    if (tid == 0) *a.loss = static_cast<float>(loss);
 }
 
-__global__ __launch_bounds__(kFinishThreads) void k_router_loss(const double *__restrict__ part_loss, int G, float *loss) {
+__global__ __launch_bounds__(kFinishThreads) void k_router_loss(const double *__restrict__ part_loss, int n, float *loss) {
     __shared__ double s_tmp[kFinishThreads / kWave];
     double v = 0.0;
-    for (int g = threadIdx.x; g < G; g += kFinishThreads) v += part_loss[g];
+    for (int i = threadIdx.x; i < n; i += kFinishThreads) v += part_loss[i];
     v = block_sum(v, s_tmp);
     if (threadIdx.x == 0) *loss = static_cast<float>(v);
 }
@@ -474,31 +526,34 @@ __global__ __launch_bounds__(kRouterWaves * kWave) void k_router_backward(Router
     }
 }
 
-// Workgroups of the loss form: 4 tokens per wave, more once that would make
-// more than kMaxParts partial rows, whose sum is one workgroup's work.
-constexpr int kMaxParts = 256;
+// Lanes' experts: the power of two that covers E.
+int lane_experts(int E) { return E <= 64 ? 1 : (E <= 128 ? 2 : (E <= 256 ? 4 : (E <= 512 ? 8 : 16))); }
+
+// Workgroups of the loss form: a token per wave, more once that would make more
+// than kMaxParts partial rows in a sequence, whose sum is one workgroup's work.
 LossShape loss_shape(const RouterArgs &a) {
+    const int v = lane_experts(a.E), waves = v <= 4 ? 16 : 64 / v;
     LossShape sh;
-    const int64_t per_seq_cap = std::max<int64_t>(1, kMaxParts / std::max(a.G, 1));
-    sh.tokens = static_cast<int>(std::max<int64_t>(4 * kRouterWaves, (a.seq + per_seq_cap - 1) / per_seq_cap));
+    sh.tokens = static_cast<int>(std::max<int64_t>(waves, (a.seq + int64_t(kMaxParts) - 1) / kMaxParts));
     sh.per_seq = std::max(1, static_cast<int>((static_cast<int64_t>(a.seq) + sh.tokens - 1) / sh.tokens));
     return sh;
 }
 
+int finish_blocks(const RouterArgs &a) { return (a.E + kFinishCols - 1) / kFinishCols; }
+
 size_t up16(size_t x) { return (x + 15) & ~size_t(15); }
 
 struct LossWorkspace {
-    size_t p, c, n, used, loss, bytes;
+    size_t part, n, used, loss, bytes;
 };
 LossWorkspace loss_workspace(const RouterArgs &a, const LossShape &sh) {
     LossWorkspace w{};
-    const size_t parts = static_cast<size_t>(a.G) * sh.per_seq, cells = parts * a.E;
-    w.p = 0;
-    w.c = up16(w.p + cells * 4);
-    w.n = up16(w.c + cells * 4);
+    const size_t parts = static_cast<size_t>(a.G) * sh.per_seq;
+    w.part = 0;
+    w.n = up16(parts * a.E * sizeof(Partial));
     w.used = up16(w.n + parts * 4);
     w.loss = w.used + 16;
-    w.bytes = up16(w.loss + static_cast<size_t>(a.G) * 8);
+    w.bytes = up16(w.loss + static_cast<size_t>(a.G) * finish_blocks(a) * 8);
     return w;
 }
 
@@ -516,11 +571,9 @@ hipError_t launch_v(const RouterArgs &a, void *workspace, hipStream_t s) {
     if (a.loss == nullptr) {
         const dim3 grid((static_cast<unsigned>(a.S) + kRouterWaves - 1) / kRouterWaves);
         if (vec)
-            hipLaunchKernelGGL((k_router<V, BF16, true, GIVEN, false>), grid, block, 0, s, a, LossShape{}, nullptr,
-                               nullptr, nullptr);
+            hipLaunchKernelGGL((k_router<V, BF16, true, GIVEN, false>), grid, block, 0, s, a, LossShape{}, nullptr, nullptr, nullptr);
         else
-            hipLaunchKernelGGL((k_router<V, BF16, false, GIVEN, false>), grid, block, 0, s, a, LossShape{}, nullptr,
-                               nullptr, nullptr);
+            hipLaunchKernelGGL((k_router<V, BF16, false, GIVEN, false>), grid, block, 0, s, a, LossShape{}, nullptr, nullptr, nullptr);
         return hipGetLastError();
     }
     if (a.G == 0) {   // no sequence: the loss is 0
@@ -530,21 +583,21 @@ hipError_t launch_v(const RouterArgs &a, void *workspace, hipStream_t s) {
     const LossShape sh = loss_shape(a);
     const LossWorkspace w = loss_workspace(a, sh);
     char *ws = static_cast<char *>(workspace);
-    float *pp = reinterpret_cast<float *>(ws + w.p);
-    int32_t *pc = reinterpret_cast<int32_t *>(ws + w.c), *pn = reinterpret_cast<int32_t *>(ws + w.n);
-    int32_t *used = reinterpret_cast<int32_t *>(ws + w.used);
+    Partial *part = reinterpret_cast<Partial *>(ws + w.part);
+    int32_t *pn = reinterpret_cast<int32_t *>(ws + w.n), *used = reinterpret_cast<int32_t *>(ws + w.used);
     double *pl = reinterpret_cast<double *>(ws + w.loss);
-    const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(a.G) * sh.per_seq));
-    const size_t lds = static_cast<size_t>(kRouterWaves + 1) * a.E * 4;
+    const int64_t parts = static_cast<int64_t>(a.G) * sh.per_seq;
+    const dim3 grid(static_cast<unsigned>(parts)), wide(loss_waves<V>() * kWave);
     if (vec)
-        hipLaunchKernelGGL((k_router<V, BF16, true, GIVEN, true>), grid, block, lds, s, a, sh, pp, pc, pn);
+        hipLaunchKernelGGL((k_router<V, BF16, true, GIVEN, true>), grid, wide, 0, s, a, sh, part, pn, used + 1);
     else
-        hipLaunchKernelGGL((k_router<V, BF16, false, GIVEN, true>), grid, block, lds, s, a, sh, pp, pc, pn);
-    const bool many = a.G > 1;
-    if (many) hipLaunchKernelGGL(k_router_used, dim3(1), dim3(kFinishThreads), 0, s, pn, a.G, sh.per_seq, used);
-    hipLaunchKernelGGL(k_router_finish, dim3(a.G), dim3(kFinishThreads), 0, s, a, sh.per_seq, pp, pc, pn,
-                       many ? used : nullptr, pl);
-    if (many) hipLaunchKernelGGL(k_router_loss, dim3(1), dim3(kFinishThreads), 0, s, pl, a.G, a.loss);
+        hipLaunchKernelGGL((k_router<V, BF16, false, GIVEN, true>), grid, wide, 0, s, a, sh, part, pn, used + 1);
+    const bool count_apart = a.G > kMaxCountedSeqs || parts > 16 * kMaxCountedSeqs;
+    if (count_apart) hipLaunchKernelGGL(k_router_used, dim3(1), dim3(kFinishThreads), 0, s, pn, a.G, sh.per_seq, used);
+    const int cols = finish_blocks(a), blocks = a.G * cols;
+    hipLaunchKernelGGL(k_router_finish, dim3(blocks), dim3(kFinishThreads), 0, s, a, sh.per_seq, cols, part, pn,
+                       count_apart ? used : nullptr, pl, used + 1);
+    if (blocks > kMaxLastParts) hipLaunchKernelGGL(k_router_loss, dim3(1), dim3(kFinishThreads), 0, s, pl, blocks, a.loss);
     return hipGetLastError();
 }
 

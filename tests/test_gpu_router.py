@@ -102,6 +102,9 @@ SHAPES = [
     (1200, 24, 3, dict(seq_len=24, alpha=3.0)),
     (5000, 16, 4, {}),
     (4608, 64, 6, dict(seq_len=1536)),
+    (2100, 48, 2, dict(seq_len=1)),          # more parts of the loss than the last workgroup adds
+    (9000, 8, 2, dict(seq_len=1, renorm=False)),   # more sequences than it counts
+    (18000, 40, 3, dict(seq_len=9000)),      # more tokens than workgroups' waves
 ]
 
 
