@@ -127,8 +127,15 @@ def lib() -> ctypes.CDLL:
 # descriptors
 # ---------------------------------------------------------------------------
 
+class _Descriptor:
+    """A frozen descriptor; its C struct is built once and is no part of its state."""
+
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k != "_ref"}
+
+
 @dataclasses.dataclass(frozen=True)
-class LayoutDesc:
+class LayoutDesc(_Descriptor):
     S: int
     K: int
     E: int
@@ -477,7 +484,7 @@ def _on_device(device):
 
 
 @dataclasses.dataclass(frozen=True)
-class RouterDesc:
+class RouterDesc(_Descriptor):
     """A router's shape and rule (fields as moe_router_desc; n_groups = 1 and
     seq_len = 0: no groups, one sequence)."""
     S: int

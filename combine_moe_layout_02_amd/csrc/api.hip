@@ -396,6 +396,8 @@ moe_status router_forward(const moe_router_desc *desc, const void *logits, int32
     if (desc == nullptr || out == nullptr) return MOE_ERR_NULL;
     if (!router_desc_ok(desc, !given) || !logits_type_ok(logits_type)) return MOE_ERR_SHAPE;
     const bool loss = out->balance_loss != nullptr;
+    moe::RouterArgs a = router_args(desc, logits, logits_type, token_mask);
+    if (!moe::router_grid_ok(a, loss)) return MOE_ERR_SHAPE;
     const bool cells = router_sequences(desc) > 0;      // no sequence: no counts and no coefficients
     if (loss && cells && (out->expert_count == nullptr || out->balance_coef == nullptr)) return MOE_ERR_NULL;
     if (!loss && (given || out->expert_count != nullptr || out->balance_coef != nullptr)) return MOE_ERR_NULL;
@@ -406,7 +408,6 @@ moe_status router_forward(const moe_router_desc *desc, const void *logits, int32
         !aligned(out->balance_coef, 4) || !aligned(out->balance_loss, 4))
         return MOE_ERR_ALIGN;
     if (!given && (!aligned(out->topk_idx, 4) || !aligned(out->topk_w, 4))) return MOE_ERR_ALIGN;
-    moe::RouterArgs a = router_args(desc, logits, logits_type, token_mask);
     a.given_idx = given ? given_idx : nullptr;
     a.given = given;
     a.idx = out->topk_idx;
@@ -424,9 +425,9 @@ moe_status router_forward(const moe_router_desc *desc, const void *logits, int32
     return moe::launch_router(a, workspace, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
-// Rows an MXFP4 conversion's launch can number: one workgroup per 8192 channels.
+// Rows an MXFP4 conversion's launch can number: a thread per 32 channels.
 bool mx4_rows_ok(int64_t rows, int32_t H) {
-    return H >= 128 && H % 128 == 0 && rows >= 0 && rows <= (int64_t(INT32_MAX) * 8192) / H;
+    return H >= 128 && H % 128 == 0 && rows >= 0 && rows <= ((moe::kMaxLaunchThreads >> 8 << 8) * 32) / H;
 }
 
 }  // namespace
@@ -435,7 +436,8 @@ extern "C" {
 
 size_t moe_router_workspace_bytes(const moe_router_desc *desc) {
     if (desc == nullptr || !router_desc_ok(desc, false)) return 0;
-    return moe::router_workspace_bytes(router_args(desc, nullptr, MOE_F32, nullptr));
+    const moe::RouterArgs a = router_args(desc, nullptr, MOE_F32, nullptr);
+    return moe::router_grid_ok(a, true) ? moe::router_workspace_bytes(a) : 0;
 }
 
 moe_status moe_router(const moe_router_desc *desc, const void *logits, int32_t logits_type, const uint8_t *token_mask,
@@ -455,6 +457,8 @@ moe_status moe_router_backward(const moe_router_desc *desc, const void *logits, 
                                void *stream) {
     if (desc == nullptr) return MOE_ERR_NULL;
     if (!router_desc_ok(desc, d_topk_w != nullptr) || !logits_type_ok(logits_type)) return MOE_ERR_SHAPE;
+    moe::RouterArgs a = router_args(desc, logits, logits_type, token_mask);
+    if (!moe::router_grid_ok(a, false)) return MOE_ERR_SHAPE;
     if (d_topk_w == nullptr && d_loss == nullptr) return MOE_ERR_NULL;
     if (desc->S == 0) return MOE_OK;
     if (logits == nullptr || d_logits == nullptr) return MOE_ERR_NULL;
@@ -464,7 +468,6 @@ moe_status moe_router_backward(const moe_router_desc *desc, const void *logits, 
     if (!aligned(logits, size) || !aligned(d_logits, size) || !aligned(topk_idx, 4) || !aligned(topk_w, 4) ||
         !aligned(balance_coef, 4) || !aligned(d_topk_w, 4) || !aligned(d_loss, 4))
         return MOE_ERR_ALIGN;
-    moe::RouterArgs a = router_args(desc, logits, logits_type, token_mask);
     a.picked = topk_idx;
     a.picked_w = topk_w;
     a.saved_coef = d_loss != nullptr ? balance_coef : nullptr;
@@ -500,7 +503,7 @@ moe_status moe_dispatch_mx4(const moe_layout_desc *desc, const moe_layout_bufs *
     if (!desc_ok(desc) || max_rows(desc) < 0 || H < 128 || H % 128 != 0) return MOE_ERR_SHAPE;
     // one single-wave workgroup per (token, 2048-channel chunk)
     if (static_cast<int64_t>(desc->S) * ((static_cast<int64_t>(H) + moe::kMx4WaveChannels - 1) / moe::kMx4WaveChannels) >
-        INT32_MAX)
+        moe::kMaxLaunchThreads / moe::kWave)
         return MOE_ERR_SHAPE;
     if (desc->S == 0) return MOE_OK;
     if (hidden == nullptr || recv == nullptr || recv_scales == nullptr || layout->pos == nullptr) return MOE_ERR_NULL;

@@ -1,6 +1,7 @@
 // The experts' products on MXFP4 rows: launch declaration.
 #pragma once
 
+#include "launch_limit.h"
 #include "moe_kernels.h"
 
 namespace moe {

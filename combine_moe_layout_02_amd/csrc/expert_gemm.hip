@@ -743,7 +743,10 @@ Grid grid_of(const ExpertGemmArgs &a) {
 
 }  // namespace
 
-bool expert_gemm_grid_ok(const ExpertGemmArgs &a) { return grid_of(a).tiles <= INT32_MAX - kCus; }
+bool expert_gemm_grid_ok(const ExpertGemmArgs &a) {
+    const Grid g = grid_of(a);
+    return g.tiles <= INT32_MAX - kCus && g.blocks * std::max(kStreamWaves * kWave, kTileThreads) <= kMaxLaunchThreads;
+}
 
 hipError_t launch_expert_gemm_mx4(const ExpertGemmArgs &a, hipStream_t s) {
     const Grid g = grid_of(a);

@@ -2,6 +2,7 @@
 // declarations and the conversion of one lane's channels.
 #pragma once
 
+#include "launch_limit.h"
 #include "moe_kernels.h"
 
 namespace moe {

@@ -1,6 +1,7 @@
 // Router and balance loss: launch declarations.
 #pragma once
 
+#include "launch_limit.h"
 #include "moe_kernels.h"
 
 namespace moe {
@@ -31,6 +32,7 @@ struct RouterArgs {
 };
 
 size_t router_workspace_bytes(const RouterArgs &a);
+bool router_grid_ok(const RouterArgs &a, bool loss);   // a launch can number that many threads
 hipError_t launch_router(const RouterArgs &a, void *workspace, hipStream_t s);
 hipError_t launch_router_backward(const RouterArgs &a, hipStream_t s);
 

@@ -630,6 +630,14 @@ hipError_t launch_backward_v(const RouterArgs &a, hipStream_t s) {
 
 size_t router_workspace_bytes(const RouterArgs &a) { return loss_workspace(a, loss_shape(a)).bytes; }
 
+bool router_grid_ok(const RouterArgs &a, bool loss) {
+    if (!loss) return static_cast<int64_t>(a.S) * kWave + kRouterWaves * kWave <= kMaxLaunchThreads;
+    const LossShape sh = loss_shape(a);
+    const int v = lane_experts(a.E), waves = v <= 4 ? 16 : 64 / v;
+    return static_cast<int64_t>(a.G) * sh.per_seq * waves * kWave <= kMaxLaunchThreads &&
+           static_cast<int64_t>(a.G) * finish_blocks(a) * kFinishThreads <= kMaxLaunchThreads;
+}
+
 hipError_t launch_router(const RouterArgs &a, void *workspace, hipStream_t s) {
     if (a.E <= 64) return launch_type<1>(a, workspace, s);
     if (a.E <= 128) return launch_type<2>(a, workspace, s);

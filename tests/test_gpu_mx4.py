@@ -107,6 +107,29 @@ def test_quantize_rows_in_use(moe):
         assert np.array_equal(bf16_values(host_bits(out)), np.where(used[:, None], mx4_values(wc, ws), 7.0))
 
 
+@pytest.mark.parametrize("H", [1920, 2048, 7168, 8320, 16640])
+@pytest.mark.parametrize("S,E,rows", [(61, 9, 31), (3, 16, 1), (0, 4, 5)])
+def test_conversions_of_long_rows_in_use(moe, H, S, E, rows):
+    """Rows of less than, exactly and many times a wave's channels; rows that are no multiple of the XCDs; a layout
+    without an entry."""
+    desc = moe.LayoutDesc(S, 2, E, 1, moe.MOE_PAD_CAPACITY, rows)
+    rng = np.random.default_rng(H + S)
+    lay = moe.moe_layout(desc, dev(rng.integers(0, E, (S, 2)).astype(np.int32)))
+    n = E * rows
+    used = lay.src.cpu().numpy()[:n] >= 0
+    assert used.any() == (S > 0)
+    bits = normal_bf16_bits(rng, (n, H))
+    codes = torch.full((n, H // 2), 0x5A, dtype=torch.uint8, device=DEV)
+    scales = torch.full((n, H // 32), 0x5B, dtype=torch.uint8, device=DEV)
+    moe.moe_quantize_mx4(dev_bf16(np.where(used[:, None], bits, 0x7FA5).astype(np.uint16), DEV), codes, scales, layout=lay)
+    wc, ws = mx4_quantize(bf16_values(bits))
+    assert np.array_equal(codes.cpu().numpy(), np.where(used[:, None], wc, 0x5A))
+    assert np.array_equal(scales.cpu().numpy(), np.where(used[:, None], ws, 0x5B))
+    out = torch.full((n, H), 7.0, dtype=torch.bfloat16, device=DEV)
+    moe.moe_dequantize_mx4(codes, scales, out=out, layout=lay)
+    assert np.array_equal(bf16_values(host_bits(out)), np.where(used[:, None], mx4_values(wc, ws), 7.0))
+
+
 def test_quantize_past_4_gib(moe):
     """The last rows of an array whose bytes pass 2^32 (rows repeat, so the reference is small)."""
     H, rows = 7168, 310_000

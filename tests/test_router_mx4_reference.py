@@ -131,10 +131,11 @@ def test_router_refusals(moe):
     for bad in [dict(ok, K=17), dict(ok, K=0), dict(ok, E=1025, K=1), dict(ok, E=0), dict(ok, S=-1), dict(ok, n_groups=3),
                 dict(ok, n_groups=4, topk_groups=5), dict(ok, n_groups=4, topk_groups=0), dict(ok, seq_len=5),
                 dict(ok, seq_len=-1), dict(ok, E=128, n_groups=128), dict(ok, n_groups=0),
-                dict(ok, n_groups=16, topk_groups=1),       # one group of one expert cannot give two picks
                 dict(S=1 << 28, E=16, K=8)]:
         assert call(bad) == moe.MOE_ERR_SHAPE, bad
-        assert call(bad, given=True) == moe.MOE_ERR_SHAPE or bad.get("topk_groups") == 1, bad
+        assert call(bad, given=True) == moe.MOE_ERR_SHAPE, bad
+    # one group of one expert cannot give two picks; a given routing has none to make, so it is not refused
+    assert call(dict(ok, n_groups=16, topk_groups=1)) == moe.MOE_ERR_SHAPE
     assert call(dict(ok, K=16, E=8)) == moe.MOE_ERR_SHAPE   # more picks than experts
     for given in (False, True):
         assert call(kind=2, given=given) == moe.MOE_ERR_SHAPE
@@ -236,3 +237,40 @@ def test_python_checks_refuse_host_tensors(moe):
         moe.moe_router(moe.RouterDesc(4, 8, 2), z)
     with pytest.raises(ValueError):
         moe.moe_quantize_mx4(torch.zeros(2, 128, dtype=torch.bfloat16))
+
+
+def test_launch_limits_are_refused(moe):
+    """A launch numbers at most 2^32 - 1 threads: shapes beyond are refused before anything is enqueued."""
+    L = moe.lib()
+    none = dict(expert_count=None, balance_coef=None, balance_loss=None)
+
+    def route(d, loss):
+        b = _bufs(moe) if loss else _bufs(moe, **none)
+        return L.moe_router(ctypes.byref(d.c()), P(FAKE), 0, None, ctypes.byref(b), P(FAKE), (1 << 62) if loss else 0, None)
+
+    assert route(moe.RouterDesc(1 << 26, 8, 1), False) == moe.MOE_ERR_SHAPE            # a wave per token
+    assert route(moe.RouterDesc(1 << 23, 8, 1, seq_len=1), True) == moe.MOE_ERR_SHAPE  # a workgroup per sequence
+    assert moe.moe_router_workspace_bytes(moe.RouterDesc(1 << 23, 8, 1, seq_len=1)) == 0
+    assert moe.moe_router_workspace_bytes(moe.RouterDesc(1 << 22, 1024, 1, seq_len=4)) == 0
+    d = moe.RouterDesc(1 << 26, 8, 1).c()
+    assert L.moe_router_backward(ctypes.byref(d), P(FAKE), 0, None, P(FAKE), P(FAKE), None, P(FAKE), None, P(FAKE),
+                                 None) == moe.MOE_ERR_SHAPE
+    A = P(FAKE)
+    assert L.moe_quantize_mx4(A, 1 << 31, 128, None, A, A, None) == moe.MOE_ERR_SHAPE
+    assert L.moe_dequantize_mx4(A, A, 1 << 30, 128, None, A, None) == moe.MOE_ERR_SHAPE
+    b = moe.moe_layout_bufs(**{n: FAKE + 4096 * i for i, (n, _) in enumerate(moe.moe_layout_bufs._fields_)})
+    d = moe.LayoutDesc(1 << 26, 1, 8, 1).c()
+    assert L.moe_dispatch_mx4(ctypes.byref(d), ctypes.byref(b), A, 128, None, A, A, None, None) == moe.MOE_ERR_SHAPE
+    d = moe.LayoutDesc(256, 1, 256, 1, moe.MOE_PAD_CAPACITY, 1).c()
+    assert L.moe_expert_gemm_mx4(ctypes.byref(d), ctypes.byref(b), None, 0, A, A, 7168, A, A, 1 << 22, 0, A,
+                                 None) == moe.MOE_ERR_SHAPE
+
+
+@pytest.mark.parametrize("make", [lambda m: m.RouterDesc(8, 8, 2, alpha=0.5), lambda m: m.LayoutDesc(8, 2, 8, 2)])
+def test_descriptors_copy_and_pickle_after_use(moe, make):
+    import copy
+    import pickle
+    d = make(moe)
+    moe._made_once(d)
+    for e in (copy.copy(d), copy.deepcopy(d), pickle.loads(pickle.dumps(d))):
+        assert e == d and hash(e) == hash(d) and "_ref" not in e.__dict__
