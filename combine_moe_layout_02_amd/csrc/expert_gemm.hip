@@ -397,8 +397,19 @@ struct TileLds {
 // the weights' and the tokens' rows, and its row of scales.
 struct TileCopies {
     unsigned int wo, xo, so;
-    int slot;               // the scales' place in LDS
+    int slot;                                 // the scales' place in LDS
+    __amdgpu_buffer_rsrc_t w[2], x, scales;   // this wave's first and last 16 weight rows, the token rows, this wave's scales
+    bool wide;                                // more than 128 token rows
 };
+
+// First weight row of a tile, among all experts', and how many there are.
+template <bool SWIGLU>
+__device__ __forceinline__ size_t first_weight_row(const ExpertGemmArgs &a, const RowTile &t, unsigned int &rows) {
+    constexpr int kOutRows = SWIGLU ? kTileWeights / 2 : kTileWeights;
+    const int n0 = t.ntile * kOutRows;
+    rows = min(kOutRows, a.N - n0);
+    return t.expert * (SWIGLU ? 2 * static_cast<size_t>(a.N) : a.N) + n0;
+}
 
 // Lane l's vector of a copy: row l/8 of the eight, chunk c at place l%8, where
 // chunk c (32 channels) of row q lies at c ^ (q % 8): eight rows' chunk c are
@@ -427,68 +438,53 @@ __device__ __forceinline__ TileCopies tile_copies(const ExpertGemmArgs &a, const
         c.so = n * scales;
         c.slot = kTileRows + (!SWIGLU ? n : (wide ? n / 32 * 64 + (n & 31) + up * 32 : n / 16 * 32 + (n & 15) + up * 16));
     }
+    unsigned int rows;
+    const size_t first = first_weight_row<SWIGLU>(a, t, rows), up_first = first + (SWIGLU ? a.N : 0);
+    c.wide = wide;
+    c.w[0] = buffer_of(a.w + (wide && (wave & 1) ? up_first : first) * half, rows * half);
+    c.w[1] = buffer_of(a.w + (!wide || (wave & 1) ? up_first : first) * half, rows * half);
+    c.x = buffer_of(a.x + static_cast<size_t>(t.row0) * half, t.rows * half);
+    c.scales = wave >= 4 ? buffer_of(a.xs + static_cast<size_t>(t.row0) * scales, t.rows * scales)
+                         : buffer_of(a.ws + (wave >= 2 ? up_first : first) * scales, rows * scales);
     return c;
-}
-
-// First weight row of a tile, among all experts', and how many there are.
-template <bool SWIGLU>
-__device__ __forceinline__ size_t first_weight_row(const ExpertGemmArgs &a, const RowTile &t, unsigned int &rows) {
-    constexpr int kOutRows = SWIGLU ? kTileWeights / 2 : kTileWeights;
-    const int n0 = t.ntile * kOutRows;
-    rows = min(kOutRows, a.N - n0);
-    return t.expert * (SWIGLU ? 2 * static_cast<size_t>(a.N) : a.N) + n0;
 }
 
 // Copies channels 256*s .. of the tile into `stage`.  A last stage of 128
 // channels leaves the second half of each row alone (the offset is past the
-// end there).
-template <bool SWIGLU>
-__device__ __forceinline__ void copy_stage(const ExpertGemmArgs &a, const RowTile &t, const TileCopies &c, int s, u32x4 *stage) {
+// end there).  Rows are told apart by the uniform offset, which counts where a
+// buffer's end is checked: two offsets per lane do for all copies (211 registers
+// instead of 256, 1 % of the time).
+template <bool SWIGLU, int XCOPIES>
+__device__ __forceinline__ void copy_stage(const ExpertGemmArgs &a, const TileCopies &c, int s, u32x4 *stage, bool wide) {
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const unsigned int half = a.H / 2;
-    unsigned int rows;
-    const size_t first = first_weight_row<SWIGLU>(a, t, rows);
-    const bool wide = t.rows > 128;
-    const unsigned int gone = 256 * s + 128 >= a.H && (((lane & 7) ^ (lane / 8)) & 4) ? kPastEnd : 0u;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const bool is_up = SWIGLU && (wide ? (wave & 1) != 0 : i == 1);
-        const auto w = buffer_of(a.w + (first + (is_up ? a.N : 0)) * half, rows * half);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const unsigned int down = (SWIGLU && !wide ? 8 * j : 16 * i + 8 * j) * half;
-            copy_to_lds(w, stage + (kTileRows + wave * 32 + i * 16 + j * 8) * 8, (c.wo + down) | gone, s * 128);
-        }
+    const int half = a.H / 2, at = s * 128;
+    unsigned int wo = c.wo, xo = c.xo;
+    if (256 * s + 128 >= a.H) {
+        const unsigned int gone = ((lane & 7) ^ (lane / 8)) & 4 ? kPastEnd : 0u;
+        wo |= gone;
+        xo |= gone;
     }
-    const auto x = buffer_of(a.x + static_cast<size_t>(t.row0) * half, t.rows * half);
-    const int groups = (t.rows + 15) / 16 * 2;   // token rows, in eights
 #pragma unroll
-    for (int i = 0; i < kTileRows / 8 / kTileWaves; ++i) {
-        const int group = i * kTileWaves + wave;
-        if (group < groups) copy_to_lds(x, stage + group * 64, (c.xo + i * kTileWaves * 8 * half) | gone, s * 128);
-    }
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            copy_to_lds(c.w[i], stage + (kTileRows + wave * 32 + i * 16 + j * 8) * 8, wo,
+                        at + (SWIGLU && !wide ? 8 * j : 16 * i + 8 * j) * half);
+#pragma unroll
+    for (int i = 0; i < XCOPIES; ++i)
+        copy_to_lds(c.x, stage + (i * kTileWaves + wave) * 64, xo, at + i * kTileWaves * 8 * half);
 }
 
 // Scale words 4S .. 4S+3 of this thread's row; those past the row's end are
 // not read.
-template <bool SWIGLU>
-__device__ __forceinline__ u32x4 load_scales(const ExpertGemmArgs &a, const RowTile &t, const TileCopies &c, int S) {
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const unsigned int scales = a.H / kMx4Block;
+__device__ __forceinline__ u32x4 load_scales(const ExpertGemmArgs &a, const TileCopies &c, int S) {
     const int steps = a.H / kStep;
-    unsigned int rows;
-    const size_t first = first_weight_row<SWIGLU>(a, t, rows);
-    const bool tokens = wave >= 4;
-    const uint8_t *base = tokens ? a.xs + static_cast<size_t>(t.row0) * scales
-                                 : a.ws + (first + (SWIGLU && wave >= 2 ? a.N : 0)) * scales;
-    const auto b = buffer_of(base, (tokens ? t.rows : rows) * scales);
-    const unsigned int at = c.so + S * 16;
-    if (4 * S + 4 <= steps) return __builtin_amdgcn_raw_buffer_load_b128(b, static_cast<int>(at), 0, 0);
+    if (4 * S + 4 <= steps) return __builtin_amdgcn_raw_buffer_load_b128(c.scales, static_cast<int>(c.so), S * 16, 0);
     u32x4 d = {0u, 0u, 0u, 0u};
-    d[0] = __builtin_amdgcn_raw_buffer_load_b32(b, static_cast<int>(at), 0, 0);
-    if (4 * S + 1 < steps) d[1] = __builtin_amdgcn_raw_buffer_load_b32(b, static_cast<int>(at + 4), 0, 0);
-    if (4 * S + 2 < steps) d[2] = __builtin_amdgcn_raw_buffer_load_b32(b, static_cast<int>(at + 8), 0, 0);
+    d[0] = __builtin_amdgcn_raw_buffer_load_b32(c.scales, static_cast<int>(c.so), S * 16, 0);
+    if (4 * S + 1 < steps) d[1] = __builtin_amdgcn_raw_buffer_load_b32(c.scales, static_cast<int>(c.so + 4), S * 16, 0);
+    if (4 * S + 2 < steps) d[2] = __builtin_amdgcn_raw_buffer_load_b32(c.scales, static_cast<int>(c.so + 8), S * 16, 0);
     return d;
 }
 
@@ -522,9 +518,12 @@ __device__ __forceinline__ RowTile tile_at(const ExpertGemmArgs &a, const SegTab
 template <int TT, int WT, bool SWIGLU, typename NextFirst>
 __device__ __forceinline__ void run_tile(const ExpertGemmArgs &a, const RowTile &t, const TileCopies &copies, const TileLds &lds,
                                          u32x4 &first_scales, NextFirst &&next_first) {
-    constexpr int kWeightWaves = kTileWeights / (16 * WT);
+    constexpr int kWeightWaves = kTileWeights / (16 * WT), kX = WT == 4 ? 4 : (TT * 2 + kTileWaves - 1) / kTileWaves;
+    constexpr bool kWide = WT == 4;
     constexpr int kOut = SWIGLU ? WT / 2 : WT;                 // 16-channel tiles of output per wave
-    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));   // what follows from it is made once per tile, not kept from tile to tile
+    const int lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int ww = wave % kWeightWaves, q0 = (wave / kWeightWaves) * 128;   // the wave's weight rows and token rows
     const int r = lane & 15, g = lane >> 4;
@@ -535,16 +534,21 @@ __device__ __forceinline__ void run_tile(const ExpertGemmArgs &a, const RowTile 
 #pragma unroll
         for (int i = 0; i < WT; ++i) acc[m][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     unsigned int sca[WT], scb[TT];
+    // Where the lane's operands of either step of a stage and its scales begin:
+    // values of their own, so that every read is one of them and a constant.
+    int wat0 = (kTileRows + ww * WT * 16 + r) * 8 + (g ^ (r & 7)), wat1 = (kTileRows + ww * WT * 16 + r) * 8 + ((4 + g) ^ (r & 7));
+    int xat0 = (q0 + r) * 8 + (g ^ (r & 7)), xat1 = (q0 + r) * 8 + ((4 + g) ^ (r & 7));
+    int wsat = (kTileRows + ww * WT * 16 + r) * 4 + g, xsat = (q0 + r) * 4 + g;
+    asm volatile("" : "+v"(wat0), "+v"(wat1), "+v"(xat0), "+v"(xat1), "+v"(wsat), "+v"(xsat));
     // Step h of a stage, the stage's byte b0 + h of the scales' words.
     const auto products = [&](const u32x4 *stage, auto byte_, int h) {
         constexpr int byte = decltype(byte_)::value;
-        const int at = (h * 4 + g) ^ (r & 7);
         u32x4 wv[WT];
 #pragma unroll
-        for (int i = 0; i < WT; ++i) wv[i] = stage[(kTileRows + ww * WT * 16 + i * 16 + r) * 8 + at];
+        for (int i = 0; i < WT; ++i) wv[i] = stage[(h ? wat1 : wat0) + i * 128];
 #pragma unroll
         for (int m = 0; m < TT; ++m) {
-            const u32x4 b = stage[(q0 + m * 16 + r) * 8 + at];
+            const u32x4 b = stage[(h ? xat1 : xat0) + m * 128];
 #pragma unroll
             for (int i = 0; i < WT; ++i)
                 acc[m][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fp4_operand(wv[i]), fp4_operand(b), acc[m][i], kFp4,
@@ -562,19 +566,19 @@ __device__ __forceinline__ void run_tile(const ExpertGemmArgs &a, const RowTile 
     barrier_after<0>();                                        // stage 0 has arrived
     for (int s = 0; s < stages; s += 2) {
         const bool second = s + 1 < stages, more = s + 2 < stages;
-        if (second) copy_stage<SWIGLU>(a, t, copies, s + 1, lds.stage1);
+        if (second) copy_stage<SWIGLU, kX>(a, copies, s + 1, lds.stage1, kWide);
         u32x4 next_scales = {0u, 0u, 0u, 0u};
-        if (more) next_scales = load_scales<SWIGLU>(a, t, copies, s / 2 + 1);
+        if (more) next_scales = load_scales(a, copies, s / 2 + 1);
         const unsigned int *p = reinterpret_cast<const unsigned int *>(lds.scale);
 #pragma unroll
-        for (int i = 0; i < WT; ++i) sca[i] = p[(kTileRows + ww * WT * 16 + i * 16 + r) * 4 + g];
+        for (int i = 0; i < WT; ++i) sca[i] = p[wsat + i * 64];
 #pragma unroll
-        for (int m = 0; m < TT; ++m) scb[m] = p[(q0 + m * 16 + r) * 4 + g];
+        for (int m = 0; m < TT; ++m) scb[m] = p[xsat + m * 64];
         products(lds.stage0, std::integral_constant<int, 0>{}, 0);
         if (2 * s + 1 < steps) products(lds.stage0, std::integral_constant<int, 1>{}, 1);
         barrier_after<0>();                                    // stage s + 1 has arrived, stage s and its scales are free
         if (more)
-            copy_stage<SWIGLU>(a, t, copies, s + 2, lds.stage0);
+            copy_stage<SWIGLU, kX>(a, copies, s + 2, lds.stage0, kWide);
         else
             next_first();
         if (second) {
@@ -666,19 +670,22 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_expert_tile(ExpertGemmArgs 
     if (tile >= total) return;                                 // the same for every wave
     const TileLds lds{stage0, stage1, scale, &segs};
     RowTile t = tile_at(a, segs, tile, tiles_n);
-    TileCopies copies = tile_copies<SWIGLU>(a, t);
-    u32x4 scales = load_scales<SWIGLU>(a, t, copies, 0);
-    copy_stage<SWIGLU>(a, t, copies, 0, stage0);
+    u32x4 scales;
+    {
+        const TileCopies c = tile_copies<SWIGLU>(a, t);
+        scales = load_scales(a, c, 0);
+        copy_stage<SWIGLU, 4>(a, c, 0, stage0, c.wide);
+    }
     while (true) {
         const int next = tile + kCus;                          // below INT32_MAX: the grid's check leaves room
+        const TileCopies copies = tile_copies<SWIGLU>(a, t);
         RowTile nt{};
-        TileCopies nc{};
         const auto next_first = [&]() {
             if (next >= total) return;
             nt = tile_at(a, segs, next, tiles_n);
-            nc = tile_copies<SWIGLU>(a, nt);
-            scales = load_scales<SWIGLU>(a, nt, nc, 0);
-            copy_stage<SWIGLU>(a, nt, nc, 0, stage0);
+            const TileCopies nc = tile_copies<SWIGLU>(a, nt);
+            scales = load_scales(a, nc, 0);
+            copy_stage<SWIGLU, 4>(a, nc, 0, stage0, nc.wide);
         };
         if (t.rows > 128)
             run_tile<8, 4, SWIGLU>(a, t, copies, lds, scales, next_first);
@@ -691,7 +698,6 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_expert_tile(ExpertGemmArgs 
         if (next >= total) return;
         tile = next;
         t = nt;
-        copies = nc;
     }
 }
 

@@ -312,7 +312,9 @@ typedef struct {
 } moe_router_bufs;
 
 /* Device workspace bytes of moe_router (when it writes the loss) and of
- * moe_balance_loss.  Host only; 0 for an invalid shape. */
+ * moe_balance_loss.  Host only; 0 for an invalid shape.  Its contents carry
+ * nothing from call to call, but calls (or graph replays) that may overlap in
+ * time need a workspace, and outputs, each. */
 size_t moe_router_workspace_bytes(const moe_router_desc *desc);
 
 /* Router: top-k routing of one batch (the gate in front of the layout), in the
@@ -337,7 +339,9 @@ size_t moe_router_workspace_bytes(const moe_router_desc *desc);
  * A counting token with a NaN or +inf logit is not routed (picks -1, weights
  * 0), and its probabilities are NaN: so is the loss, and its row of the
  * gradient.  The results do not depend on the order in which work runs.
- * No alignment beyond the element types' is needed; workspace 16 bytes. */
+ * No alignment beyond the element types' is needed; workspace 16 bytes.  Fewer
+ * than 2^26 - 4 tokens, and with the loss sequences * ceil(E/32) < 2^22; else
+ * MOE_ERR_SHAPE. */
 moe_status moe_router(const moe_router_desc *desc, const void *logits, int32_t logits_type, const uint8_t *token_mask,
                       const moe_router_bufs *out, void *workspace, size_t workspace_bytes, void *stream);
 
