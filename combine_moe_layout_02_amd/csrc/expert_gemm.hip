@@ -352,7 +352,13 @@ __global__ __launch_bounds__(kStreamWaves * kWave, 4) void k_expert_stream(Exper
 // Measured at the prompt case (98304 rows, 64 experts, H = 2048, 2 x 1280
 // weight rows, SwiGLU): weights straight to registers 396 us; 128 x 256 tiles
 // of four waves, two workgroups per CU, one step per stage, three stages deep
-// 336 us; this 321 us.
+// 336 us; this 317 us (3.3 PFLOP/s).  In copies that leave parts out: no stage
+// copies 251, no LDS reads 295, no stores 281, products and barriers alone 170,
+// stage copies alone 213.  A stage's copies take about 1.4 us with one stage in
+// flight (a quarter of their lines come from beyond the L2), its products 1.1 us,
+// and LDS holds no third stage; nothing runs beside a tile's stores.  Asking the
+// L2 for lines one to three stages ahead (332 and more), reading operands across
+// the barriers (330) and raising the waves' priority (320) did not help.
 constexpr int kTileRows = 256;
 constexpr int kTileWeights = 256;
 constexpr int kTileWaves = 8;
