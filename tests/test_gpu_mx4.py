@@ -303,7 +303,8 @@ def test_product_any_scale(moe, S, act):
 
 
 @pytest.mark.parametrize("S,K,E,R,B,H,N", [(40, 2, 8, 4, 2, 256, 40), (600, 4, 16, 4, 6, 384, 136), (700, 2, 24, 2, 0, 128, 64),
-                                           (9000, 4, 12, 3, 8, 256, 72)])
+                                           (9000, 4, 12, 3, 8, 256, 72), (500, 2, 1024, 8, 64, 128, 16),
+                                           (9000, 8, 1024, 8, 64, 384, 264)])
 def test_product_balanced(moe, S, K, E, R, B, H, N):
     """Rows of a replica slot use the weights of the expert in it."""
     rng = np.random.default_rng(S)
@@ -446,6 +447,53 @@ def test_layer(moe, case):
     got = host_bits(out)
     assert np.array_equal(got, oracle.combine(ybits, buf.layout.pos.cpu().numpy(), r.topk_w.cpu().numpy()))
     assert not got[140:].any()                           # tokens that do not count
+
+
+def test_layer_in_graphs(moe):
+    """The layer of two micro-batches, each captured into a graph of its own, replayed in turn and at the same time
+    with new tokens and weights, eager work between: every replay as the eager calls."""
+    S, H, K, E, R, F = 130, 384, 3, 12, 3, 128
+    rng = np.random.default_rng(78)
+    rd = moe.RouterDesc(S, E, K, n_groups=3, topk_groups=2, seq_len=65, alpha=0.1)
+    up = moe.moe_quantize_mx4(dev_bf16(normal_bf16_bits(rng, (E * 2 * F, H)).reshape(E, 2 * F, H), DEV).mul_(2.0 ** -5))
+    down = moe.moe_quantize_mx4(dev_bf16(normal_bf16_bits(rng, (E * H, F)).reshape(E, H, F), DEV).mul_(2.0 ** -4))
+
+    def layer(buf, z, hid):
+        r = moe.moe_router(rd, z)
+        buf.dispatch(hid, r.topk_w, r.topk_idx)
+        h = buf.expert_gemm(*up, act=moe.MOE_ACT_SWIGLU)
+        h4 = moe.moe_quantize_mx4(h, layout=buf.layout)
+        out = buf.combine(buf.expert_gemm(*down, x=h4[0], x_scales=h4[1]), r.topk_w)
+        d = moe.moe_router_backward(rd, z, r, d_topk_w=torch.ones_like(r.topk_w), d_loss=torch.ones(1, device=DEV))
+        return out, r.topk_idx, r.topk_w, r.expert_count, r.balance_loss, d
+
+    def fresh():
+        return dev(rng.standard_normal((S, E)).astype(np.float32)), dev_bf16(normal_bf16_bits(rng, (S, H)), DEV)
+
+    bufs = [moe.Buffer(S=S, H=H, K=K, E=E, R=R, mx4=True, device=DEV) for _ in range(3)]
+    ins = [fresh(), fresh()]
+    layer(bufs[2], *ins[0])
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for b, i in zip(bufs, ins):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(layer(b, *i))
+        graphs.append(g)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for k in range(4):
+        want = []
+        for i in ins:
+            for t, n in zip(i, fresh()):
+                t.copy_(n)
+            want.append([t.clone() for t in layer(bufs[2], *i)])
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):                # at the same time, or one behind the other
+            with torch.cuda.stream(s if k % 2 else streams[0]):
+                g.replay()
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert all(torch.equal(a, b) for a, b in zip(o, w)), k
 
 
 def router_rows(z, K, mask):

@@ -317,6 +317,30 @@ def test_autograd(moe):
     assert torch.equal(count, r.expert_count)
 
 
+def test_autograd_twice_and_not_at_all(moe, monkeypatch):
+    """A graph walked twice, gradients that add up, leaves that need none, and a backward pass under capture."""
+    z = torch.randn((33, 24), generator=torch.Generator().manual_seed(31)).to(DEV)
+    desc = moe.RouterDesc(33, 24, 3, alpha=2.0)
+    r = moe.moe_router(desc, z)
+    once = moe.moe_router_backward(desc, z, r, torch.ones_like(r.topk_w), torch.ones(1, device=DEV))
+    leaf = z.clone().requires_grad_()
+    _, w, loss, _ = moe.router(desc, leaf)
+    total = w.sum() + loss                                # the sum's gradient comes expanded, not contiguous
+    total.backward(retain_graph=True)
+    assert torch.equal(leaf.grad, once)
+    total.backward(retain_graph=True)
+    assert torch.equal(leaf.grad, once + once)
+    with monkeypatch.context() as m:
+        m.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+        with pytest.raises(RuntimeError, match="captured"):
+            total.backward()
+    with torch.no_grad():
+        _, w, loss, _ = moe.router(desc, leaf)
+    assert not w.requires_grad and not loss.requires_grad
+    _, w, loss, _ = moe.router(desc, z)
+    assert not w.requires_grad and not loss.requires_grad
+
+
 def test_python_refusals(moe):
     z = torch.zeros((4, 8), device=DEV)
     desc = moe.RouterDesc(4, 8, 2)

@@ -274,3 +274,12 @@ def test_descriptors_copy_and_pickle_after_use(moe, make):
     moe._made_once(d)
     for e in (copy.copy(d), copy.deepcopy(d), pickle.loads(pickle.dumps(d))):
         assert e == d and hash(e) == hash(d) and "_ref" not in e.__dict__
+
+
+def test_autograd_functions_refuse_capture(moe, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    desc, z = moe.RouterDesc(4, 8, 2), torch.zeros(4, 8)
+    with pytest.raises(RuntimeError, match="captured"):
+        moe.router(desc, z)
+    with pytest.raises(RuntimeError, match="captured"):
+        moe.balance_loss(desc, z, torch.zeros(4, 2, dtype=torch.int32))
