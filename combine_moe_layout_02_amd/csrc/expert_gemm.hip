@@ -352,7 +352,7 @@ __global__ __launch_bounds__(kStreamWaves * kWave, 4) void k_expert_stream(Exper
 // Measured at the prompt case (98304 rows, 64 experts, H = 2048, 2 x 1280
 // weight rows, SwiGLU): weights straight to registers 396 us; 128 x 256 tiles
 // of four waves, two workgroups per CU, one step per stage, three stages deep
-// 336 us; this 317 us (3.3 PFLOP/s).  In copies that leave parts out: no stage
+// 336 us; this 309 us (3.3 PFLOP/s).  In copies that leave parts out: no stage
 // copies 251, no LDS reads 295, no stores 281, products and barriers alone 170,
 // stage copies alone 213.  A stage's copies take about 1.4 us with one stage in
 // flight (a quarter of their lines come from beyond the L2), its products 1.1 us,
@@ -389,7 +389,7 @@ __device__ __forceinline__ void barrier_after() {
     asm volatile("" ::: "memory");
 }
 
-// Segments with the number of row tiles before each.
+// Segments with the number of tiles before each (row tiles by weight tiles).
 struct SegTable {
     int before[kMaxSegments + 1], first[kMaxSegments], rows[kMaxSegments];
 };
@@ -494,20 +494,29 @@ __device__ __forceinline__ u32x4 load_scales(const ExpertGemmArgs &a, const Tile
     return d;
 }
 
-// Row tile number `row_tile` from the table; every lane calls it.
-__device__ __forceinline__ RowTile tile_at(const ExpertGemmArgs &a, const SegTable &segs, int tile, int tiles_n) {
+// Tile number `tile` from the table; every lane calls it.
+__device__ __forceinline__ RowTile tile_at(const ExpertGemmArgs &a, const SegTable &segs, int tile) {
     const int lane = threadIdx.x & (kWave - 1);
-    const int row_tile = tile / tiles_n, per = (a.nseg + kWave - 1) / kWave;
-    // the last lane, then the last of its segments, with at most row_tile tiles before it
+    const int per = (a.nseg + kWave - 1) / kWave;
+    // the last lane, then the last of its segments, with at most `tile` tiles before it
     int from = segs.before[min(lane * per, a.nseg)];
-    const int owner = kWave - 1 - __builtin_clzll(__ballot(from <= row_tile && lane * per < a.nseg));
+    const int owner = kWave - 1 - __builtin_clzll(__ballot(from <= tile && lane * per < a.nseg));
     const int i = owner * per + lane;
     from = segs.before[min(i, a.nseg)];
-    const int seg = owner * per + kWave - 1 - __builtin_clzll(__ballot(lane < per && i < a.nseg && from <= row_tile));
+    const int seg = owner * per + kWave - 1 - __builtin_clzll(__ballot(lane < per && i < a.nseg && from <= tile));
     const int n = __builtin_amdgcn_readfirstlane(segs.rows[seg]), before = __builtin_amdgcn_readfirstlane(segs.before[seg]);
-    const int seg_tiles = (n + kTileRows - 1) / kTileRows, local = tile - before * tiles_n, m = local % seg_tiles;
+    // local / seg_tiles is the weight tile's number, below 2^15: the estimate is within one
+    const int seg_tiles = (n + kTileRows - 1) / kTileRows, local = tile - before;
     RowTile t;
-    t.ntile = local / seg_tiles;
+    t.ntile = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<float>(local) * __builtin_amdgcn_rcpf(static_cast<float>(seg_tiles))));
+    int m = local - t.ntile * seg_tiles;
+    if (m < 0) {
+        t.ntile -= 1;
+        m += seg_tiles;
+    } else if (m >= seg_tiles) {
+        t.ntile += 1;
+        m -= seg_tiles;
+    }
     t.rows = min(kTileRows, n - m * kTileRows);
     t.row0 = __builtin_amdgcn_readfirstlane(segs.first[seg]) + m * kTileRows;
     t.expert = seg;
@@ -659,36 +668,52 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_expert_tile(ExpertGemmArgs 
     for (int j = 0; j < kPer; ++j) {
         const int i = tid * kPer + j;
         if (i < a.nseg) {
-            segs.before[i] = at;
+            segs.before[i] = at * tiles_n;
             segs.first[i] = first[j];
             segs.rows[i] = n[j];
         }
         at += (n[j] + kTileRows - 1) / kTileRows;
     }
-    if (tid == 0) segs.before[a.nseg] = all.x;
+    if (tid == 0) segs.before[a.nseg] = all.x * tiles_n;
     __syncthreads();
-    // Runs of neighbouring tiles go to the workgroups of one XCD, whose L2 then
-    // serves the tiles' common weights and tokens.
+    // Rounds of kCus tiles.  Runs of neighbouring tiles go to the workgroups of one
+    // XCD, whose L2 then serves the tiles' common weights and tokens.  Where the
+    // last round has at most a half or a quarter of them, its tiles are taken in
+    // two or four parts of 128 or 64 token rows.  Measured without / with (us; E
+    // experts, about m rows each): E=8 H=7168 N=2048 m=128 48 / 30, m=256 49 / 37,
+    // m=1024 112 / 98; E=64 H=2048 N=1408 m=256 58 / 53; E=32 H=5120 N=1536 m=700
+    // 133 / 126.
     const int total = __builtin_amdgcn_readfirstlane(all.x) * tiles_n;
-    const int run = min(kCus / kXcds, (total + kXcds - 1) / kXcds);
-    const int place = static_cast<int>(blockIdx.x) / kXcds;
-    int tile = place < run ? (static_cast<int>(blockIdx.x) % kXcds) * run + place : total;
-    if (tile >= total) return;                                 // the same for every wave
+    const int whole = total / kCus * kCus, rest = total - whole;
+    const int halvings = rest * 4 <= kCus ? 2 : (rest * 2 <= kCus ? 1 : 0), items = whole + (rest << halvings);
+    const int place = static_cast<int>(blockIdx.x) / kXcds, xcd = static_cast<int>(blockIdx.x) % kXcds;
+    // What this workgroup takes in a round; false: nothing, then or later.
+    const auto tile_of = [&](int round, RowTile &t) {
+        const int left = min(items - round * kCus, kCus), run = (left + kXcds - 1) / kXcds, at = xcd * run + place;
+        if (place >= run || at >= left) return false;
+        const int item = round * kCus + at, cut = item < whole ? 0 : halvings;
+        t = tile_at(a, segs, item - (cut ? item - whole - ((item - whole) >> cut) : 0));
+        const int part_rows = kTileRows >> cut, skip = cut ? (((item - whole) & ((1 << cut) - 1)) * part_rows) : 0;
+        t.row0 += skip;
+        t.rows = __builtin_amdgcn_readfirstlane(min(t.rows - skip, part_rows));
+        return t.rows > 0;
+    };
     const TileLds lds{stage0, stage1, scale, &segs};
-    RowTile t = tile_at(a, segs, tile, tiles_n);
+    RowTile t;
+    if (!tile_of(0, t)) return;                                // the same for every wave
     u32x4 scales;
     {
         const TileCopies c = tile_copies<SWIGLU>(a, t);
         scales = load_scales(a, c, 0);
         copy_stage<SWIGLU, 4>(a, c, 0, stage0, c.wide);
     }
-    while (true) {
-        const int next = tile + kCus;                          // below INT32_MAX: the grid's check leaves room
+    for (int round = 1;; ++round) {
         const TileCopies copies = tile_copies<SWIGLU>(a, t);
         RowTile nt{};
+        bool more = false;
         const auto next_first = [&]() {
-            if (next >= total) return;
-            nt = tile_at(a, segs, next, tiles_n);
+            more = tile_of(round, nt);
+            if (!more) return;
             const TileCopies nc = tile_copies<SWIGLU>(a, nt);
             scales = load_scales(a, nc, 0);
             copy_stage<SWIGLU, 4>(a, nc, 0, stage0, nc.wide);
@@ -701,8 +726,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_expert_tile(ExpertGemmArgs 
             run_tile<4, 2, SWIGLU>(a, t, copies, lds, scales, next_first);
         else
             run_tile<2, 2, SWIGLU>(a, t, copies, lds, scales, next_first);
-        if (next >= total) return;
-        tile = next;
+        if (!more) return;
         t = nt;
     }
 }
@@ -714,27 +738,33 @@ int64_t most_tiles(const ExpertGemmArgs &a, int BM) {
 }
 
 // The rule between the two kernels: the sooner by these estimates, in
-// microseconds, which hold what was measured within about a fifth.
-//   stream: a workgroup's work is one 16-row tile by 32 weight rows, with about 6
-//     steps' worth of its own start and end; 3200 such steps a microsecond, or
-//     the weights at 6.0 TB/s.
-//   tile: a start of 6 us, then each round of 256 workgroups one tile, 0.4 us a
-//     step for few rows to 0.8 us for 128 and more; or the weights at 4.9 TB/s.
+// microseconds, which near the crossing hold what was measured within about a
+// fifth.  Experts with a row: as many as a routing at random leaves with one.
+//   stream: a start of 4 us; a workgroup's work is one 16-row tile by 32 weight
+//     rows, with about 7 steps' worth of its own start and end; 3200 such steps a
+//     microsecond, or the weights at 6.0 TB/s.
+//   tile: a start of 6 us, then rounds of 256 workgroups one tile each, 0.38 us a
+//     step and 0.0015 more for each row of a tile, or of a part of it in the last
+//     round; or the weights at 5.2 TB/s.
 // Measured, stream / tile (us; E experts with m rows each, M weight rows):
-//   E=256 H=7168 M=2048  m=1 214 / 257   m=4 338 / 400   m=8 374 / 406   m=12 445 / 411
-//   E=256 H=2048 M=7168  m=4 421 / 391   m=16 644 / 438
-//   E=64  H=1024 M=4096  m=1 23 / 19     m=12 44 / 30
-//   E=64  H=2048 M=2048  m=1 20 / 21     m=12 33 / 27
-//   E=8   H=7168 M=2048  m=32 26 / 30    m=64 41 / 34    m=256 134 / 51
-//   E=4   H=7168 M=512   m=256 24 / 49
+//   E=256 H=7168 M=2048  m=1 218 / 279   m=4 328 / 384   m=8 362 / 391   m=12 428 / 396
+//   E=256 H=2048 M=7168  m=1 288 / 233   m=4 422 / 391   m=16 645 / 415
+//   E=64  H=1024 M=4096  m=1 25 / 21     m=12 48 / 34
+//   E=64  H=2048 M=2048  m=1 20 / 26     m=4 34 / 32     m=12 38 / 33
+//   E=8   H=7168 M=2048  m=4 14 / 28     m=32 26 / 29    m=64 42 / 30    m=256 134 / 38
+//   E=4   H=7168 M=512   m=128 16 / 28   m=256 24 / 29
 bool long_segments(const ExpertGemmArgs &a) {
-    const double used = static_cast<double>(std::min<int64_t>(a.nseg, a.entries)), rows = static_cast<double>(a.entries);
-    if (used == 0) return false;
+    if (a.entries == 0) return false;
+    const double rows = static_cast<double>(a.entries), used = std::max(1.0, a.nseg * -std::expm1(-rows / a.nseg));
     const double M = a.swiglu ? 2.0 * a.N : a.N, steps = a.H / kStep, weights = used * M * a.H * (17.0 / 32.0);
-    const double stream_tiles = std::max(used, rows / kStreamRows + used / 2), tiles = std::max(used, rows / kTileRows + used / 2);
-    const double stream = std::max(stream_tiles * (M / (16 * kWTiles)) * (steps + 6) / 3200, weights / 6.0e6);
-    const double rounds = std::ceil(tiles * std::ceil(M / kTileWeights) / kCus), step_us = 0.4 + 0.4 * std::min(1.0, rows / used / 128);
-    return std::max(6 + rounds * steps * step_us, weights / 4.9e6) < stream;
+    const double stream_tiles = std::max(used, rows / kStreamRows + used / 2), row_tiles = std::max(used, rows / kTileRows + used / 2);
+    const double stream = 4 + std::max(stream_tiles * (M / (16 * kWTiles)) * (steps + 7) / 3200, weights / 6.0e6);
+    const double tiles = row_tiles * std::ceil(M / kTileWeights), whole = std::floor(tiles / kCus), rest = tiles - whole * kCus;
+    const double last_rows = rest * 4 <= kCus ? kTileRows / 4 : (rest * 2 <= kCus ? kTileRows / 2 : kTileRows);
+    const auto step_us = [](double tile_rows) { return 0.38 + 0.0015 * tile_rows; };
+    const double tile_rows = std::min(rows / used, static_cast<double>(kTileRows));
+    const double rounds_us = whole * step_us(tile_rows) + (rest > 0 ? step_us(std::min(tile_rows, last_rows)) : 0);
+    return 6 + std::max(steps * rounds_us, weights / 5.2e6) < stream;
 }
 
 struct Grid {
@@ -749,7 +779,7 @@ Grid grid_of(const ExpertGemmArgs &a) {
     g.tiles_n = (a.N + out - 1) / out;
     const int64_t all = most_tiles(a, tiles ? kTileRows : kStreamRows) * g.tiles_n;
     g.tiles = (all + kXcds - 1) / kXcds * kXcds;
-    g.blocks = tiles ? std::min<int64_t>(g.tiles, kCus) : g.tiles;
+    g.blocks = tiles ? std::min<int64_t>(4 * g.tiles, kCus) : g.tiles;   // a tile may be taken in four parts
     return g;
 }
 

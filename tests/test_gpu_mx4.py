@@ -248,6 +248,9 @@ PRODUCTS = [
     (700, 1, 5, 5, 128, 200, PAD_MULTIPLE, 64),
     (1500, 4, 6, 2, 768, 384, PAD_NONE, 0),
     (2000, 2, 300, 4, 512, 272, PAD_MULTIPLE, 8),
+    # more tiles than one round of workgroups, and a last round of few
+    (30000, 1, 10, 1, 128, 520, PAD_NONE, 0),
+    (9000, 3, 7, 1, 256, 776, PAD_NONE, 0),
 ]
 
 
