@@ -532,14 +532,14 @@ def alloc_router(desc: RouterDesc, device, picks: bool = True, loss: bool = True
     empty, i32, f32 = torch.empty, torch.int32, torch.float32
     idx = w = count = coef = value = ws = None
     if picks:
-        idx = empty((desc.S, desc.K), dtype=i32, device=device)
-        w = empty((desc.S, desc.K), dtype=f32, device=device)
+        idx = empty(desc.S, desc.K, dtype=i32, device=device)   # sizes one by one: a tuple takes longer to parse
+        w = empty(desc.S, desc.K, dtype=f32, device=device)
     if loss:
         need = moe_router_workspace_bytes(desc)
         if need == 0:
             raise MoeError(MOE_ERR_SHAPE, "alloc_router")
-        cells = (desc.sequences, desc.E)
-        count, coef = empty(cells, dtype=i32, device=device), empty(cells, dtype=f32, device=device)
+        G, E = desc.sequences, desc.E
+        count, coef = empty(G, E, dtype=i32, device=device), empty(G, E, dtype=f32, device=device)
         value, ws = empty(1, dtype=f32, device=device), empty(need, dtype=torch.uint8, device=device)
     return Router(idx, w, count, coef, value, ws)
 
@@ -740,11 +740,11 @@ def moe_quantize_mx4(x: torch.Tensor, codes=None, scales=None, layout: Optional[
     lead = x.shape[:-1]
     with _alloc_on(stream):
         if codes is None:
-            codes = torch.empty((*lead, H // 2), dtype=torch.uint8, device=dev)
+            codes = torch.empty(*lead, H // 2, dtype=torch.uint8, device=dev)
         else:
             _check(codes, "codes", torch.uint8, (*lead, H // 2), dev)
         if scales is None:
-            scales = torch.empty((*lead, H // 32), dtype=torch.uint8, device=dev)
+            scales = torch.empty(*lead, H // 32, dtype=torch.uint8, device=dev)
         else:
             _check(scales, "scales", torch.uint8, (*lead, H // 32), dev)
     with _on_device(dev):
@@ -765,7 +765,7 @@ def moe_dequantize_mx4(codes: torch.Tensor, scales: torch.Tensor, out=None, layo
     src = _check_src(layout, rows, dev)
     if out is None:
         with _alloc_on(stream):
-            out = torch.empty((*codes.shape[:-1], H), dtype=torch.bfloat16, device=dev)
+            out = torch.empty(*codes.shape[:-1], H, dtype=torch.bfloat16, device=dev)
     else:
         _check(out, "out", torch.bfloat16, (*codes.shape[:-1], H), dev)
     with _on_device(dev):
@@ -788,9 +788,9 @@ def moe_dispatch_mx4(desc: LayoutDesc, layout: Layout, hidden: torch.Tensor, top
     _check(layout.pos, "layout.pos", torch.int32, (desc.S, desc.K), dev)
     with _alloc_on(stream):
         if recv is None:
-            recv = torch.empty((rows, H // 2), dtype=torch.uint8, device=dev)
+            recv = torch.empty(rows, H // 2, dtype=torch.uint8, device=dev)
         if recv_scales is None:
-            recv_scales = torch.empty((rows, H // 32), dtype=torch.uint8, device=dev)
+            recv_scales = torch.empty(rows, H // 32, dtype=torch.uint8, device=dev)
         if recv_w is None and topk_w is not None:
             recv_w = torch.empty(rows, dtype=torch.float32, device=dev)
     _check_mx4(recv, recv_scales, ("recv", "recv_scales"), rows, H, dev)
@@ -834,7 +834,7 @@ def moe_expert_gemm_mx4(desc: LayoutDesc, layout: Layout, x: torch.Tensor, x_sca
         _check(balance.slot_expert, "balance.slot_expert", torch.int32, (max(desc.R * slots_per_rank, 1),), dev)
     if out is None:
         with _alloc_on(stream):
-            out = torch.empty((rows, N), dtype=torch.bfloat16, device=dev)
+            out = torch.empty(rows, N, dtype=torch.bfloat16, device=dev)
     _check(out, "out", torch.bfloat16, None, dev)
     if out.dim() != 2 or out.shape[1] != N or out.shape[0] < rows:
         raise ValueError(f"out: shape {tuple(out.shape)}, expected [at least {rows}, {N}]")
