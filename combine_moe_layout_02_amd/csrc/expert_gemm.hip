@@ -141,10 +141,13 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, un
 
 typedef __attribute__((address_space(3))) void lds_void;
 
-// Copies 16 bytes per lane to 1 KiB of LDS from `to` (the same in every lane).
+// Copies 16 bytes per lane to 1 KiB of LDS at `to` (the same in every lane).
+// ONCE: past the caches (non-temporal).
+constexpr int kNonTemporal = 2;
+template <bool ONCE = false>
 __device__ __forceinline__ void copy_to_lds(__amdgpu_buffer_rsrc_t b, u32x4 *to, unsigned int offset, int uniform_offset) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(b, reinterpret_cast<lds_void *>(reinterpret_cast<uintptr_t>(to)), 16,
-                                             static_cast<int>(offset), uniform_offset, 0, 0);
+                                             static_cast<int>(offset), uniform_offset, 0, ONCE ? kNonTemporal : 0);
 }
 
 // Orders the wave's own LDS accesses; nothing else uses the memory between.
@@ -166,17 +169,18 @@ __device__ __forceinline__ void wave_lds_fence() {
 // multiplied, four workgroups of four such waves per CU.  (The operands' own
 // order, straight to registers, asks for 64 pieces of 16 bytes per instruction:
 // 432 us at the decode case, 1024 rows of 256 experts, H = 7168, 2 x 1024 weight
-// rows, against 328 us = 6.0 TB/s here; 64 weight rows and two workgroups per CU
-// took 350 us, two waves of 32 rows 339, one 348, eight 395.)  The wave's channels' weight scales come
-// in parts of 8 units; tokens and their scales, few and shared by every
-// workgroup of the segment, go straight to registers.
+// rows, against 328 us here, 306 = 6.4 TB/s past the caches; 64 weight rows and two
+// workgroups per CU took 350 us, two waves of 32 rows 339, one 348, eight 395.)
+// The wave's channels' weight scales come in parts of 8 units; tokens and their
+// scales, few and shared by every workgroup of the segment, go straight to
+// registers.
 constexpr int kStreamRows = 16;
 constexpr int kStreamWaves = 4;
 constexpr int kWTiles = 2;         // 16-row weight tiles (SWIGLU: half gate, half up)
 constexpr int kUnitVecs = kWTiles * 16 * 8;
 constexpr int kPartUnits = 8;      // units whose scales are in LDS
 
-template <bool SWIGLU>
+template <bool SWIGLU, bool ONCE>
 __global__ __launch_bounds__(kStreamWaves * kWave, 4) void k_expert_stream(ExpertGemmArgs a, int tiles_n) {
     constexpr int kOutTiles = SWIGLU ? kWTiles / 2 : kWTiles;
     __shared__ u32x4 unit0[kStreamWaves][kUnitVecs], unit1[kStreamWaves][kUnitVecs];
@@ -213,7 +217,7 @@ __global__ __launch_bounds__(kStreamWaves * kWave, 4) void k_expert_stream(Exper
         for (int j = 0; j < kWTiles * 2; ++j) {
             const int row = 8 * j;
             const bool is_up = row >= kOutTiles * 16;
-            copy_to_lds(is_up ? w_up : w_gate, to + row * 8, (wo + (is_up ? row - kOutTiles * 16 : row) * half) | gone, u * 128);
+            copy_to_lds<ONCE>(is_up ? w_up : w_gate, to + row * 8, (wo + (is_up ? row - kOutTiles * 16 : row) * half) | gone, u * 128);
         }
     };
     // Scale words of 8 units from u0: row 16*i + lane/4, words 4*(lane%4) .. +3;
@@ -610,7 +614,9 @@ __device__ __forceinline__ void run_tile(const ExpertGemmArgs &a, const RowTile 
     // tiles at a time pass through LDS (4 KB of the wave's own) so that a store
     // instruction writes runs of whole rows.  Rows of kChunks 16-byte chunks,
     // chunk c of row q at c ^ turn(q), against bank conflicts.  Stores outside
-    // the tile's rows fall past the buffer's end, those past N are sent there.
+    // the tile's rows fall past the buffer's end, those past N are sent there.  They
+    // pass the caches: 470 MB of results 584 -> 573 us, 268 MB with the quantise
+    // behind it 230 -> 214, 46 MB or less with it 1 % more.
     constexpr int kChunks = 2 * kOut, kRowsPerStore = kWave / kChunks;
     const auto turn = [](int q) { return (q * kChunks / 8) & (kChunks - 1); };
     const unsigned int row_bytes = static_cast<unsigned int>(a.N) * 2u;
@@ -639,7 +645,7 @@ __device__ __forceinline__ void run_tile(const ExpertGemmArgs &a, const RowTile 
             const u32x4 v = mine[q * kChunks + (c ^ turn(q))];
             const int n = n0 + c * 8;
             const unsigned int at = n < a.N ? (q0 + m0 * 16 + q) * row_bytes + 2u * n : kPastEnd;
-            __builtin_amdgcn_raw_buffer_store_b128(v, ob, static_cast<int>(at), 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b128(v, ob, static_cast<int>(at), 0, kNonTemporal);
         }
         wave_lds_fence();
     }
@@ -737,28 +743,40 @@ int64_t most_tiles(const ExpertGemmArgs &a, int BM) {
     return std::min(a.entries / BM + used, used * ((a.max_count + BM - 1) / BM));
 }
 
+// Segments with a row, if the routing is at random, and the bytes of their weights.
+double used_segments(const ExpertGemmArgs &a) {
+    return std::max(1.0, a.nseg * -std::expm1(-static_cast<double>(a.entries) / a.nseg));
+}
+double weight_bytes(const ExpertGemmArgs &a) { return used_segments(a) * (a.swiglu ? 2.0 : 1.0) * a.N * a.H * (17.0 / 32.0); }
+
+// Weights that the Infinity Cache (256 MB) does not hold from call to call are
+// read past the caches by the streaming kernel.  Ordinary / past the caches (us,
+// 7168 x 2048 weights each): 24 experts with a row, 190 MB, 25.8 / 28.9; 35,
+// 270 MB, 41.8 / 44.2; 55, 432 MB, 76 / 68.5; 252, 1.96 GB, 328 / 306.
+bool weights_once(const ExpertGemmArgs &a) { return weight_bytes(a) > 320.0e6; }
+
 // The rule between the two kernels: the sooner by these estimates, in
 // microseconds, which near the crossing hold what was measured within about a
 // fifth.  Experts with a row: as many as a routing at random leaves with one.
 //   stream: a start of 4 us; a workgroup's work is one 16-row tile by 32 weight
 //     rows, with about 7 steps' worth of its own start and end; 3200 such steps a
-//     microsecond, or the weights at 6.0 TB/s.
+//     microsecond, or the weights at 6.0 TB/s (6.4 past the caches).
 //   tile: a start of 6 us, then rounds of 256 workgroups one tile each, 0.38 us a
 //     step and 0.0015 more for each row of a tile, or of a part of it in the last
 //     round; or the weights at 5.2 TB/s.
 // Measured, stream / tile (us; E experts with m rows each, M weight rows):
-//   E=256 H=7168 M=2048  m=1 218 / 279   m=4 328 / 384   m=8 362 / 391   m=12 428 / 396
-//   E=256 H=2048 M=7168  m=1 288 / 233   m=4 422 / 391   m=16 645 / 415
+//   E=256 H=7168 M=2048  m=1 197 / 279   m=4 306 / 384   m=8 342 / 391   m=12 412 / 397
+//   E=256 H=2048 M=7168  m=1 274 / 234   m=4 411 / 387   m=16 659 / 406
 //   E=64  H=1024 M=4096  m=1 25 / 21     m=12 48 / 34
 //   E=64  H=2048 M=2048  m=1 20 / 26     m=4 34 / 32     m=12 38 / 33
 //   E=8   H=7168 M=2048  m=4 14 / 28     m=32 26 / 29    m=64 42 / 30    m=256 134 / 38
 //   E=4   H=7168 M=512   m=128 16 / 28   m=256 24 / 29
 bool long_segments(const ExpertGemmArgs &a) {
     if (a.entries == 0) return false;
-    const double rows = static_cast<double>(a.entries), used = std::max(1.0, a.nseg * -std::expm1(-rows / a.nseg));
-    const double M = a.swiglu ? 2.0 * a.N : a.N, steps = a.H / kStep, weights = used * M * a.H * (17.0 / 32.0);
+    const double rows = static_cast<double>(a.entries), used = used_segments(a), weights = weight_bytes(a);
+    const double M = a.swiglu ? 2.0 * a.N : a.N, steps = a.H / kStep;
     const double stream_tiles = std::max(used, rows / kStreamRows + used / 2), row_tiles = std::max(used, rows / kTileRows + used / 2);
-    const double stream = 4 + std::max(stream_tiles * (M / (16 * kWTiles)) * (steps + 7) / 3200, weights / 6.0e6);
+    const double stream = 4 + std::max(stream_tiles * (M / (16 * kWTiles)) * (steps + 7) / 3200, weights / (weights_once(a) ? 6.4e6 : 6.0e6));
     const double tiles = row_tiles * std::ceil(M / kTileWeights), whole = std::floor(tiles / kCus), rest = tiles - whole * kCus;
     const double last_rows = rest * 4 <= kCus ? kTileRows / 4 : (rest * 2 <= kCus ? kTileRows / 2 : kTileRows);
     const auto step_us = [](double tile_rows) { return 0.38 + 0.0015 * tile_rows; };
@@ -799,10 +817,16 @@ hipError_t launch_expert_gemm_mx4(const ExpertGemmArgs &a, hipStream_t s) {
             hipLaunchKernelGGL(k_expert_tile<true>, grid, tile_block, 0, s, a, g.tiles_n);
         else
             hipLaunchKernelGGL(k_expert_tile<false>, grid, tile_block, 0, s, a, g.tiles_n);
-    } else if (a.swiglu) {
-        hipLaunchKernelGGL(k_expert_stream<true>, grid, stream_block, 0, s, a, g.tiles_n);
+    } else if (weights_once(a)) {
+        if (a.swiglu)
+            hipLaunchKernelGGL((k_expert_stream<true, true>), grid, stream_block, 0, s, a, g.tiles_n);
+        else
+            hipLaunchKernelGGL((k_expert_stream<false, true>), grid, stream_block, 0, s, a, g.tiles_n);
     } else {
-        hipLaunchKernelGGL(k_expert_stream<false>, grid, stream_block, 0, s, a, g.tiles_n);
+        if (a.swiglu)
+            hipLaunchKernelGGL((k_expert_stream<true, false>), grid, stream_block, 0, s, a, g.tiles_n);
+        else
+            hipLaunchKernelGGL((k_expert_stream<false, false>), grid, stream_block, 0, s, a, g.tiles_n);
     }
     return hipGetLastError();
 }
