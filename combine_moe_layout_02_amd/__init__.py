@@ -197,13 +197,17 @@ def _stream(stream, device) -> int:
 def _check(t: Optional[torch.Tensor], name: str, dtype, shape=None, device=None):
     if t is None:
         return
+    # the usual case in one line
+    if t.is_cuda and t.dtype is dtype and t.is_contiguous() and (shape is None or t.shape == shape) and \
+            (device is None or t.device == device):
+        return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if dtype is not None and t.dtype is not dtype and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+    if dtype is not None and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and t.shape != shape and tuple(t.shape) != tuple(shape):
+    if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
@@ -710,8 +714,9 @@ def _check_mx4(codes, scales, names, rows, H, device):
         if t is None:
             raise ValueError(f"{name} is missing")
         _check(t, name, torch.uint8, None, device)
-        if t.dim() != 2 or t.shape[1] != width or t.shape[0] < rows:
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [at least {rows}, {width}]")
+        shape = t.shape
+        if len(shape) != 2 or shape[1] != width or shape[0] < rows:
+            raise ValueError(f"{name}: shape {tuple(shape)}, expected [at least {rows}, {width}]")
 
 
 def _mx4_width(H: int, what: str):
@@ -748,7 +753,7 @@ def moe_quantize_mx4(x: torch.Tensor, codes=None, scales=None, layout: Optional[
         else:
             _check(scales, "scales", torch.uint8, (*lead, H // 32), dev)
     with _on_device(dev):
-        rc = _lib.moe_quantize_mx4(_ptr(x), rows, H, _ptr(src), _ptr(codes), _ptr(scales), _stream(stream, dev))
+        rc = _lib.moe_quantize_mx4(x.data_ptr(), rows, H, _ptr(src), codes.data_ptr(), scales.data_ptr(), _stream(stream, dev))
     if rc != MOE_OK:
         raise MoeError(rc, "moe_quantize_mx4")
     return codes, scales
@@ -769,7 +774,7 @@ def moe_dequantize_mx4(codes: torch.Tensor, scales: torch.Tensor, out=None, layo
     else:
         _check(out, "out", torch.bfloat16, (*codes.shape[:-1], H), dev)
     with _on_device(dev):
-        rc = _lib.moe_dequantize_mx4(_ptr(codes), _ptr(scales), rows, H, _ptr(src), _ptr(out), _stream(stream, dev))
+        rc = _lib.moe_dequantize_mx4(codes.data_ptr(), scales.data_ptr(), rows, H, _ptr(src), out.data_ptr(), _stream(stream, dev))
     if rc != MOE_OK:
         raise MoeError(rc, "moe_dequantize_mx4")
     return out
@@ -836,13 +841,14 @@ def moe_expert_gemm_mx4(desc: LayoutDesc, layout: Layout, x: torch.Tensor, x_sca
         with _alloc_on(stream):
             out = torch.empty(rows, N, dtype=torch.bfloat16, device=dev)
     _check(out, "out", torch.bfloat16, None, dev)
-    if out.dim() != 2 or out.shape[1] != N or out.shape[0] < rows:
-        raise ValueError(f"out: shape {tuple(out.shape)}, expected [at least {rows}, {N}]")
-    b = moe_layout_bufs(tokens_per_expert=layout.tokens_per_expert.data_ptr(), expert_offset=layout.expert_offset.data_ptr())
+    shape = out.shape
+    if len(shape) != 2 or shape[1] != N or shape[0] < rows:
+        raise ValueError(f"out: shape {tuple(shape)}, expected [at least {rows}, {N}]")
+    b = moe_layout_bufs(layout.tokens_per_expert.data_ptr(), None, layout.expert_offset.data_ptr())
     bal = None if balance is None else ctypes.byref(balance.c())
     with _on_device(dev):
-        rc = _lib.moe_expert_gemm_mx4(_made_once(desc), ctypes.byref(b), bal, slots_per_rank, _ptr(x), _ptr(x_scales), H,
-                                      _ptr(w), _ptr(w_scales), N, act, _ptr(out), _stream(stream, dev))
+        rc = _lib.moe_expert_gemm_mx4(_made_once(desc), ctypes.byref(b), bal, slots_per_rank, x.data_ptr(), x_scales.data_ptr(),
+                                      H, w.data_ptr(), w_scales.data_ptr(), N, act, out.data_ptr(), _stream(stream, dev))
     if rc != MOE_OK:
         raise MoeError(rc, "moe_expert_gemm_mx4")
     return out

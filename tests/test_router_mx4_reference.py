@@ -238,6 +238,22 @@ def test_python_checks_refuse_host_tensors(moe):
     with pytest.raises(ValueError):
         moe.moe_quantize_mx4(torch.zeros(2, 128, dtype=torch.bfloat16))
 
+    # every operand on the host, so that they agree with each other
+    u8, desc, S, E, H = dict(dtype=torch.uint8), moe.LayoutDesc(4, 2, 8, 1), 4, 8, 128
+    lay = moe.alloc_layout(desc, torch.device("cpu"))
+    with pytest.raises(ValueError):
+        moe.moe_dequantize_mx4(torch.zeros(2, H // 2, **u8), torch.zeros(2, H // 32, **u8))
+    with pytest.raises(ValueError):
+        moe.moe_dispatch_mx4(desc, lay, torch.zeros(S, H, dtype=torch.bfloat16))
+    with pytest.raises(ValueError):
+        moe.moe_expert_gemm_mx4(desc, lay, torch.zeros(8, H // 2, **u8), torch.zeros(8, H // 32, **u8),
+                                torch.zeros(E, 16, H // 2, **u8), torch.zeros(E, 16, H // 32, **u8))
+    with pytest.raises(ValueError):
+        moe.moe_balance_loss(moe.RouterDesc(4, 8, 2), z, torch.zeros(4, 2, dtype=torch.int32))
+    r = moe.Router(torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2), None, None, None)
+    with pytest.raises(ValueError):
+        moe.moe_router_backward(moe.RouterDesc(4, 8, 2), z, r, d_topk_w=torch.zeros(4, 2))
+
 
 def test_launch_limits_are_refused(moe):
     """A launch numbers at most 2^32 - 1 threads: shapes beyond are refused before anything is enqueued."""
