@@ -117,7 +117,10 @@ __device__ __forceinline__ void inspect(const float (&z)[V], float &top, bool &b
     top = wave_max(m);
 }
 
-// Softmax over the wave's logits (top = their maximum, finite).
+// Softmax over the wave's logits (top = their maximum, finite).  The product
+// with the rounded reciprocal has two roundings; its remainder, exact in a fused
+// step, times the reciprocal makes it the quotient with one, as the route
+// weights are (the division itself takes 10 instructions per logit).
 template <int V>
 __device__ __forceinline__ void softmax(const float (&z)[V], float top, float (&p)[V]) {
     float sum = 0.0f;
@@ -126,9 +129,12 @@ __device__ __forceinline__ void softmax(const float (&z)[V], float top, float (&
         p[j] = expf(z[j] - top);
         sum += p[j];
     }
-    const float inv = 1.0f / wave_sum(sum);
+    const float total = wave_sum(sum), inv = 1.0f / total;
 #pragma unroll
-    for (int j = 0; j < V; ++j) p[j] *= inv;
+    for (int j = 0; j < V; ++j) {
+        const float q = p[j] * inv;
+        p[j] = __builtin_fmaf(__builtin_fmaf(-q, total, p[j]), inv, q);
+    }
 }
 
 // Bits that order like the floats (no NaN; -0 was added to +0 before).
