@@ -15,6 +15,7 @@
 // the work), k_expert_tile for longer ones.
 #include "expert_gemm.h"
 #include "mx4.h"
+#include "tile_copies.h"
 
 #include <algorithm>
 #include <cmath>
@@ -132,9 +133,10 @@ __device__ __forceinline__ u32x2 pack_bf16x4(f32x4 v) {
 }
 
 // A raw buffer over `bytes` bytes: loads take a 32-bit offset per lane and read
-// zeros, stores write nothing, where it lies past the end.
+// zeros, stores write nothing, where it lies past the end.  An offset that all
+// lanes share is always smaller than `bytes`: whether the end is found there too
+// does not matter then.
 constexpr int kBufferRsrcWord3 = 0x00020000;
-constexpr unsigned int kPastEnd = ~0u - 15u;
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, unsigned int bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, static_cast<int>(bytes), kBufferRsrcWord3);
 }
@@ -365,7 +367,6 @@ __global__ __launch_bounds__(kStreamWaves * kWave, 4) void k_expert_stream(Exper
 // the barriers (330) and raising the waves' priority (320) did not help.
 constexpr int kTileRows = 256;
 constexpr int kTileWeights = 256;
-constexpr int kTileWaves = 8;
 constexpr int kTileThreads = kTileWaves * kWave;
 constexpr int kCus = 256;                    // workgroups that run at once
 constexpr int kStageVecs = (kTileRows + kTileWeights) * 8;   // 16-byte vectors: 128 bytes of every token row, then weight row
@@ -423,21 +424,16 @@ __device__ __forceinline__ size_t first_weight_row(const ExpertGemmArgs &a, cons
 
 // Lane l's vector of a copy: row l/8 of the eight, chunk c at place l%8, where
 // chunk c (32 channels) of row q lies at c ^ (q % 8): eight rows' chunk c are
-// then in eight different groups of banks.
+// then in eight different groups of banks (tile_copies.h).
 template <bool SWIGLU>
 __device__ __forceinline__ TileCopies tile_copies(const ExpertGemmArgs &a, const RowTile &t) {
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const unsigned int half = a.H / 2, scales = a.H / kMx4Block;
     const bool wide = t.rows > 128;
-    const int q8 = lane / 8;
-    const unsigned int chunk = ((lane & 7) ^ q8) * 16;
     TileCopies c;
-    // Weight row j of the tile belongs to wave j/64 (wide) or j/32, and is row
-    // j%16 of its 16-row tile; with SWIGLU the second half of a wave's tiles are
-    // the up rows of the first.  This wave copies rows 32*wave .. +31.
-    c.wo = ((SWIGLU ? (wide ? wave / 2 * 32 : wave * 16) : wave * 32) + q8) * half + chunk;
-    c.xo = (wave * 8 + q8) * half + chunk;
+    c.wo = first_weight(SWIGLU, wide, wave, lane) * half + lane_chunk(lane);
+    c.xo = first_token(wave, lane) * half + lane_chunk(lane);
     // scales: a row per thread.  Waves 0 to 3 weight rows (SWIGLU: 0 and 1 gate,
     // 2 and 3 up), 4 to 7 token rows.
     if (wave >= 4) {
@@ -461,29 +457,28 @@ __device__ __forceinline__ TileCopies tile_copies(const ExpertGemmArgs &a, const
 
 // Copies channels 256*s .. of the tile into `stage`.  A last stage of 128
 // channels leaves the second half of each row alone (the offset is past the
-// end there).  Rows are told apart by the uniform offset, which counts where a
-// buffer's end is checked: two offsets per lane do for all copies (211 registers
-// instead of 256, 1 % of the time).
+// end there).  Every copy's offset is made here from one per lane and operand:
+// kept from stage to stage they would take a register each.
 template <bool SWIGLU, int XCOPIES>
 __device__ __forceinline__ void copy_stage(const ExpertGemmArgs &a, const TileCopies &c, int s, u32x4 *stage, bool wide) {
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int half = a.H / 2, at = s * 128;
+    const int half = a.H / 2;
+    const unsigned int gone = left_out(a.H, s, lane);
     unsigned int wo = c.wo, xo = c.xo;
-    if (256 * s + 128 >= a.H) {
-        const unsigned int gone = ((lane & 7) ^ (lane / 8)) & 4 ? kPastEnd : 0u;
-        wo |= gone;
-        xo |= gone;
-    }
+    asm volatile("" : "+v"(wo), "+v"(xo));
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            copy_to_lds(c.w[i], stage + (kTileRows + wave * 32 + i * 16 + j * 8) * 8, wo,
-                        at + (SWIGLU && !wide ? 8 * j : 16 * i + 8 * j) * half);
+        for (int j = 0; j < 2; ++j) {
+            const CopyAt at = copy_at(wo, weight_step(SWIGLU, wide, i, j), half, s, gone);
+            copy_to_lds(c.w[i], stage + (kTileRows + wave * 32 + i * 16 + j * 8) * 8, at.lane, at.uniform);
+        }
 #pragma unroll
-    for (int i = 0; i < XCOPIES; ++i)
-        copy_to_lds(c.x, stage + (i * kTileWaves + wave) * 64, xo, at + i * kTileWaves * 8 * half);
+    for (int i = 0; i < XCOPIES; ++i) {
+        const CopyAt at = copy_at(xo, token_step(i), half, s, gone);
+        copy_to_lds(c.x, stage + (i * kTileWaves + wave) * 64, at.lane, at.uniform);
+    }
 }
 
 // Scale words 4S .. 4S+3 of this thread's row; those past the row's end are
