@@ -29,7 +29,8 @@ constexpr int kMaxGroups = 64;
 constexpr int kFinishThreads = 1024;
 constexpr int kMaxParts = 256;               // workgroups per sequence
 constexpr int kMaxLastParts = 1024;          // workgroups whose last one adds up the loss
-constexpr int kMaxCountedSeqs = 8192;        // sequences that k_router_finish counts itself
+constexpr int kMaxCountedSeqs = 1024;        // sequences that k_router_finish counts itself,
+constexpr int64_t kMaxCounting = 1 << 23;    // and the partial rows that its workgroups read for it in all
 
 // Wave-wide reductions: DPP shifts inside rows of 16, then across rows; lane
 // 63 ends with the result and every lane reads it from there.
@@ -335,8 +336,8 @@ __device__ __forceinline__ double block_sum(double v, double *s_tmp) {
     return s;
 }
 
-// Sequences with a token that counts, for more of them than k_router_finish
-// counts itself (one workgroup).
+// Sequences with a token that counts, where k_router_finish does not count them
+// itself (one workgroup).
 __global__ __launch_bounds__(kFinishThreads) void k_router_used(const int32_t *__restrict__ part_n, int G, int per_seq,
                                                                int32_t *used) {
     __shared__ double s_tmp[kFinishThreads / kWave];
@@ -598,9 +599,15 @@ hipError_t launch_v(const RouterArgs &a, void *workspace, hipStream_t s) {
         hipLaunchKernelGGL((k_router<V, BF16, true, GIVEN, true>), grid, wide, 0, s, a, sh, part, pn, used + 1);
     else
         hipLaunchKernelGGL((k_router<V, BF16, false, GIVEN, true>), grid, wide, 0, s, a, sh, part, pn, used + 1);
-    const bool count_apart = a.G > kMaxCountedSeqs || parts > 16 * kMaxCountedSeqs;
-    if (count_apart) hipLaunchKernelGGL(k_router_used, dim3(1), dim3(kFinishThreads), 0, s, pn, a.G, sh.per_seq, used);
+    // Which sequences count: every finishing workgroup finds out by itself, or one
+    // more launch does for all of them.  The former grows as workgroups times
+    // partial rows.  Measured in place / apart (us, the whole call): 64 workgroups
+    // x 32 rows 10.8 / 12.6; 256 x 8192 105 / 119; 512 x 4096 53 / 51; 1024 x 128
+    // 33 / 35; 1024 x 32768 515 / 432; 2048 x 1024 37 / 28; 16384 x 8192 616 / 162;
+    // 65536 x 8192 2285 / 446.
     const int cols = finish_blocks(a), blocks = a.G * cols;
+    const bool count_apart = blocks > kMaxCountedSeqs || blocks * parts > kMaxCounting;
+    if (count_apart) hipLaunchKernelGGL(k_router_used, dim3(1), dim3(kFinishThreads), 0, s, pn, a.G, sh.per_seq, used);
     hipLaunchKernelGGL(k_router_finish, dim3(blocks), dim3(kFinishThreads), 0, s, a, sh.per_seq, cols, part, pn,
                        count_apart ? used : nullptr, pl, used + 1);
     if (blocks > kMaxLastParts) hipLaunchKernelGGL(k_router_loss, dim3(1), dim3(kFinishThreads), 0, s, pl, blocks, a.loss);

@@ -1,8 +1,11 @@
 """What the router's numbers are made of, on the GPU: probabilities, and sums over many tokens."""
 from __future__ import annotations
 
+import numpy as np
 import pytest
 import torch
+
+from router_mx4_reference import router_reference
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -27,3 +30,52 @@ def test_the_loss_has_the_weights_probabilities(moe, E):
                        for t in range(16) for k in range(K)]).reshape(16, K)
     want = (r.topk_w.double() * E).float()
     assert torch.equal(got, want), f"{int((got != want).sum())} of {got.numel()} differ"
+
+
+def _capture(f, n):
+    f()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(n):
+            f()
+    return graph
+
+
+def test_the_loss_of_many_sequences_takes_time_in_proportion(moe):
+    """Four times the sequences take about four times as long (3.8 measured; counting the used sequences in every
+    workgroup took 9): at most six."""
+    graphs = []
+    for G in (2048, 8192):
+        desc = moe.RouterDesc(16 * G, 256, 2, seq_len=16)
+        z = torch.randn((16 * G, 256), device=DEV)
+        r = moe.alloc_router(desc, z.device)
+        graphs.append(_capture(lambda: moe.moe_router(desc, z, router=r), 4))
+    best = [float("inf")] * 2
+    for _ in range(8):
+        for i, g in enumerate(graphs):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            g.replay()
+            b.record()
+            torch.cuda.synchronize()
+            best[i] = min(best[i], a.elapsed_time(b))
+    assert best[1] < 6 * best[0], best
+
+
+@pytest.mark.parametrize("G,T,E", [(1023, 3, 16), (1024, 1, 16), (1025, 2, 32), (512, 2, 40), (513, 2, 33), (340, 40, 70),
+                                   (1000, 130, 8), (1024, 140, 8)])
+def test_sequences_that_count_are_counted(moe, G, T, E):
+    """On both sides of where a launch of its own counts them; a third of the sequences have no token that counts."""
+    rng = np.random.default_rng(G + T)
+    z = rng.standard_normal((G * T, E)).astype(np.float32)
+    mask = np.repeat(rng.random(G) < 0.67, T) & (rng.random(G * T) < 0.9)
+    idx = rng.integers(0, E, (G * T, 2)).astype(np.int32)
+    desc = moe.RouterDesc(G * T, E, 2, seq_len=T)
+    r = moe.moe_balance_loss(desc, torch.from_numpy(z).to(DEV), torch.from_numpy(idx).to(DEV), torch.from_numpy(mask).to(DEV))
+    ref = router_reference(z.astype(np.float64), 2, seq_len=T, mask=mask, given=idx)
+    assert np.array_equal(r.expert_count.cpu().numpy(), ref["count"])
+    # a coefficient holds the number of sequences and is rounded once
+    assert np.all(np.abs(r.balance_coef.cpu().numpy() - ref["coef"]) <= 2.0 ** -23 * ref["coef"])
+    # probabilities within 80 units of 2^-24 (test_gpu_router.py), their sums and the loss a few more
+    assert abs(float(r.balance_loss) - ref["loss"]) <= 160 * 2.0 ** -24 * ref["loss"]
