@@ -5,7 +5,7 @@
 // among equal logits is the lowest lane, then the lowest register.  Softmax is
 // one maximum and one sum across the wave (DPP); a pick is the wave's maximum,
 // one ballot for its lane, and the owner's register struck out, K times.
-// Arithmetic is fp32, sums over workgroups fp64.
+// Arithmetic within a token is fp32, sums over tokens are fp64.
 //
 // Loss = sum over tokens and experts of coef[sequence][e] * p[t][e], where coef
 // comes from the counts alone.  A workgroup adds up its own tokens'
@@ -249,9 +249,12 @@ __global__ __launch_bounds__(WAVES * kWave) void k_router(RouterArgs a, LossShap
         t0 = static_cast<int64_t>(blockIdx.x) * WAVES;
         t1 = min(t0 + WAVES, static_cast<int64_t>(a.S));
     }
-    float sum[V];
+    // 64 bits: a wave of a long sequence adds thousands of tokens.  Its sum is
+    // rounded to fp32 where it passes to LDS, and the workgroup's in its partial
+    // row: half a unit each, however long the sequence.
+    double sum[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) sum[j] = 0.0f;
+    for (int j = 0; j < V; ++j) sum[j] = 0.0;
     int n = 0;
     for (int64_t t = t0 + wave; t < t1; t += WAVES) {
         float z[V];
@@ -269,7 +272,7 @@ __global__ __launch_bounds__(WAVES * kWave) void k_router(RouterArgs a, LossShap
                 n += 1;
                 if (broken) {
 #pragma unroll
-                    for (int j = 0; j < V; ++j) sum[j] = __builtin_nanf("");
+                    for (int j = 0; j < V; ++j) sum[j] = __builtin_nan("");
                 } else {
                     softmax<V>(z, top, p);
 #pragma unroll
@@ -309,15 +312,15 @@ __global__ __launch_bounds__(WAVES * kWave) void k_router(RouterArgs a, LossShap
     if constexpr (LOSS) {
 #pragma unroll
         for (int j = 0; j < V; ++j)
-            if (lane * V + j < E) s_p[wave * E + lane * V + j] = sum[j];
+            if (lane * V + j < E) s_p[wave * E + lane * V + j] = static_cast<float>(sum[j]);
         if (lane == 0) atomicAdd(&s_n, n);
         __syncthreads();
         const size_t base = static_cast<size_t>(blockIdx.x) * E;
         for (int e = threadIdx.x; e < E; e += WAVES * kWave) {
-            float v = 0.0f;
+            double v = 0.0;
 #pragma unroll
             for (int w = 0; w < WAVES; ++w) v += s_p[w * E + e];
-            part[base + e] = Partial{v, s_c[e]};
+            part[base + e] = Partial{static_cast<float>(v), s_c[e]};
         }
         if (threadIdx.x == 0) part_n[blockIdx.x] = s_n;
         if (blockIdx.x == 0 && threadIdx.x == 0) *counter = 0;   // for k_router_finish, launched behind this

@@ -79,3 +79,28 @@ def test_sequences_that_count_are_counted(moe, G, T, E):
     assert np.all(np.abs(r.balance_coef.cpu().numpy() - ref["coef"]) <= 2.0 ** -23 * ref["coef"])
     # probabilities within 80 units of 2^-24 (test_gpu_router.py), their sums and the loss a few more
     assert abs(float(r.balance_loss) - ref["loss"]) <= 160 * 2.0 ** -24 * ref["loss"]
+
+
+@pytest.mark.parametrize("E,S", [(3, 1 << 22), (10, 1 << 21), (250, 1 << 20), (300, 1 << 20), (1000, 1 << 19)])
+def test_the_loss_of_a_long_sequence(moe, E, S):
+    """Equal logits: every probability is 1/E rounded once and the loss is 1 whatever the routing.  Roundings, half a
+    unit (2^-24) each: the probability, a wave's sum, a workgroup's, the loss; sums between them are in 64 bits
+    (errors below S * 2^-53 = 2^-31).  Sums of all a wave's tokens in fp32 were off by 15 to 99 such halves here."""
+    z = torch.zeros((S, E), dtype=torch.bfloat16, device=DEV)
+    idx = torch.randint(0, E, (S, 1), generator=torch.Generator().manual_seed(E), dtype=torch.int32).to(DEV)
+    r = moe.moe_balance_loss(moe.RouterDesc(S, E, 1), z, idx)
+    assert int(r.expert_count.sum()) == S
+    assert abs(float(r.balance_loss) - 1.0) <= 4 * 2.0 ** -24 + 2.0 ** -31
+
+
+def test_the_loss_of_a_long_sequence_of_near_equal_logits(moe):
+    """Logits within 0.1 of each other: a probability has the exponential's one unit (2 halves), its argument's
+    rounding (0.1), 6 steps of the sum over the wave and their terms' 2.1, and the quotient's 1; then as above 3."""
+    S, E = 1 << 20, 50
+    z = torch.rand((S, E), generator=torch.Generator().manual_seed(1)).mul_(0.1).to(DEV)
+    idx = torch.randint(0, E, (S, 2), generator=torch.Generator().manual_seed(2), dtype=torch.int32).to(DEV)
+    r = moe.moe_balance_loss(moe.RouterDesc(S, E, 2), z, idx)
+    count = torch.bincount(idx.flatten(), minlength=E).double()
+    p = torch.softmax(z.double(), 1).sum(0)
+    want = float((E * count / (2.0 * S) * p / S).sum())
+    assert abs(float(r.balance_loss) - want) <= (2.1 + 6 + 2.1 + 1 + 3) * 2.0 ** -24 * want
