@@ -65,9 +65,10 @@
  *     Calls on one stream run in order; calls on different streams that share
  *     output buffers race.
  *   - Limits: 0 <= S, 1 <= K <= 16, 1 <= E <= 1024, R divides E,
- *     S*K and every row count below 2^31; dispatch: S*ceil(H/512) (bf16),
- *     S*ceil(H/1024) (FP8) or S*ceil(H/2048) (MXFP4) below 2^31; combine:
- *     S*ceil(H/512) below 2^31.  Offsets inside every array are 64-bit.
+ *     S*K and every row count below 2^31; dispatch: S*ceil(H/512) (bf16) or
+ *     S*ceil(H/1024) (FP8) below 2^31, S*ceil(H/2048) (MXFP4) below 2^26;
+ *     combine: S*ceil(H/512) below 2^31.  Offsets inside every array are 64-bit.
+ *     The router's, the conversions' and the products' stand at their calls.
  */
 #ifndef MOE_EP_H
 #define MOE_EP_H
@@ -339,9 +340,10 @@ size_t moe_router_workspace_bytes(const moe_router_desc *desc);
  * A counting token with a NaN or +inf logit is not routed (picks -1, weights
  * 0), and its probabilities are NaN: so is the loss, and its row of the
  * gradient.  The results do not depend on the order in which work runs.
- * No alignment beyond the element types' is needed; workspace 16 bytes.  Fewer
- * than 2^26 - 4 tokens, and with the loss sequences * ceil(E/32) < 2^22; else
- * MOE_ERR_SHAPE. */
+ * No alignment beyond the element types' is needed; workspace 16 bytes.
+ * MOE_ERR_SHAPE where a launch cannot number the work; it always can with fewer
+ * than 2^26 - 4 tokens and, for the loss, sequences * ceil(E/32) and
+ * sequences * min(ceil(T/16), 256) below 2^22, T tokens in a sequence. */
 moe_status moe_router(const moe_router_desc *desc, const void *logits, int32_t logits_type, const uint8_t *token_mask,
                       const moe_router_bufs *out, void *workspace, size_t workspace_bytes, void *stream);
 
@@ -391,12 +393,16 @@ moe_status moe_router_backward(const moe_router_desc *desc, const void *logits, 
  *   x       [rows,H] bf16, 16-byte aligned.
  *   src     [rows] or NULL: with a layout's src only the rows that hold an
  *           entry (src[r] >= 0) are read and written.
- *   codes   [rows,H/2], 16-byte aligned; scales [rows,H/32] (any alignment). */
+ *   codes   [rows,H/2], 16-byte aligned; scales [rows,H/32] (any alignment).
+ * rows * H at most 2^37 - 8192. */
 moe_status moe_quantize_mx4(const void *x, int64_t rows, int32_t H, const int32_t *src, void *codes, uint8_t *scales,
                             void *stream);
 
-/* MXFP4 rows -> bf16 (exact; a block of scale 255 gives NaN).  Arguments as in
- * moe_quantize_mx4: rows with src[r] < 0 are neither read nor written. */
+/* MXFP4 rows -> bf16.  Exact, but for the values past bf16's range, 2^128 and
+ * more (scale byte 253 with 4 and 6, 254 with 2 and more; moe_quantize_mx4 writes
+ * neither), which become infinities; a block of scale 255 gives NaN.  Arguments
+ * and limit as in moe_quantize_mx4: rows with src[r] < 0 are neither read nor
+ * written. */
 moe_status moe_dequantize_mx4(const void *codes, const uint8_t *scales, int64_t rows, int32_t H, const int32_t *src,
                               void *out, void *stream);
 
@@ -430,7 +436,9 @@ typedef enum {
  *             w_scales 4 bytes.
  * Rows that hold no entry are neither read nor written: expert_offset,
  * tokens_per_expert, seg_offset and slot_expert say which rows hold one.  No
- * workspace; the grid depends on the shape alone, not on the routing. */
+ * workspace; the grid depends on the shape alone, not on the routing:
+ * MOE_ERR_SHAPE where a launch cannot number it; it always can with
+ * (S*K/16 + segments that can hold a row) * ceil(M/32) at most 2^23 - 8. */
 moe_status moe_expert_gemm_mx4(const moe_layout_desc *desc, const moe_layout_bufs *layout,
                                const moe_balance_bufs *bal, int32_t slots_per_rank, const void *x,
                                const uint8_t *x_scales, int32_t H, const void *w, const uint8_t *w_scales, int32_t N,
