@@ -15,7 +15,7 @@ struct RouterArgs {
     int32_t seq;               // tokens per sequence (> 0)
     int32_t G;                 // sequences
     float alpha;
-    bool given;                // the routing is the caller's (given_idx [S,K]); else the router picks
+    bool given;                // the routing is the caller's (given_idx [S,K], with the loss); else the router picks
     const int32_t *given_idx;
     int32_t *idx;              // [S,K]
     float *w;                  // [S,K]

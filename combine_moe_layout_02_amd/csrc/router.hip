@@ -231,6 +231,7 @@ struct LossShape {
 template <int V, bool BF16, bool VEC, bool GIVEN, bool LOSS, int WAVES = LOSS ? loss_waves<V>() : kRouterWaves>
 __global__ __launch_bounds__(WAVES * kWave) void k_router(RouterArgs a, LossShape sh, Partial *part, int32_t *part_n,
                                                          int32_t *counter) {
+    static_assert(LOSS || !GIVEN, "without the loss the router makes the routing");
     __shared__ float s_p[LOSS ? WAVES * V * kWave : 1];       // [waves][E] probabilities
     __shared__ int32_t s_c[LOSS ? V * kWave : 1];             // [E] picks
     __shared__ unsigned int best[GIVEN ? 1 : WAVES][kMaxGroups];
@@ -267,7 +268,7 @@ __global__ __launch_bounds__(WAVES * kWave) void k_router(RouterArgs a, LossShap
         inspect<V>(z, top, broken);
         const bool counts = !masked && (broken || top > -__builtin_inff());
         float p[V];
-        if constexpr (LOSS || GIVEN) {
+        if constexpr (LOSS) {
             if (counts) {
                 n += 1;
                 if (broken) {
@@ -577,14 +578,15 @@ bool whole_vectors(const RouterArgs &a, const void *p) {
 template <int V, bool BF16, bool GIVEN>
 hipError_t launch_v(const RouterArgs &a, void *workspace, hipStream_t s) {
     const bool vec = whole_vectors<V>(a, a.logits);
-    const dim3 block(kRouterWaves * kWave);
-    if (a.loss == nullptr) {
-        const dim3 grid((static_cast<unsigned>(a.S) + kRouterWaves - 1) / kRouterWaves);
-        if (vec)
-            hipLaunchKernelGGL((k_router<V, BF16, true, GIVEN, false>), grid, block, 0, s, a, LossShape{}, nullptr, nullptr, nullptr);
-        else
-            hipLaunchKernelGGL((k_router<V, BF16, false, GIVEN, false>), grid, block, 0, s, a, LossShape{}, nullptr, nullptr, nullptr);
-        return hipGetLastError();
+    if constexpr (!GIVEN) {
+        if (a.loss == nullptr) {
+            const dim3 block(kRouterWaves * kWave), grid((static_cast<unsigned>(a.S) + kRouterWaves - 1) / kRouterWaves);
+            if (vec)
+                hipLaunchKernelGGL((k_router<V, BF16, true, false, false>), grid, block, 0, s, a, LossShape{}, nullptr, nullptr, nullptr);
+            else
+                hipLaunchKernelGGL((k_router<V, BF16, false, false, false>), grid, block, 0, s, a, LossShape{}, nullptr, nullptr, nullptr);
+            return hipGetLastError();
+        }
     }
     if (a.G == 0) {   // no sequence: the loss is 0
         hipLaunchKernelGGL(k_router_loss, dim3(1), dim3(kFinishThreads), 0, s, nullptr, 0, a.loss);
