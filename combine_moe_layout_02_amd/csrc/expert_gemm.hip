@@ -401,7 +401,6 @@ struct SegTable {
 
 struct TileLds {
     u32x4 *stage0, *stage1, *scale;   // scale: token rows, then weight rows
-    SegTable *segs;
 };
 
 // What a tile's copies need besides the tile: this lane's first offsets into
@@ -699,7 +698,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_expert_tile(ExpertGemmArgs 
         t.rows = __builtin_amdgcn_readfirstlane(min(t.rows - skip, part_rows));
         return t.rows > 0;
     };
-    const TileLds lds{stage0, stage1, scale, &segs};
+    const TileLds lds{stage0, stage1, scale};
     RowTile t;
     if (!tile_of(0, t)) return;                                // the same for every wave
     u32x4 scales;
