@@ -892,7 +892,7 @@ class Buffer:
         dev = torch.device(device)
         if dev.type == "cuda" and dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
-        self.H, self.fp8, self.mx4, self.device = H, fp8, mx4, dev
+        self.H, self.fp8, self.mx4, self.device, self._index = H, fp8, mx4, dev, dev.index
         self.layout = alloc_layout(self.desc, dev)
         if mx4:
             self.recv = torch.empty((self.rows, H // 2), dtype=torch.uint8, device=dev)
@@ -926,7 +926,14 @@ class Buffer:
         _check(hidden, "hidden", torch.bfloat16, (S, self.H), self.device)
         _check(topk_w, "topk_w", torch.float32, (S, K), self.device)
 
+    # The C calls launch on the current device.  A call that finds another one
+    # than the buffer's makes itself again with the buffer's: one comparison in
+    # the usual case (a context manager around every call takes 0.3 us).
+
     def layout_call(self, topk_idx, stream=None, check=True):
+        if self._index != _raw_current_device():
+            with torch.cuda.device(self.device):
+                return self.layout_call(topk_idx, stream, check)
         if check:
             _check(topk_idx, "topk_idx", torch.int32, (self.desc.S, self.desc.K), self.device)
         if self.balance is not None:
@@ -941,6 +948,9 @@ class Buffer:
             raise MoeError(rc, "moe_layout")
 
     def dispatch_call(self, hidden, topk_idx=None, topk_w=None, stream=None, check=True):
+        if self._index != _raw_current_device():
+            with torch.cuda.device(self.device):
+                return self.dispatch_call(hidden, topk_idx, topk_w, stream, check)
         if check:
             self._inputs(hidden, topk_idx, topk_w)
         if self.mx4:
@@ -958,6 +968,9 @@ class Buffer:
     def layout_dispatch_call(self, hidden, topk_idx, topk_w=None, stream=None, check=True):
         """moe_layout_dispatch: one launch for decode-sized batches (with a
         balanced layout or MXFP4 rows: the layout, then the dispatch)."""
+        if self._index != _raw_current_device():
+            with torch.cuda.device(self.device):
+                return self.layout_dispatch_call(hidden, topk_idx, topk_w, stream, check)
         if check:
             self._inputs(hidden, topk_idx, topk_w)
         if self.balance is not None or self.mx4:
@@ -971,6 +984,9 @@ class Buffer:
             raise MoeError(rc, "moe_layout_dispatch")
 
     def combine_call(self, expert_out, w=None, shared_out=None, stream=None, check=True):
+        if self._index != _raw_current_device():
+            with torch.cuda.device(self.device):
+                return self.combine_call(expert_out, w, shared_out, stream, check)
         if check:
             _check(expert_out, "expert_out", torch.bfloat16, (self.rows, self.H), self.device)
             _check(w, "w", torch.float32, (self.desc.S, self.desc.K), self.device)
@@ -985,6 +1001,9 @@ class Buffer:
         for MXFP4 rows, whose consumers skip padding)."""
         if self.mx4:
             raise MoeError(MOE_ERR_SHAPE, "moe_zero_padding")
+        if self._index != _raw_current_device():
+            with torch.cuda.device(self.device):
+                return self.zero_padding_call(stream)
         rc = _lib.moe_zero_padding(self._dp, self._bp, self.H, 1 if self.fp8 else 0, self._recv, self._scales,
                                    _stream(stream, self.device))
         if rc != MOE_OK:
