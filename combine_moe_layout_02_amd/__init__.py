@@ -3,8 +3,8 @@
 Thin ctypes binding over libmoe_ep.so (declared in include/moe_ep.h).  The
 Python functions carry the C names and only marshal arguments: torch tensors
 supply device memory and the current HIP stream, every step of the path runs
-in the library's HIP kernels.  ``router`` and ``balance_loss`` are the same
-calls as autograd functions.  Importing this package fails loudly when the
+in the library's HIP kernels.  ``router``, ``balance_loss``, ``dispatch``,
+``expert_ffn`` and ``combine`` are the same calls as autograd functions.  Importing this package fails loudly when the
 library has not been built; there is no CPU fallback.
 """
 from __future__ import annotations
@@ -30,7 +30,9 @@ EXPORTED = ("moe_max_recv_rows", "moe_layout_workspace_bytes", "moe_layout", "mo
             "moe_layout_dispatch", "moe_combine", "moe_layout_balanced_workspace_bytes", "moe_layout_balanced",
             "moe_zero_padding", "moe_stream_create_cu_limited", "moe_stream_create_cu_range", "moe_stream_destroy",
             "moe_status_str", "moe_layout_noalloc", "moe_router_workspace_bytes", "moe_router", "moe_balance_loss",
-            "moe_router_backward", "moe_quantize_mx4", "moe_dequantize_mx4", "moe_dispatch_mx4", "moe_expert_gemm_mx4")
+            "moe_router_backward", "moe_quantize_mx4", "moe_dequantize_mx4", "moe_dispatch_mx4", "moe_expert_gemm_mx4",
+            "moe_expert_gemm", "moe_expert_gemm_backward_x", "moe_expert_gemm_backward_w", "moe_combine_backward",
+            "moe_quantize_i8", "moe_dequantize_i8", "moe_dispatch_i8", "moe_expert_gemm_i8")
 
 
 class MoeError(RuntimeError):
@@ -110,8 +112,19 @@ def _load():
     L.moe_dequantize_mx4.argtypes = [P, P, I64, I, P, P, P]
     L.moe_dispatch_mx4.argtypes = [D, B, P, I, P, P, P, P, P]
     L.moe_expert_gemm_mx4.argtypes = [D, B, ctypes.POINTER(moe_balance_bufs), I, P, P, I, P, P, I, I, P, P]
+    BB = ctypes.POINTER(moe_balance_bufs)
+    L.moe_expert_gemm.argtypes = [D, B, BB, I, P, I, P, I, I, P, P, P]
+    L.moe_expert_gemm_backward_x.argtypes = [D, B, BB, I, P, I, P, I, P, P, P]
+    L.moe_expert_gemm_backward_w.argtypes = [D, B, BB, I, P, I, P, I, I, P, P]
+    L.moe_combine_backward.argtypes = [D, B, P, I, P, P, P, P, P]
+    L.moe_quantize_i8.argtypes = [P, I64, I, P, P, P, P]
+    L.moe_dequantize_i8.argtypes = [P, P, I64, I, P, P, P]
+    L.moe_dispatch_i8.argtypes = [D, B, P, I, P, P, P, P, P]
+    L.moe_expert_gemm_i8.argtypes = [D, B, BB, I, P, P, I, P, P, I, I, P, P]
     for f in (L.moe_router, L.moe_balance_loss, L.moe_router_backward, L.moe_quantize_mx4, L.moe_dequantize_mx4,
-              L.moe_dispatch_mx4, L.moe_expert_gemm_mx4):
+              L.moe_dispatch_mx4, L.moe_expert_gemm_mx4, L.moe_expert_gemm, L.moe_expert_gemm_backward_x,
+              L.moe_expert_gemm_backward_w, L.moe_combine_backward, L.moe_quantize_i8, L.moe_dequantize_i8, L.moe_dispatch_i8,
+              L.moe_expert_gemm_i8):
         f.restype = ctypes.c_int
     return L
 
@@ -169,7 +182,7 @@ class Layout:
     workspace: Optional[torch.Tensor] = None
 
     def c(self) -> moe_layout_bufs:
-        return moe_layout_bufs(*(t.data_ptr() for t in (
+        return moe_layout_bufs(*(_ptr(t) for t in (
             self.tokens_per_expert, self.tokens_per_rank, self.expert_offset, self.rank_offset,
             self.pos, self.src, self.status)))
 
@@ -855,6 +868,397 @@ def moe_expert_gemm_mx4(desc: LayoutDesc, layout: Layout, x: torch.Tensor, x_sca
 
 
 # ---------------------------------------------------------------------------
+# The experts in bf16, with their gradients, and in 8-bit integers
+# ---------------------------------------------------------------------------
+
+def _check_segments(desc: LayoutDesc, layout: Layout, balance: Optional[Balance], slots_per_rank: int, device):
+    """The layout's arrays that a product reads, as C structs (layout, balance or None)."""
+    _check(layout.tokens_per_expert, "layout.tokens_per_expert", torch.int32, (desc.E,), device)
+    _check(layout.expert_offset, "layout.expert_offset", torch.int32, (desc.E + 1,), device)
+    b = moe_layout_bufs(layout.tokens_per_expert.data_ptr(), None, layout.expert_offset.data_ptr())
+    if balance is None:
+        return ctypes.byref(b), None
+    _check(balance.seg_offset, "balance.seg_offset", torch.int32, (desc.E + desc.R * slots_per_rank + 1,), device)
+    _check(balance.slot_expert, "balance.slot_expert", torch.int32, (max(desc.R * slots_per_rank, 1),), device)
+    return ctypes.byref(b), ctypes.byref(balance.c())
+
+
+def _product_rows(desc: LayoutDesc, what: str) -> int:
+    rows = int(_lib.moe_max_recv_rows(_made_once(desc)))
+    if rows < 0:
+        raise MoeError(MOE_ERR_SHAPE, what)
+    return rows
+
+
+def _check_rows(t: torch.Tensor, name: str, dtype, rows: int, width: int, device):
+    """A row buffer [at least `rows`, width]."""
+    _check(t, name, dtype, None, device)
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != width or shape[0] < rows:
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected [at least {rows}, {width}]")
+
+
+def _gemm_shape(desc: LayoutDesc, x: torch.Tensor, w: torch.Tensor, act: int, dtype, what: str):
+    """(H, N, M) of a product of rows x [.., H] with weights w [E,M,H]."""
+    if act not in (MOE_ACT_NONE, MOE_ACT_SWIGLU):
+        raise MoeError(MOE_ERR_SHAPE, what)
+    H = x.shape[-1]
+    if w.dim() != 3 or (act == MOE_ACT_SWIGLU and w.shape[1] % 2):
+        raise ValueError(f"w: shape {tuple(w.shape)}, expected [E, N or 2N, H]")
+    M = w.shape[1]
+    _check(w, "w", dtype, (desc.E, M, H), x.device)
+    return H, (M // 2 if act == MOE_ACT_SWIGLU else M), M
+
+
+def moe_expert_gemm(desc: LayoutDesc, layout: Layout, x: torch.Tensor, w: torch.Tensor, act: int = MOE_ACT_NONE, out=None,
+                    pre=None, balance: Optional[Balance] = None, slots_per_rank: int = 0, stream=None) -> torch.Tensor:
+    """Every expert's bf16 rows times its weights: out [max_recv,N] bf16.
+
+    x [max_recv,H]; w [E,M,H], M = N, or 2N with MOE_ACT_SWIGLU (N gate rows,
+    then N up rows).  ``pre`` [max_recv,2N] (SWIGLU only) receives the gate's
+    and up's values before the activation, for moe_expert_gemm_backward_x.
+    Rows that hold no entry are neither read nor written."""
+    dev, rows = x.device, _product_rows(desc, "moe_expert_gemm")
+    H, N, M = _gemm_shape(desc, x, w, act, torch.bfloat16, "moe_expert_gemm")
+    _check_rows(x, "x", torch.bfloat16, rows, H, dev)
+    if pre is not None:
+        if act != MOE_ACT_SWIGLU:
+            raise MoeError(MOE_ERR_SHAPE, "moe_expert_gemm")
+        _check_rows(pre, "pre", torch.bfloat16, rows, M, dev)
+    if out is None:
+        with _alloc_on(stream):
+            out = torch.empty(rows, N, dtype=torch.bfloat16, device=dev)
+    else:
+        _check_rows(out, "out", torch.bfloat16, rows, N, dev)
+    b, bal = _check_segments(desc, layout, balance, slots_per_rank, dev)
+    with _on_device(dev):
+        rc = _lib.moe_expert_gemm(_made_once(desc), b, bal, slots_per_rank, x.data_ptr(), H, w.data_ptr(), N, act, _ptr(pre),
+                                  out.data_ptr(), _stream(stream, dev))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_expert_gemm")
+    return out
+
+
+def moe_expert_gemm_backward_x(desc: LayoutDesc, layout: Layout, d_out: torch.Tensor, w: torch.Tensor, pre=None, out=None,
+                               balance: Optional[Balance] = None, slots_per_rank: int = 0, stream=None) -> torch.Tensor:
+    """Gradient of a product's rows: d_out [max_recv,N] times w [E,N,H] -> [max_recv,H] bf16.
+
+    With ``pre`` [max_recv,2H], of the SWIGLU product that made those rows, the
+    gradient goes on through the activation to pre: [max_recv,2H] (which may be
+    pre itself).  Rows that hold no entry are neither read nor written."""
+    dev, rows = d_out.device, _product_rows(desc, "moe_expert_gemm_backward_x")
+    N = d_out.shape[-1]
+    _check_rows(d_out, "d_out", torch.bfloat16, rows, N, dev)
+    if w.dim() != 3:
+        raise ValueError(f"w: shape {tuple(w.shape)}, expected [E, N, H]")
+    H = w.shape[2]
+    _check(w, "w", torch.bfloat16, (desc.E, N, H), dev)
+    width = H
+    if pre is not None:
+        width = 2 * H
+        _check_rows(pre, "pre", torch.bfloat16, rows, width, dev)
+    if out is None:
+        with _alloc_on(stream):
+            out = torch.empty(rows, width, dtype=torch.bfloat16, device=dev)
+    else:
+        _check_rows(out, "out", torch.bfloat16, rows, width, dev)
+    b, bal = _check_segments(desc, layout, balance, slots_per_rank, dev)
+    with _on_device(dev):
+        rc = _lib.moe_expert_gemm_backward_x(_made_once(desc), b, bal, slots_per_rank, d_out.data_ptr(), N, w.data_ptr(), H,
+                                             _ptr(pre), out.data_ptr(), _stream(stream, dev))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_expert_gemm_backward_x")
+    return out
+
+
+def moe_expert_gemm_backward_w(desc: LayoutDesc, layout: Layout, d_out: torch.Tensor, x: torch.Tensor, out=None,
+                               dtype=torch.bfloat16, balance: Optional[Balance] = None, slots_per_rank: int = 0,
+                               stream=None) -> torch.Tensor:
+    """Gradient of a product's weights: [E,N,H] in ``dtype`` (bf16 or fp32; of
+    ``out`` if it is given) from d_out [max_recv,N] and the rows x [max_recv,H].
+    Every element is written, 0 for an expert without a row."""
+    dev, rows = x.device, _product_rows(desc, "moe_expert_gemm_backward_w")
+    N, H = d_out.shape[-1], x.shape[-1]
+    _check_rows(d_out, "d_out", torch.bfloat16, rows, N, dev)
+    _check_rows(x, "x", torch.bfloat16, rows, H, dev)
+    if out is None:
+        if dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError(f"dtype {dtype}, expected bfloat16 or float32")
+        with _alloc_on(stream):
+            out = torch.empty(desc.E, N, H, dtype=dtype, device=dev)
+    else:
+        _check(out, "out", (torch.bfloat16, torch.float32), (desc.E, N, H), dev)
+    b, bal = _check_segments(desc, layout, balance, slots_per_rank, dev)
+    with _on_device(dev):
+        rc = _lib.moe_expert_gemm_backward_w(_made_once(desc), b, bal, slots_per_rank, d_out.data_ptr(), N, x.data_ptr(), H,
+                                             MOE_F32 if out.dtype is torch.float32 else MOE_BF16, out.data_ptr(),
+                                             _stream(stream, dev))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_expert_gemm_backward_w")
+    return out
+
+
+def moe_combine_backward(desc: LayoutDesc, layout: Layout, d_out: torch.Tensor, expert_out=None, w=None, d_expert_out=None,
+                         d_w=None, rows: bool = True, weights: bool = True, stream=None):
+    """Gradient of moe_combine: (d_expert_out [max_recv,H] bf16 or None, d_w
+    [S,K] fp32 or None) from d_out [S,H] bf16; ``rows`` and ``weights`` say
+    which of the two are wanted.  d_w needs expert_out; w None: weight 1.
+    d_expert_out may be expert_out itself; rows that hold no entry are neither
+    read nor written."""
+    dev, n, H = d_out.device, _product_rows(desc, "moe_combine_backward"), d_out.shape[-1]
+    _check(d_out, "d_out", torch.bfloat16, (desc.S, H))
+    _check(w, "w", torch.float32, (desc.S, desc.K), dev)
+    _check(layout.pos, "layout.pos", torch.int32, (desc.S, desc.K), dev)
+    if weights:
+        if expert_out is None:
+            raise ValueError("d_w needs expert_out")
+        _check_rows(expert_out, "expert_out", torch.bfloat16, n, H, dev)
+    with _alloc_on(stream):
+        if not rows:
+            d_expert_out = None
+        elif d_expert_out is None:
+            d_expert_out = torch.empty(n, H, dtype=torch.bfloat16, device=dev)
+        else:
+            _check_rows(d_expert_out, "d_expert_out", torch.bfloat16, n, H, dev)
+        if not weights:
+            d_w = None
+        elif d_w is None:
+            d_w = torch.empty(desc.S, desc.K, dtype=torch.float32, device=dev)
+        else:
+            _check(d_w, "d_w", torch.float32, (desc.S, desc.K), dev)
+    b = moe_layout_bufs(pos=layout.pos.data_ptr())
+    with _on_device(dev):
+        rc = _lib.moe_combine_backward(_made_once(desc), ctypes.byref(b), d_out.data_ptr(), H,
+                                       _ptr(expert_out) if weights else None, _ptr(w), _ptr(d_expert_out), _ptr(d_w),
+                                       _stream(stream, dev))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_combine_backward")
+    return d_expert_out, d_w
+
+
+def moe_quantize_i8(x: torch.Tensor, codes=None, scales=None, layout: Optional[Layout] = None, stream=None):
+    """bf16 rows [..,H] -> 8-bit integers: (codes [..,H] int8, scales [..] fp32),
+    a scale per row: per token of activations, per output channel of weights
+    [E,N,H].  With ``layout`` only the rows that hold an entry are converted."""
+    dev, H = x.device, x.shape[-1]
+    _check(x, "x", torch.bfloat16)
+    if H < 16 or H % 16:
+        raise MoeError(MOE_ERR_SHAPE, "moe_quantize_i8")
+    rows = x.numel() // H
+    src = _check_src(layout, rows, dev)
+    lead = x.shape[:-1]
+    with _alloc_on(stream):
+        if codes is None:
+            codes = torch.empty(*lead, H, dtype=torch.int8, device=dev)
+        else:
+            _check(codes, "codes", torch.int8, x.shape, dev)
+        if scales is None:
+            scales = torch.empty(lead, dtype=torch.float32, device=dev)
+        else:
+            _check(scales, "scales", torch.float32, lead, dev)
+    with _on_device(dev):
+        rc = _lib.moe_quantize_i8(x.data_ptr(), rows, H, _ptr(src), codes.data_ptr(), scales.data_ptr(), _stream(stream, dev))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_quantize_i8")
+    return codes, scales
+
+
+def moe_dequantize_i8(codes: torch.Tensor, scales: torch.Tensor, out=None, layout: Optional[Layout] = None, stream=None):
+    """8-bit rows -> bf16 [..,H].  With ``layout`` only the rows that hold an
+    entry are converted; the others keep what they held."""
+    dev, H = codes.device, codes.shape[-1]
+    _check(codes, "codes", torch.int8)
+    if H < 16 or H % 16:
+        raise MoeError(MOE_ERR_SHAPE, "moe_dequantize_i8")
+    _check(scales, "scales", torch.float32, codes.shape[:-1], dev)
+    rows = codes.numel() // H
+    src = _check_src(layout, rows, dev)
+    if out is None:
+        with _alloc_on(stream):
+            out = torch.empty(codes.shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _check(out, "out", torch.bfloat16, codes.shape, dev)
+    with _on_device(dev):
+        rc = _lib.moe_dequantize_i8(codes.data_ptr(), scales.data_ptr(), rows, H, _ptr(src), out.data_ptr(), _stream(stream, dev))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_dequantize_i8")
+    return out
+
+
+def moe_dispatch_i8(desc: LayoutDesc, layout: Layout, hidden: torch.Tensor, topk_w=None, recv=None, recv_scales=None,
+                    recv_w=None, stream=None):
+    """moe_dispatch in 8-bit integers.  Returns (recv [max_recv,H] int8,
+    recv_scales [max_recv] fp32, recv_w or None)."""
+    dev, H, rows = hidden.device, hidden.shape[-1], _product_rows(desc, "moe_dispatch_i8")
+    _check(hidden, "hidden", torch.bfloat16, (desc.S, H))
+    _check(topk_w, "topk_w", torch.float32, (desc.S, desc.K), dev)
+    _check(layout.pos, "layout.pos", torch.int32, (desc.S, desc.K), dev)
+    with _alloc_on(stream):
+        if recv is None:
+            recv = torch.empty(rows, H, dtype=torch.int8, device=dev)
+        else:
+            _check_rows(recv, "recv", torch.int8, rows, H, dev)
+        if recv_scales is None:
+            recv_scales = torch.empty(rows, dtype=torch.float32, device=dev)
+        if recv_w is None and topk_w is not None:
+            recv_w = torch.empty(rows, dtype=torch.float32, device=dev)
+    for t, name in ((recv_scales, "recv_scales"), (recv_w, "recv_w")):
+        _check(t, name, torch.float32, None, dev)
+        if t is not None and t.numel() < rows:
+            raise ValueError(f"{name}: {t.numel()} rows, expected at least {rows}")
+    b = moe_layout_bufs(pos=layout.pos.data_ptr())
+    with _on_device(dev):
+        rc = _lib.moe_dispatch_i8(_made_once(desc), ctypes.byref(b), hidden.data_ptr(), H, _ptr(topk_w), recv.data_ptr(),
+                                  recv_scales.data_ptr(), _ptr(recv_w), _stream(stream, dev))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_dispatch_i8")
+    return recv, recv_scales, recv_w
+
+
+def moe_expert_gemm_i8(desc: LayoutDesc, layout: Layout, x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor,
+                       w_scales: torch.Tensor, act: int = MOE_ACT_NONE, out=None, balance: Optional[Balance] = None,
+                       slots_per_rank: int = 0, stream=None) -> torch.Tensor:
+    """Every expert's 8-bit rows times its 8-bit weights: out [max_recv,N] bf16.
+
+    x [max_recv,H] int8 and x_scales [max_recv] fp32; w [E,M,H] int8 and
+    w_scales [E,M] fp32, M = N, or 2N with MOE_ACT_SWIGLU (N gate rows, then N up
+    rows).  Rows that hold no entry are neither read nor written."""
+    dev, rows = x.device, _product_rows(desc, "moe_expert_gemm_i8")
+    H, N, M = _gemm_shape(desc, x, w, act, torch.int8, "moe_expert_gemm_i8")
+    _check_rows(x, "x", torch.int8, rows, H, dev)
+    _check(x_scales, "x_scales", torch.float32, None, dev)
+    if x_scales.dim() != 1 or x_scales.numel() < rows:
+        raise ValueError(f"x_scales: shape {tuple(x_scales.shape)}, expected [at least {rows}]")
+    _check(w_scales, "w_scales", torch.float32, (desc.E, M), dev)
+    if out is None:
+        with _alloc_on(stream):
+            out = torch.empty(rows, N, dtype=torch.bfloat16, device=dev)
+    else:
+        _check_rows(out, "out", torch.bfloat16, rows, N, dev)
+    b, bal = _check_segments(desc, layout, balance, slots_per_rank, dev)
+    with _on_device(dev):
+        rc = _lib.moe_expert_gemm_i8(_made_once(desc), b, bal, slots_per_rank, x.data_ptr(), x_scales.data_ptr(), H, w.data_ptr(),
+                                     w_scales.data_ptr(), N, act, out.data_ptr(), _stream(stream, dev))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_expert_gemm_i8")
+    return out
+
+
+class _DispatchFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, hidden, desc, layout):
+        ctx.desc = desc
+        ctx.save_for_backward(layout.pos)
+        recv = moe_dispatch(desc, layout, hidden)[0]
+        moe_zero_padding(desc, layout, recv)
+        return recv
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d):
+        _no_capture("the backward pass of dispatch")
+        pos, = ctx.saved_tensors
+        return moe_combine(ctx.desc, _only(pos=pos), d.contiguous()), None, None
+
+
+class _ExpertFfnFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w_in, w_out, desc, layout, balance, slots):
+        rows, M = _product_rows(desc, "expert_ffn"), w_in.shape[1]
+        pre = torch.empty(rows, M, dtype=torch.bfloat16, device=x.device)
+        h = moe_expert_gemm(desc, layout, x, w_in, MOE_ACT_SWIGLU, pre=pre, balance=balance, slots_per_rank=slots)
+        y = moe_expert_gemm(desc, layout, h, w_out, balance=balance, slots_per_rank=slots)
+        moe_zero_padding(desc, layout, y)
+        ctx.desc, ctx.slots, ctx.balanced = desc, slots, balance is not None
+        seg = (balance.seg_offset, balance.slot_expert) if balance is not None else (None, None)
+        ctx.save_for_backward(x, w_in, w_out, h, pre, layout.tokens_per_expert, layout.expert_offset, layout.src, *seg)
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        _no_capture("the backward pass of expert_ffn")
+        x, w_in, w_out, h, pre, count, offset, src, seg, slot_expert = ctx.saved_tensors
+        layout = _only(tokens_per_expert=count, expert_offset=offset, src=src)
+        balance = Balance(seg, slot_expert, None) if ctx.balanced else None
+        at = dict(balance=balance, slots_per_rank=ctx.slots)
+        want_x, want_in, want_out = ctx.needs_input_grad[:3]
+        dy = dy.contiguous()
+        dx = dw_in = dw_out = None
+        if want_out:
+            dw_out = moe_expert_gemm_backward_w(ctx.desc, layout, dy, h, **at)
+        if want_x or want_in:
+            d_pre = moe_expert_gemm_backward_x(ctx.desc, layout, dy, w_out, pre=pre, **at)
+        if want_in:
+            dw_in = moe_expert_gemm_backward_w(ctx.desc, layout, d_pre, x, **at)
+        if want_x:
+            dx = moe_expert_gemm_backward_x(ctx.desc, layout, d_pre, w_in, **at)
+            moe_zero_padding(ctx.desc, layout, dx)
+        return dx, dw_in, dw_out, None, None, None, None
+
+
+class _CombineFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, expert_out, w, shared_out, desc, layout):
+        ctx.desc = desc
+        ctx.save_for_backward(expert_out, w, layout.pos, layout.src)
+        return moe_combine(desc, layout, expert_out, w, shared_out)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d):
+        _no_capture("the backward pass of combine")
+        expert_out, w, pos, src = ctx.saved_tensors
+        want_y, want_w, want_shared = ctx.needs_input_grad[:3]
+        d = d.contiguous()
+        dy = dw = None
+        if want_y or want_w:
+            layout = _only(pos=pos, src=src)
+            dy, dw = moe_combine_backward(ctx.desc, layout, d, expert_out, w, rows=want_y, weights=want_w)
+            if want_y:
+                moe_zero_padding(ctx.desc, layout, dy)
+        return dy, dw, d if want_shared else None, None, None
+
+
+def _only(**arrays) -> Layout:
+    """A layout of which a call reads these arrays alone."""
+    return Layout(**{f.name: arrays.get(f.name) for f in dataclasses.fields(Layout)})
+
+
+def dispatch(desc: LayoutDesc, layout: Layout, hidden: torch.Tensor) -> torch.Tensor:
+    """moe_dispatch in bf16 as an autograd function of hidden: the receive rows
+    [max_recv,H], those that hold no entry zero.  As for router, not capturable
+    (nor are expert_ffn and combine); the layout must stay as it is until the
+    backward pass has run."""
+    _no_capture("dispatch")
+    with _on_device(hidden.device):
+        return _DispatchFunction.apply(hidden, desc, layout)
+
+
+def expert_ffn(desc: LayoutDesc, layout: Layout, x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor,
+               balance: Optional[Balance] = None, slots_per_rank: int = 0) -> torch.Tensor:
+    """The experts' gated feed-forward block as an autograd function of its rows
+    x [max_recv,H] and of the weights w_in [E,2N,H] (N gate rows, then N up rows) and
+    w_out [E,H',N], all bf16: moe_expert_gemm twice.  Rows that hold no entry are
+    zero, in the result and in x's gradient."""
+    _no_capture("expert_ffn")
+    _check(x, "x", torch.bfloat16, (_product_rows(desc, "expert_ffn"), x.shape[-1]))
+    _check(layout.src, "layout.src", torch.int32, (x.shape[0],), x.device)
+    with _on_device(x.device):
+        return _ExpertFfnFunction.apply(x, w_in, w_out, desc, layout, balance, slots_per_rank)
+
+
+def combine(desc: LayoutDesc, layout: Layout, expert_out: torch.Tensor, w=None, shared_out=None) -> torch.Tensor:
+    """moe_combine as an autograd function of the experts' rows, the route
+    weights and the shared output."""
+    _no_capture("combine")
+    _check(expert_out, "expert_out", torch.bfloat16, (_product_rows(desc, "combine"), expert_out.shape[-1]))
+    _check(layout.src, "layout.src", torch.int32, (expert_out.shape[0],), expert_out.device)
+    with _on_device(expert_out.device):
+        return _CombineFunction.apply(expert_out, w, shared_out, desc, layout)
+
+
+# ---------------------------------------------------------------------------
 # Static-shape buffer: validate once, then bare C calls
 # ---------------------------------------------------------------------------
 
@@ -877,26 +1281,31 @@ class Buffer:
 
     With ``mx4`` the rows travel in MXFP4 (recv [rows,H/2] and recv_scales
     [rows,H/32], both uint8; moe_dispatch_mx4), and expert_gemm multiplies them
-    with the experts' weights, with either layout.
+    with the experts' weights, with either layout.  With ``i8`` they travel in
+    8-bit integers (recv [rows,H] int8, recv_scales [rows] fp32; moe_dispatch_i8).
     """
 
     def __init__(self, S: int, H: int, K: int, E: int, R: int, fp8: bool = False,
                  pad_mode: int = MOE_PAD_NONE, pad_rows: int = 0, device="cuda",
-                 balance_slots: Optional[int] = None, mx4: bool = False):
+                 balance_slots: Optional[int] = None, mx4: bool = False, i8: bool = False):
         if balance_slots is not None and pad_mode != MOE_PAD_NONE:
             raise MoeError(MOE_ERR_SHAPE, "Buffer: the balanced layout has no padding")
         self.desc = LayoutDesc(S, K, E, R, pad_mode, pad_rows)
         self.rows = moe_max_recv_rows(self.desc)
-        if self.rows < 0 or H < 8 or H % 8 or ((fp8 or mx4) and H % 128) or (fp8 and mx4):
+        if self.rows < 0 or H < 8 or H % 8 or ((fp8 or mx4) and H % 128) or (i8 and H % 16) or \
+                fp8 + mx4 + i8 > 1:
             raise MoeError(MOE_ERR_SHAPE, "Buffer")
         dev = torch.device(device)
         if dev.type == "cuda" and dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
-        self.H, self.fp8, self.mx4, self.device, self._index = H, fp8, mx4, dev, dev.index
+        self.H, self.fp8, self.mx4, self.i8, self.device, self._index = H, fp8, mx4, i8, dev, dev.index
         self.layout = alloc_layout(self.desc, dev)
         if mx4:
             self.recv = torch.empty((self.rows, H // 2), dtype=torch.uint8, device=dev)
             self.recv_scales = torch.empty((self.rows, H // 32), dtype=torch.uint8, device=dev)
+        elif i8:
+            self.recv = torch.empty((self.rows, H), dtype=torch.int8, device=dev)
+            self.recv_scales = torch.empty(self.rows, dtype=torch.float32, device=dev)
         else:
             self.recv = torch.empty((self.rows, H), dtype=torch.uint8 if fp8 else torch.bfloat16, device=dev)
             self.recv_scales = torch.empty((self.rows, H // 128), dtype=torch.float32, device=dev) if fp8 else None
@@ -953,11 +1362,12 @@ class Buffer:
                 return self.dispatch_call(hidden, topk_idx, topk_w, stream, check)
         if check:
             self._inputs(hidden, topk_idx, topk_w)
-        if self.mx4:
-            rc = _lib.moe_dispatch_mx4(self._dp, self._bp, _ptr(hidden), self.H, _ptr(topk_w), self._recv, self._scales,
-                                       self._recv_w if topk_w is not None else None, _stream(stream, self.device))
+        if self.mx4 or self.i8:
+            call = _lib.moe_dispatch_mx4 if self.mx4 else _lib.moe_dispatch_i8
+            rc = call(self._dp, self._bp, _ptr(hidden), self.H, _ptr(topk_w), self._recv, self._scales,
+                      self._recv_w if topk_w is not None else None, _stream(stream, self.device))
             if rc != MOE_OK:
-                raise MoeError(rc, "moe_dispatch_mx4")
+                raise MoeError(rc, "moe_dispatch_mx4" if self.mx4 else "moe_dispatch_i8")
             return
         rc = _lib.moe_dispatch(self._dp, self._bp, _ptr(hidden), self.H, _ptr(topk_idx), _ptr(topk_w),
                                1 if self.fp8 else 0, self._recv, self._scales,
@@ -967,13 +1377,13 @@ class Buffer:
 
     def layout_dispatch_call(self, hidden, topk_idx, topk_w=None, stream=None, check=True):
         """moe_layout_dispatch: one launch for decode-sized batches (with a
-        balanced layout or MXFP4 rows: the layout, then the dispatch)."""
+        balanced layout, MXFP4 or 8-bit rows: the layout, then the dispatch)."""
         if self._index != _raw_current_device():
             with torch.cuda.device(self.device):
                 return self.layout_dispatch_call(hidden, topk_idx, topk_w, stream, check)
         if check:
             self._inputs(hidden, topk_idx, topk_w)
-        if self.balance is not None or self.mx4:
+        if self.balance is not None or self.mx4 or self.i8:
             self.layout_call(topk_idx, stream, check=False)
             self.dispatch_call(hidden, topk_idx, topk_w, stream, check=False)
             return
@@ -998,8 +1408,8 @@ class Buffer:
 
     def zero_padding_call(self, stream=None):
         """moe_zero_padding on this buffer's receive rows (after a dispatch; not
-        for MXFP4 rows, whose consumers skip padding)."""
-        if self.mx4:
+        for MXFP4 and 8-bit rows, whose consumers skip padding)."""
+        if self.mx4 or self.i8:
             raise MoeError(MOE_ERR_SHAPE, "moe_zero_padding")
         if self._index != _raw_current_device():
             with torch.cuda.device(self.device):
@@ -1019,13 +1429,20 @@ class Buffer:
         self.combine_call(expert_out, w, shared_out, stream)
         return self.out
 
-    def expert_gemm(self, w, w_scales, act: int = MOE_ACT_NONE, x=None, x_scales=None, out=None, stream=None):
-        """moe_expert_gemm_mx4 on the rows of the last dispatch, or on x and
-        x_scales (MXFP4 rows in the same order, such as the previous product's
-        result through moe_quantize_mx4).  Returns [rows,N] bf16."""
+    def expert_gemm(self, w, w_scales=None, act: int = MOE_ACT_NONE, x=None, x_scales=None, out=None, stream=None):
+        """The experts' product in the weights' format, MXFP4 (uint8), 8-bit integers
+        (int8) or bf16 (no scales): moe_expert_gemm_mx4, moe_expert_gemm_i8 or
+        moe_expert_gemm on the rows of the last dispatch, or on x and x_scales (rows of
+        that format in the same order, such as the previous product's result,
+        quantised).  Returns [rows,N] bf16."""
+        mx4, i8 = w.dtype is torch.uint8, w.dtype is torch.int8
         if x is None:
-            if not self.mx4:
-                raise MoeError(MOE_ERR_SHAPE, "Buffer.expert_gemm: the receive rows are not MXFP4")
+            if self.fp8 or (self.mx4, self.i8) != (mx4, i8):
+                raise MoeError(MOE_ERR_SHAPE, "Buffer.expert_gemm: the receive rows have another format than the weights")
             x, x_scales = self.recv, self.recv_scales
-        return moe_expert_gemm_mx4(self.desc, self.layout, x, x_scales, w, w_scales, act, out, self.balance,
-                                   self.slots or 0, stream)
+        if mx4 or i8:
+            call = moe_expert_gemm_mx4 if mx4 else moe_expert_gemm_i8
+            return call(self.desc, self.layout, x, x_scales, w, w_scales, act, out, self.balance, self.slots or 0, stream)
+        if w_scales is not None or x_scales is not None:
+            raise ValueError("bf16 rows and weights have no scales")
+        return moe_expert_gemm(self.desc, self.layout, x, w, act, out, None, self.balance, self.slots or 0, stream)

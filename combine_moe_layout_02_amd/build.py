@@ -21,7 +21,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmoe_ep.so")
 SOURCES = ["api.hip", "layout.hip", "dispatch.hip", "combine.hip", "fused.hip", "balance.hip", "padding.hip", "router.hip",
-           "mx4.hip", "expert_gemm.hip"]
+           "mx4.hip", "expert_gemm.hip", "expert_products.hip", "int8.hip", "combine_backward.hip"]
 CEIL_LIB = os.path.join(HERE, "libmoe_ceilings.so")
 CEIL_SOURCES = ["ceilings.hip"]
 ARCH = "gfx950"

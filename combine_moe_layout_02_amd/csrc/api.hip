@@ -8,7 +8,10 @@
 #include <atomic>
 #include <vector>
 
+#include "combine_backward.h"
 #include "expert_gemm.h"
+#include "expert_products.h"
+#include "int8.h"
 #include "moe_ep.h"
 #include "moe_kernels.h"
 #include "mx4.h"
@@ -430,6 +433,57 @@ bool mx4_rows_ok(int64_t rows, int32_t H) {
     return H >= 128 && H % 128 == 0 && rows >= 0 && rows <= ((moe::kMaxLaunchThreads >> 8 << 8) * 32) / H;
 }
 
+// Sizes of a product's segments; false outside the limits.
+bool segments_of(const moe_layout_desc *desc, const moe_balance_bufs *bal, int32_t slots_per_rank, moe::Segments &g) {
+    if (!desc_ok(desc) || max_rows(desc) < 0) return false;
+    if (bal == nullptr ? slots_per_rank != 0
+                       : (desc->pad_mode != MOE_PAD_NONE || slots_per_rank < 0 || slots_per_rank > moe::kMaxSlotsPerRank ||
+                          static_cast<int64_t>(desc->R) * slots_per_rank > moe::kMaxBalanceSlots))
+        return false;
+    g.E = desc->E;
+    g.R = desc->R;
+    g.B = slots_per_rank;
+    g.nseg = desc->E + (bal != nullptr ? desc->R * slots_per_rank : 0);
+    g.entries = static_cast<int64_t>(desc->S) * desc->K;
+    g.max_count = desc->pad_mode == MOE_PAD_CAPACITY ? std::min<int64_t>(g.entries, desc->pad_rows) : g.entries;
+    return true;
+}
+
+// Where its segments lie.
+moe_status segment_arrays(const moe_layout_bufs *layout, const moe_balance_bufs *bal, int32_t slots_per_rank, moe::Segments &g) {
+    if (bal != nullptr) {
+        if (bal->seg_offset == nullptr || (slots_per_rank > 0 && bal->slot_expert == nullptr)) return MOE_ERR_NULL;
+        if (!aligned(bal->seg_offset, 4) || !aligned(bal->slot_expert, 4)) return MOE_ERR_ALIGN;
+        g.seg_offset = bal->seg_offset;
+        g.slot_expert = bal->slot_expert;
+    } else {
+        if (layout->tokens_per_expert == nullptr || layout->expert_offset == nullptr) return MOE_ERR_NULL;
+        if (!aligned(layout->tokens_per_expert, 4) || !aligned(layout->expert_offset, 4)) return MOE_ERR_ALIGN;
+        g.count = layout->tokens_per_expert;
+        g.offset = layout->expert_offset;
+    }
+    return MOE_OK;
+}
+
+bool channels_ok(int32_t n, int32_t multiple) { return n >= multiple && n % multiple == 0 && n <= moe::kMaxGemmChannels; }
+
+// A bf16 or 8-bit product whose formats and channels are in `a` and were found
+// in order.
+moe_status run_product(const moe_layout_desc *desc, const moe_layout_bufs *layout, const moe_balance_bufs *bal,
+                       int32_t slots_per_rank, moe::ProductArgs &a, void *stream) {
+    if (!segments_of(desc, bal, slots_per_rank, a) || !moe::product_grid_ok(a)) return MOE_ERR_SHAPE;
+    const bool i8 = a.kind == moe::Product::kForwardI8, weights = a.kind == moe::Product::kBackwardW;
+    if (desc->S == 0 && !weights) return MOE_OK;
+    if (a.out == nullptr || (desc->S > 0 && (a.x == nullptr || a.w == nullptr))) return MOE_ERR_NULL;
+    if (i8 && (a.xs == nullptr || a.ws == nullptr)) return MOE_ERR_NULL;
+    const moe_status st = segment_arrays(layout, bal, slots_per_rank, a);
+    if (st != MOE_OK) return st;
+    if (!aligned(a.x, 16) || !aligned(a.w, 16) || !aligned(a.out, 16) || !aligned(a.pre, 16) || !aligned(a.pre_in, 16) ||
+        !aligned(a.xs, 4) || !aligned(a.ws, 4))
+        return MOE_ERR_ALIGN;
+    return moe::launch_product(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
 }  // namespace
 
 extern "C" {
@@ -519,15 +573,10 @@ moe_status moe_expert_gemm_mx4(const moe_layout_desc *desc, const moe_layout_buf
                                const uint8_t *x_scales, int32_t H, const void *w, const uint8_t *w_scales, int32_t N,
                                int32_t act, void *out, void *stream) {
     if (desc == nullptr || layout == nullptr) return MOE_ERR_NULL;
-    if (!desc_ok(desc) || max_rows(desc) < 0 || H < 128 || H % 128 != 0 || N < 8 || N % 8 != 0 ||
-        H > moe::kMaxGemmChannels || N > moe::kMaxGemmChannels)
-        return MOE_ERR_SHAPE;
+    if (H < 128 || H % 128 != 0 || !channels_ok(N, 8) || H > moe::kMaxGemmChannels) return MOE_ERR_SHAPE;
     if (act != MOE_ACT_NONE && act != MOE_ACT_SWIGLU) return MOE_ERR_SHAPE;
-    if (bal == nullptr ? slots_per_rank != 0
-                       : (desc->pad_mode != MOE_PAD_NONE || slots_per_rank < 0 || slots_per_rank > moe::kMaxSlotsPerRank ||
-                          static_cast<int64_t>(desc->R) * slots_per_rank > moe::kMaxBalanceSlots))
-        return MOE_ERR_SHAPE;
     moe::ExpertGemmArgs a{};
+    if (!segments_of(desc, bal, slots_per_rank, a)) return MOE_ERR_SHAPE;
     a.x = static_cast<const uint8_t *>(x);
     a.xs = x_scales;
     a.w = static_cast<const uint8_t *>(w);
@@ -536,29 +585,130 @@ moe_status moe_expert_gemm_mx4(const moe_layout_desc *desc, const moe_layout_buf
     a.H = H;
     a.N = N;
     a.swiglu = act == MOE_ACT_SWIGLU;
-    a.E = desc->E;
-    a.R = desc->R;
-    a.B = slots_per_rank;
-    a.nseg = desc->E + (bal != nullptr ? desc->R * slots_per_rank : 0);
-    a.entries = static_cast<int64_t>(desc->S) * desc->K;
-    a.max_count = desc->pad_mode == MOE_PAD_CAPACITY ? std::min<int64_t>(a.entries, desc->pad_rows) : a.entries;
     if (!moe::expert_gemm_grid_ok(a)) return MOE_ERR_SHAPE;
     if (desc->S == 0) return MOE_OK;
     if (x == nullptr || x_scales == nullptr || w == nullptr || w_scales == nullptr || out == nullptr) return MOE_ERR_NULL;
-    if (bal != nullptr) {
-        if (bal->seg_offset == nullptr || (slots_per_rank > 0 && bal->slot_expert == nullptr)) return MOE_ERR_NULL;
-        if (!aligned(bal->seg_offset, 4) || !aligned(bal->slot_expert, 4)) return MOE_ERR_ALIGN;
-        a.seg_offset = bal->seg_offset;
-        a.slot_expert = bal->slot_expert;
-    } else {
-        if (layout->tokens_per_expert == nullptr || layout->expert_offset == nullptr) return MOE_ERR_NULL;
-        if (!aligned(layout->tokens_per_expert, 4) || !aligned(layout->expert_offset, 4)) return MOE_ERR_ALIGN;
-        a.count = layout->tokens_per_expert;
-        a.offset = layout->expert_offset;
-    }
+    const moe_status st = segment_arrays(layout, bal, slots_per_rank, a);
+    if (st != MOE_OK) return st;
     if (!aligned(x, 16) || !aligned(w, 16) || !aligned(out, 16) || !aligned(x_scales, 4) || !aligned(w_scales, 4))
         return MOE_ERR_ALIGN;
     return moe::launch_expert_gemm_mx4(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+moe_status moe_expert_gemm(const moe_layout_desc *desc, const moe_layout_bufs *layout, const moe_balance_bufs *bal,
+                           int32_t slots_per_rank, const void *x, int32_t H, const void *w, int32_t N, int32_t act, void *pre,
+                           void *out, void *stream) {
+    if (desc == nullptr || layout == nullptr) return MOE_ERR_NULL;
+    if (!channels_ok(H, 8) || !channels_ok(N, 8) || (act != MOE_ACT_NONE && act != MOE_ACT_SWIGLU)) return MOE_ERR_SHAPE;
+    if (act == MOE_ACT_NONE && pre != nullptr) return MOE_ERR_SHAPE;
+    moe::ProductArgs a{};
+    a.kind = moe::Product::kForward;
+    a.gated = act == MOE_ACT_SWIGLU;
+    a.inner = H;
+    a.cols = N;
+    a.x = x;
+    a.w = w;
+    a.pre = pre;
+    a.out = out;
+    return run_product(desc, layout, bal, slots_per_rank, a, stream);
+}
+
+moe_status moe_expert_gemm_backward_x(const moe_layout_desc *desc, const moe_layout_bufs *layout, const moe_balance_bufs *bal,
+                                      int32_t slots_per_rank, const void *d_out, int32_t N, const void *w, int32_t H,
+                                      const void *pre, void *dx, void *stream) {
+    if (desc == nullptr || layout == nullptr) return MOE_ERR_NULL;
+    if (!channels_ok(H, 8) || !channels_ok(N, 8)) return MOE_ERR_SHAPE;
+    moe::ProductArgs a{};
+    a.kind = moe::Product::kBackwardX;
+    a.gated = pre != nullptr;
+    a.inner = N;
+    a.cols = H;
+    a.x = d_out;
+    a.w = w;
+    a.pre_in = pre;
+    a.out = dx;
+    return run_product(desc, layout, bal, slots_per_rank, a, stream);
+}
+
+moe_status moe_expert_gemm_backward_w(const moe_layout_desc *desc, const moe_layout_bufs *layout, const moe_balance_bufs *bal,
+                                      int32_t slots_per_rank, const void *d_out, int32_t N, const void *x, int32_t H,
+                                      int32_t dw_type, void *dw, void *stream) {
+    if (desc == nullptr || layout == nullptr) return MOE_ERR_NULL;
+    if (!channels_ok(H, 8) || !channels_ok(N, 8) || (dw_type != MOE_F32 && dw_type != MOE_BF16)) return MOE_ERR_SHAPE;
+    moe::ProductArgs a{};
+    a.kind = moe::Product::kBackwardW;
+    a.out_f32 = dw_type == MOE_F32;
+    a.inner = N;
+    a.cols = H;
+    a.x = d_out;
+    a.w = x;
+    a.out = dw;
+    return run_product(desc, layout, bal, slots_per_rank, a, stream);
+}
+
+moe_status moe_expert_gemm_i8(const moe_layout_desc *desc, const moe_layout_bufs *layout, const moe_balance_bufs *bal,
+                              int32_t slots_per_rank, const void *x, const float *x_scales, int32_t H, const void *w,
+                              const float *w_scales, int32_t N, int32_t act, void *out, void *stream) {
+    if (desc == nullptr || layout == nullptr) return MOE_ERR_NULL;
+    if (!channels_ok(H, 16) || H > moe::kMaxInt8Inner || !channels_ok(N, 8) || (act != MOE_ACT_NONE && act != MOE_ACT_SWIGLU))
+        return MOE_ERR_SHAPE;
+    moe::ProductArgs a{};
+    a.kind = moe::Product::kForwardI8;
+    a.gated = act == MOE_ACT_SWIGLU;
+    a.inner = H;
+    a.cols = N;
+    a.x = x;
+    a.w = w;
+    a.xs = x_scales;
+    a.ws = w_scales;
+    a.out = out;
+    return run_product(desc, layout, bal, slots_per_rank, a, stream);
+}
+
+moe_status moe_quantize_i8(const void *x, int64_t rows, int32_t H, const int32_t *src, void *codes, float *scales, void *stream) {
+    if (!moe::int8_rows_ok(rows, H)) return MOE_ERR_SHAPE;
+    if (rows == 0) return MOE_OK;
+    if (x == nullptr || codes == nullptr || scales == nullptr) return MOE_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(src, 4) || !aligned(scales, 4)) return MOE_ERR_ALIGN;
+    const moe::QuantizeI8Args a{x, rows, H, src, codes, scales};
+    return moe::launch_quantize_i8(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+moe_status moe_dequantize_i8(const void *codes, const float *scales, int64_t rows, int32_t H, const int32_t *src, void *out,
+                             void *stream) {
+    if (!moe::int8_rows_ok(rows, H)) return MOE_ERR_SHAPE;
+    if (rows == 0) return MOE_OK;
+    if (codes == nullptr || scales == nullptr || out == nullptr) return MOE_ERR_NULL;
+    if (!aligned(codes, 16) || !aligned(out, 16) || !aligned(src, 4) || !aligned(scales, 4)) return MOE_ERR_ALIGN;
+    const moe::DequantizeI8Args a{codes, scales, rows, H, src, out};
+    return moe::launch_dequantize_i8(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+moe_status moe_dispatch_i8(const moe_layout_desc *desc, const moe_layout_bufs *layout, const void *hidden, int32_t H,
+                           const float *topk_w, void *recv, float *recv_scales, float *recv_w, void *stream) {
+    if (desc == nullptr || layout == nullptr) return MOE_ERR_NULL;
+    if (!desc_ok(desc) || max_rows(desc) < 0 || !moe::int8_rows_ok(desc->S, H)) return MOE_ERR_SHAPE;
+    if (desc->S == 0) return MOE_OK;
+    if (hidden == nullptr || recv == nullptr || recv_scales == nullptr || layout->pos == nullptr) return MOE_ERR_NULL;
+    if (!aligned(hidden, 16) || !aligned(recv, 16) || !aligned(recv_scales, 4) || !aligned(topk_w, 4) || !aligned(recv_w, 4) ||
+        !aligned(layout->pos, 4))
+        return MOE_ERR_ALIGN;
+    const moe::DispatchI8Args a{hidden, desc->S, H, desc->K, layout->pos, topk_w, recv, recv_scales, recv_w};
+    return moe::launch_dispatch_i8(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+moe_status moe_combine_backward(const moe_layout_desc *desc, const moe_layout_bufs *layout, const void *d_out, int32_t H,
+                                const void *expert_out, const float *w, void *d_expert_out, float *d_w, void *stream) {
+    if (desc == nullptr || layout == nullptr) return MOE_ERR_NULL;
+    if (!desc_ok(desc) || max_rows(desc) < 0 || !channels_ok(H, 8) || !moe::combine_backward_grid_ok(desc->S)) return MOE_ERR_SHAPE;
+    if (d_expert_out == nullptr && d_w == nullptr) return MOE_ERR_NULL;
+    if (desc->S == 0) return MOE_OK;
+    if (d_out == nullptr || layout->pos == nullptr || (d_w != nullptr && expert_out == nullptr)) return MOE_ERR_NULL;
+    if (!aligned(d_out, 16) || !aligned(expert_out, 16) || !aligned(d_expert_out, 16) || !aligned(w, 4) || !aligned(d_w, 4) ||
+        !aligned(layout->pos, 4))
+        return MOE_ERR_ALIGN;
+    const moe::CombineBackwardArgs a{d_out, desc->S, H, desc->K, layout->pos, expert_out, w, d_expert_out, d_w};
+    return moe::launch_combine_backward(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
 const char *moe_status_str(int32_t status) {

@@ -19,7 +19,10 @@
  * (moe_balance_loss, moe_router_backward).  Between dispatch and combine,
  * moe_dispatch_mx4 carries the rows in microscaled 4-bit floating point
  * (MXFP4), moe_quantize_mx4 / moe_dequantize_mx4 convert rows, and
- * moe_expert_gemm_mx4 multiplies every expert's rows with its weights.
+ * moe_expert_gemm_mx4 multiplies every expert's rows with its weights.  The same
+ * in 8-bit integers: moe_dispatch_i8, moe_quantize_i8 / moe_dequantize_i8,
+ * moe_expert_gemm_i8.  In bf16, with what training needs: moe_expert_gemm,
+ * moe_expert_gemm_backward_x / _w, moe_combine_backward.
  *
  * Around them: moe_layout_dispatch (layout + dispatch in one launch for
  * decode-sized batches), moe_layout_balanced (every rank receives the same
@@ -443,6 +446,110 @@ moe_status moe_expert_gemm_mx4(const moe_layout_desc *desc, const moe_layout_buf
                                const moe_balance_bufs *bal, int32_t slots_per_rank, const void *x,
                                const uint8_t *x_scales, int32_t H, const void *w, const uint8_t *w_scales, int32_t N,
                                int32_t act, void *out, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * The experts in bf16: products and their gradients
+ * ------------------------------------------------------------------------- */
+
+/* moe_expert_gemm_mx4's products in bf16: for every row r that holds an entry,
+ * of expert e,
+ *   MOE_ACT_NONE    out[r,n] = bf16( sum_h x[r,h] * w[e,n,h] ),  n < N
+ *   MOE_ACT_SWIGLU  out[r,n] = bf16( silu(g) * u ), g = sum_h x[r,h] * w[e,n,h],
+ *                   u = sum_h x[r,h] * w[e,N+n,h]
+ * with fp32 sums.  The two make an expert's gated feed-forward block:
+ * MOE_ACT_SWIGLU with its gate and up weights, MOE_ACT_NONE with its down weights.
+ *   x         [max_recv,H], H % 8 == 0.
+ *   w         [E,M,H], M = N or (SWIGLU) 2*N; N % 8 == 0.
+ *   pre       [max_recv,2*N] or NULL, with SWIGLU only: bf16(g), then bf16(u) of
+ *             every row, as moe_expert_gemm_backward_x takes them.
+ *   out       [max_recv,N].
+ *   layout, bal, slots_per_rank as for moe_expert_gemm_mx4.
+ * H and N are at most 2^22; all row arrays 16-byte aligned.  Rows that hold no
+ * entry are neither read nor written.  No workspace; the grid depends on the
+ * shape alone: MOE_ERR_SHAPE where a launch cannot number it (this holds for
+ * the calls below too); it always can with (S*K/16 + segments that can hold a
+ * row) * ceil(M/32) at most 2^23 - 8. */
+moe_status moe_expert_gemm(const moe_layout_desc *desc, const moe_layout_bufs *layout, const moe_balance_bufs *bal,
+                           int32_t slots_per_rank, const void *x, int32_t H, const void *w, int32_t N, int32_t act, void *pre,
+                           void *out, void *stream);
+
+/* Gradient of a product with respect to its rows, from d_out [max_recv,N] bf16
+ * and the weights w [E,N,H] of the MOE_ACT_NONE product (of a SWIGLU one: N
+ * counts gate and up rows, d_out is the gradient of its pre):
+ *   pre NULL  dx[r,h] = bf16( sum_n d_out[r,n] * w[e,n,h] ),  dx [max_recv,H]
+ *   pre given [max_recv,2*H], of the SWIGLU product that made the rows x: the
+ *             gradient goes on through the activation to pre itself.  With d the
+ *             sum above in fp32, g = pre[r,h], u = pre[r,H+h], s = 1/(1+exp(-g)):
+ *             dx[r,h] = bf16( d*u*s*(1 + g*(1-s)) ), dx[r,H+h] = bf16( d*g*s ),
+ *             dx [max_recv,2*H]; it may be pre's own buffer.
+ * The values at g = -inf or +inf are NaN.  Arguments otherwise as above. */
+moe_status moe_expert_gemm_backward_x(const moe_layout_desc *desc, const moe_layout_bufs *layout, const moe_balance_bufs *bal,
+                                      int32_t slots_per_rank, const void *d_out, int32_t N, const void *w, int32_t H,
+                                      const void *pre, void *dx, void *stream);
+
+/* Gradient of a product with respect to its weights:
+ *   dw[e,n,h] = sum over the rows r of expert e, replicas' rows too, of
+ *               d_out[r,n] * x[r,h]
+ * d_out [max_recv,N], x [max_recv,H], both bf16; dw [E,N,H], bf16 or fp32
+ * (dw_type), fp32 sums.  Every element is written, 0 for an expert without a
+ * row.  The order of a sum is fixed by the layout.  Always taken:
+ * E*ceil(N/64)*ceil(H/64) at most 2^24 - 16. */
+moe_status moe_expert_gemm_backward_w(const moe_layout_desc *desc, const moe_layout_bufs *layout, const moe_balance_bufs *bal,
+                                      int32_t slots_per_rank, const void *d_out, int32_t N, const void *x, int32_t H,
+                                      int32_t dw_type, void *dw, void *stream);
+
+/* Gradient of moe_combine, out[t] = sum_k w[t,k] * expert_out[pos[t,k]] (+ shared_out):
+ *   d_expert_out  [max_recv,H] bf16 or NULL: row pos[t,k] gets bf16(w[t,k] * d_out[t]);
+ *                 it may be expert_out's own buffer.
+ *   d_w           [S,K] fp32 or NULL: sum_c d_out[t,c] * expert_out[pos[t,k],c] in
+ *                 fp32, 0 where pos[t,k] is -1; needs expert_out.
+ * At least one of the two.  d_out [S,H] bf16 (it is shared_out's gradient too);
+ * w [S,K] fp32 or NULL for weight 1; H % 8 == 0, at most 2^22; S below 2^23.  Rows that hold
+ * no entry are neither read nor written.  (The gradient of moe_dispatch's rows
+ * with respect to hidden is moe_combine of them with w = NULL.) */
+moe_status moe_combine_backward(const moe_layout_desc *desc, const moe_layout_bufs *layout, const void *d_out, int32_t H,
+                                const void *expert_out, const float *w, void *d_expert_out, float *d_w, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * 8-bit integers: rows with one scale each, and the experts' products
+ * ------------------------------------------------------------------------- */
+
+/* An 8-bit row of H channels (H % 16 == 0, at most 2^22): H codes (int8) and one fp32 scale,
+ * amax/127; code = round(x / scale), ties to the even code, both divisions
+ * correctly rounded in fp32, within +-127.  A row of zeros has scale 0 and codes
+ * 0, a row with a NaN or an infinity scale NaN and codes 0.
+ *
+ * bf16 rows -> 8-bit rows (activations with a scale per token, or weights with
+ * a scale per output channel).
+ *   x       [rows,H] bf16, codes [rows,H] int8, 16-byte aligned both.
+ *   src     [rows] or NULL: with a layout's src only the rows that hold an
+ *           entry (src[r] >= 0) are read and written.
+ *   scales  [rows] fp32.
+ * rows at most 2^23 - 8. */
+moe_status moe_quantize_i8(const void *x, int64_t rows, int32_t H, const int32_t *src, void *codes, float *scales, void *stream);
+
+/* 8-bit rows -> bf16: bf16(code * scale), the product in fp32.  Arguments and
+ * limits as in moe_quantize_i8. */
+moe_status moe_dequantize_i8(const void *codes, const float *scales, int64_t rows, int32_t H, const int32_t *src, void *out,
+                             void *stream);
+
+/* moe_dispatch in 8-bit integers: row pos[t,k] of the receive buffer gets
+ * token t's row as moe_quantize_i8 rounds it.  recv [max_recv,H] int8, 16-byte
+ * aligned; recv_scales [max_recv] fp32; other arguments as in moe_dispatch; S
+ * at most 2^23 - 8.  Rows that no entry maps to are not written. */
+moe_status moe_dispatch_i8(const moe_layout_desc *desc, const moe_layout_bufs *layout, const void *hidden, int32_t H,
+                           const float *topk_w, void *recv, float *recv_scales, float *recv_w, void *stream);
+
+/* moe_expert_gemm in 8-bit integers, with a scale for each row and each
+ * channel: the sum over h of x[r,h] * w[e,n,h] is exact (32 bits, H at most
+ * 131056), becomes fp32 and is multiplied by x_scales[r], then by w_scales[e,n];
+ * SWIGLU as there, of two such values; one rounding to bf16.
+ *   x [max_recv,H] int8, x_scales [max_recv] fp32; H % 16 == 0.
+ *   w [E,M,H] int8, w_scales [E,M] fp32.
+ * Arguments and limits otherwise as in moe_expert_gemm. */
+moe_status moe_expert_gemm_i8(const moe_layout_desc *desc, const moe_layout_bufs *layout, const moe_balance_bufs *bal,
+                              int32_t slots_per_rank, const void *x, const float *x_scales, int32_t H, const void *w,
+                              const float *w_scales, int32_t N, int32_t act, void *out, void *stream);
 
 /* Static string naming a moe_status value. */
 const char *moe_status_str(int32_t status);
