@@ -471,6 +471,9 @@ bool channels_ok(int32_t n, int32_t multiple) { return n >= multiple && n % mult
 // in order.
 moe_status run_product(const moe_layout_desc *desc, const moe_layout_bufs *layout, const moe_balance_bufs *bal,
                        int32_t slots_per_rank, moe::ProductArgs &a, void *stream) {
+    // a tile's 256 rows of out lie within 32-bit offsets of each other
+    const bool wide = a.gated || a.out_f32;
+    if (wide && a.cols > moe::kMaxGemmChannels / 2) return MOE_ERR_SHAPE;
     if (!segments_of(desc, bal, slots_per_rank, a) || !moe::product_grid_ok(a)) return MOE_ERR_SHAPE;
     const bool i8 = a.kind == moe::Product::kForwardI8, weights = a.kind == moe::Product::kBackwardW;
     if (desc->S == 0 && !weights) return MOE_OK;

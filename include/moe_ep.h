@@ -464,7 +464,7 @@ moe_status moe_expert_gemm_mx4(const moe_layout_desc *desc, const moe_layout_buf
  *             every row, as moe_expert_gemm_backward_x takes them.
  *   out       [max_recv,N].
  *   layout, bal, slots_per_rank as for moe_expert_gemm_mx4.
- * H and N are at most 2^22; all row arrays 16-byte aligned.  Rows that hold no
+ * H and M are at most 2^22; all row arrays 16-byte aligned.  Rows that hold no
  * entry are neither read nor written.  No workspace; the grid depends on the
  * shape alone: MOE_ERR_SHAPE where a launch cannot number it (this holds for
  * the calls below too); it always can with (S*K/16 + segments that can hold a
@@ -481,7 +481,7 @@ moe_status moe_expert_gemm(const moe_layout_desc *desc, const moe_layout_bufs *l
  *             gradient goes on through the activation to pre itself.  With d the
  *             sum above in fp32, g = pre[r,h], u = pre[r,H+h], s = 1/(1+exp(-g)):
  *             dx[r,h] = bf16( d*u*s*(1 + g*(1-s)) ), dx[r,H+h] = bf16( d*g*s ),
- *             dx [max_recv,2*H]; it may be pre's own buffer.
+ *             dx [max_recv,2*H], H at most 2^21; it may be pre's own buffer.
  * The values at g = -inf or +inf are NaN.  Arguments otherwise as above. */
 moe_status moe_expert_gemm_backward_x(const moe_layout_desc *desc, const moe_layout_bufs *layout, const moe_balance_bufs *bal,
                                       int32_t slots_per_rank, const void *d_out, int32_t N, const void *w, int32_t H,
@@ -491,7 +491,7 @@ moe_status moe_expert_gemm_backward_x(const moe_layout_desc *desc, const moe_lay
  *   dw[e,n,h] = sum over the rows r of expert e, replicas' rows too, of
  *               d_out[r,n] * x[r,h]
  * d_out [max_recv,N], x [max_recv,H], both bf16; dw [E,N,H], bf16 or fp32
- * (dw_type), fp32 sums.  Every element is written, 0 for an expert without a
+ * (dw_type; then H at most 2^21), fp32 sums.  Every element is written, 0 for an expert without a
  * row.  The order of a sum is fixed by the layout.  Always taken:
  * E*ceil(N/64)*ceil(H/64) at most 2^24 - 16. */
 moe_status moe_expert_gemm_backward_w(const moe_layout_desc *desc, const moe_layout_bufs *layout, const moe_balance_bufs *bal,

@@ -81,6 +81,14 @@ def test_what_only_some_take(moe):
     assert call(moe, "forward", act=1, pre=FAKE + 8) == moe.MOE_ERR_ALIGN
     assert call(moe, "backward_x", pre=FAKE + 8) == moe.MOE_ERR_ALIGN
     assert call(moe, "backward_w", dtype=2) == moe.MOE_ERR_SHAPE
+    # rows of more than 2^23 bytes of results
+    most = 1 << 21
+    for which, kw in (("forward", dict(N=most, act=1)), ("int8", dict(N=most, act=1)), ("backward_x", dict(H=most, pre=FAKE)),
+                      ("backward_w", dict(H=most, dtype=0))):
+        assert call(moe, which, out=None, **kw) == moe.MOE_ERR_NULL
+        size = "N" if "N" in kw else "H"
+        assert call(moe, which, out=None, **{**kw, size: most + 8}) == moe.MOE_ERR_SHAPE
+    assert call(moe, "backward_w", H=1 << 22, dtype=1, out=None) == moe.MOE_ERR_NULL
     assert call(moe, "int8", H=72) == moe.MOE_ERR_SHAPE
     assert call(moe, "int8", H=131072) == moe.MOE_ERR_SHAPE             # 131072 * 128 * 128 passes 32 bits
     assert call(moe, "int8", H=131056, x=None) == moe.MOE_ERR_NULL
