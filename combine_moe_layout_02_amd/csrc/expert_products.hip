@@ -51,15 +51,18 @@ __device__ __forceinline__ void gated_gradient(float g, float u, float dh, float
 
 // A tile is up to 256 rows q by 256 channels c.  One workgroup of eight waves per
 // CU takes tile after tile; each wave holds 128 x 64 (128 accumulator registers),
-// or for at most 128 rows all of them by 32 channels.  A stage, 128 bytes of k of
-// every row (64 rows of k where those are the memory's rows), 64 KB, is copied to
-// LDS while the stage before it is multiplied; it has two steps of 64 bytes.
+// or for at most 128 rows all of them by 32 channels.  A stage is 64 bytes of k of
+// every row (32 rows of k where those are the memory's rows), one matrix
+// instruction deep, 32 KB; four buffers: while one stage is multiplied the next
+// three are on their way, across tiles too.
 constexpr int kGemmWaves = 8;
 constexpr int kGemmThreads = kGemmWaves * kWave;
 constexpr int kTileCols = 256;
-constexpr int kOperandVecs = 2048;             // 16-byte vectors of one operand's stage
+constexpr int kOperandVecs = 1024;             // 16-byte vectors of one operand's stage
 constexpr int kPairVecs = 2 * kOperandVecs;    // X, then W
-constexpr int kStageK = 64;                    // rows of k of a stage of a transposed operand
+constexpr int kStageKBytes = 64;               // bytes of k of a stage
+constexpr int kStageK = 32;                    // rows of k of a stage of a transposed operand
+constexpr int kCopies = 4;                     // copies of a wave and stage: two of X, two of W
 
 template <Product KIND>
 struct Form {
@@ -76,11 +79,15 @@ struct Form {
 // wave reads are in eight different groups of banks.
 __device__ __forceinline__ int k_turn(int k) { return (k & 3) | (k >> 1 & 4); }
 
-// Where a lane's operands lie.  K neighbours: row i*16 + r of the wave's, chunk
-// 4h + g at (4h + g) ^ (r % 8).
+// K neighbours: rows lie at a pitch of 64 bytes, chunk c (16 bytes) of row q at
+// c ^ chunk_turn(q): eight and sixteen neighbouring rows' chunk c are in different
+// groups of banks.
+__device__ __forceinline__ int chunk_turn(int q) { return q >> 1 & 2; }
+
+// Where a lane's operands lie.  K neighbours: row i*16 + r of the wave's, chunk g.
 template <bool BY_K>
 struct Reader {
-    int at[2];
+    int at;
     unsigned int base;
     __device__ __forceinline__ Reader(int first, int lane) {   // the wave's first row (of 16 * a power of two)
         const int r = lane & 15, g = lane >> 4;
@@ -88,24 +95,32 @@ struct Reader {
             const int k = 8 * g + r / 4;
             base = static_cast<unsigned int>(k * 512 + ((first / 16) ^ k_turn(k)) * 32 + (r & 3) * 8);
         } else {
-            at[0] = (first + r) * 8 + (g ^ (r & 7));
-            at[1] = (first + r) * 8 + ((4 + g) ^ (r & 7));
+            at = (first + r) * 4 + (g ^ chunk_turn(r));
         }
     }
-    __device__ __forceinline__ u32x4 operator()(const u32x4 *stage, int h, int i) const {
+    __device__ __forceinline__ u32x4 operator()(const u32x4 *stage, int i) const {
         if constexpr (BY_K) {
             typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-            const char *const p = reinterpret_cast<const char *>(stage) + (base ^ static_cast<unsigned int>(i * 32)) + h * 16384;
-            // rows 8g .. 8g+3 of the step, then 8g+4 .. 8g+7
+            const char *const p = reinterpret_cast<const char *>(stage) + (base ^ static_cast<unsigned int>(i * 32));
+            // rows 8g .. 8g+3 of the stage, then 8g+4 .. 8g+7
             const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p));
             const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 2048));
             const u32x2 a = __builtin_bit_cast(u32x2, lo), b = __builtin_bit_cast(u32x2, hi);
             return u32x4{a[0], a[1], b[0], b[1]};
         } else {
-            return stage[at[h] + i * 128];
+            return stage[at + i * 64];
         }
     }
 };
+
+// The same in every lane: keeps descriptors and branches on the scalar side.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+__device__ __forceinline__ const char *uniform(const char *p) {
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    const uint64_t lo = static_cast<uint32_t>(uniform(static_cast<int>(v))), hi = static_cast<uint32_t>(uniform(static_cast<int>(v >> 32)));
+    return reinterpret_cast<const char *>(hi << 32 | lo);
+}
 
 struct ProductTile {
     int row0, rows;    // rows q: of the receive buffer, or (kBackwardW) n
@@ -114,22 +129,30 @@ struct ProductTile {
     int first, end;    // kBackwardW: the expert's rows, but for its replicas'
 };
 
-// Asks for a tile's stages, one after the other.
+// Asks for a tile's stages, one after the other; past the last one for zeros.
 template <Product KIND, bool GATED>
 struct Feed {
     using F = Form<KIND>;
     static constexpr bool kSplit = F::kForward && GATED;
     unsigned int xo, wo;                 // this lane's first offsets
-    __amdgpu_buffer_rsrc_t x, gate, up;  // K neighbours: the tile's rows; gate, then up weights
-    const char *xk, *wk;                 // rows of k: the next stage's first
+    // K neighbours: X's first row, and of W the first row of each of the wave's two
+    // copies, with the bytes from there to the tile's end; rows of k: the next stage's
+    // first row and the tile's bytes of each row
+    const char *x, *w, *w1;
+    unsigned int x_bytes, w_bytes, w1_bytes;
     int left;                            // rows of k, or bytes of k, not asked for yet
-    int s;                               // stage
+    int at;                              // bytes of k asked for
     int slot;                            // kBackwardW, balanced: replica slots looked at
 
-    __device__ __forceinline__ bool next_run(const ProductArgs &a, const ProductTile &t) {
-        if (a.seg_offset == nullptr) return false;
+    // kBackwardW: rows first .. end-1 of the receive buffer
+    __device__ __forceinline__ void run(const ProductArgs &a, const ProductTile &t, int first, int end) {
+        left = uniform(end - first);
+        x = static_cast<const char *>(a.x) + (static_cast<size_t>(uniform(first)) * a.inner + t.row0) * 2;
+        w = static_cast<const char *>(a.w) + (static_cast<size_t>(uniform(first)) * a.cols + t.c0) * 2;
+    }
+    __device__ __forceinline__ void next_run(const ProductArgs &a, const ProductTile &t) {
         const int lane = threadIdx.x & (kWave - 1), slots = a.R * a.B;
-        while (slot < slots) {
+        while (left <= 0 && slot < slots) {
             const int i = slot + lane;
             const uint64_t mine = __ballot(i < slots && a.slot_expert[min(i, slots - 1)] == t.expert);
             if (mine == 0) {
@@ -140,124 +163,122 @@ struct Feed {
             slot = found + 1;
             const int epr = a.E / a.R, seg = found / a.B * (epr + a.B) + epr + found % a.B;
             run(a, t, a.seg_offset[seg], a.seg_offset[seg + 1]);
-            if (left > 0) return true;
         }
-        return false;
-    }
-    __device__ __forceinline__ void run(const ProductArgs &a, const ProductTile &t, int first, int end) {
-        first = __builtin_amdgcn_readfirstlane(first);
-        left = __builtin_amdgcn_readfirstlane(end) - first;
-        xk = static_cast<const char *>(a.x) + static_cast<size_t>(first) * a.inner * 2 + static_cast<size_t>(t.row0) * 2;
-        wk = static_cast<const char *>(a.w) + static_cast<size_t>(first) * a.cols * 2 + static_cast<size_t>(t.c0) * 2;
     }
 
+    // A tile's first stage comes next.
     __device__ __forceinline__ void start(const ProductArgs &a, const ProductTile &t) {
         const int lane = threadIdx.x & (kWave - 1);
-        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+        const int wave = uniform(static_cast<int>(threadIdx.x) / kWave);
         const unsigned int xb = static_cast<unsigned int>(a.inner) * F::kSize, cb = static_cast<unsigned int>(a.cols) * 2;
-        // of eight rows of k neighbours: row lane/8, its chunk; of two rows of k: row
+        // of 16 rows of k neighbours: row lane/4, its chunk; of two rows of k: row
         // lane/32, its chunk (copy_k() has the rows that this wave takes)
+        const unsigned int chunk = ((lane & 3) ^ chunk_turn(lane / 4)) * 16;
         const int k = 2 * (wave & 1) + 8 * (wave >> 1 & 1) + 4 * (wave >> 2) + lane / 32;
         const unsigned int k_chunk = ((lane & 31) ^ (2 * k_turn(k))) * 16;
-        s = 0;
+        at = 0;
         slot = 0;
         if constexpr (KIND == Product::kBackwardW) {
             xo = k * xb + k_chunk;
             wo = k * cb + k_chunk;
+            x_bytes = min(512u, xb - static_cast<unsigned int>(t.row0) * 2);
+            w_bytes = min(512u, cb - static_cast<unsigned int>(t.c0) * 2);
             run(a, t, t.first, t.end);
+            if (a.seg_offset != nullptr) next_run(a, t);
         } else {
-            x = buffer_of(static_cast<const char *>(a.x) + static_cast<size_t>(t.row0) * xb, t.rows * xb);
-            xo = (wave * 8 + lane / 8) * xb + lane_chunk(lane);
+            x = static_cast<const char *>(a.x) + static_cast<size_t>(t.row0) * xb;
+            x_bytes = t.rows * xb;
+            xo = (wave * 16 + lane / 4) * xb + chunk;
             if constexpr (F::kForward) {
                 left = static_cast<int>(xb);
-                const unsigned int wrows = min(kSplit ? kTileCols / 2 : kTileCols, a.cols - t.c0);
+                // the wave copies 32 rows of W's place in LDS; gated, the second half of the
+                // rows that one wave multiplies (64, or 32 for at most 128 rows q) are the up
+                // weights of the first
+                const bool wide = t.rows > 128;
+                const int row = !kSplit ? wave * 32 : (wide ? (wave >> 1) * 32 : wave * 16), row1 = kSplit && !wide ? row : row + 16;
+                const bool up = kSplit && wide && (wave & 1), up1 = kSplit && (!wide || (wave & 1));
+                const int rows = min(kSplit ? kTileCols / 2 : kTileCols, a.cols - t.c0);
                 const char *const first = static_cast<const char *>(a.w) + (static_cast<size_t>(t.expert) * (kSplit ? 2 : 1) * a.cols + t.c0) * xb;
-                gate = buffer_of(first, wrows * xb);
-                up = kSplit ? buffer_of(first + static_cast<size_t>(a.cols) * xb, wrows * xb) : gate;
-                wo = lane / 8 * xb + lane_chunk(lane);
+                w = first + (static_cast<size_t>(up ? a.cols : 0) + row) * xb;
+                w1 = first + (static_cast<size_t>(up1 ? a.cols : 0) + row1) * xb;
+                w_bytes = max(rows - row, 0) * xb;
+                w1_bytes = max(rows - row1, 0) * xb;
+                wo = lane / 4 * xb + chunk;
             } else {
                 left = a.inner;
-                wk = static_cast<const char *>(a.w) + static_cast<size_t>(t.expert) * a.inner * cb + static_cast<size_t>(t.c0) * 2;
+                w_bytes = min(512u, cb - static_cast<unsigned int>(t.c0) * 2);
+                w = static_cast<const char *>(a.w) + (static_cast<size_t>(t.expert) * a.inner * a.cols + t.c0) * 2;
                 wo = k * cb + k_chunk;
             }
         }
     }
+    // No tile comes next: zeros.
+    __device__ __forceinline__ void stop() { left = 0; }
 
-    // Rows of k `n` (at most 64) from `from`: the wave's copies take two rows each,
-    // with the same turn.  Rows past the last read zeros.
-    __device__ __forceinline__ void copy_k(const char *from, int n, unsigned int row_bytes, unsigned int first, u32x4 *to) const {
-        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-        // the first row begins at the tile's column: what follows it in memory belongs
-        // to the buffer as far as the last row's end of the columns asked for
-        const auto b = buffer_of(from, n > 0 ? static_cast<unsigned int>(n - 1) * row_bytes + k_bytes : 0u);
+    // Rows of k `n` (at most 32) from `from`: the wave's copies take two rows each,
+    // with the same turn.  Rows past the last read zeros; `bytes` of the last row
+    // belong to the tile.
+    __device__ __forceinline__ static void copy_k(const char *from, int n, unsigned int bytes, unsigned int row_bytes, unsigned int first, u32x4 *to) {
+        const int wave = uniform(static_cast<int>(threadIdx.x) / kWave);
+        const auto b = buffer_of(uniform(from), n > 0 ? static_cast<unsigned int>(n - 1) * row_bytes + bytes : 0u);
         const int k0 = 2 * (wave & 1) + 8 * (wave >> 1 & 1) + 4 * (wave >> 2);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int dk = 16 * j;
-            copy_to_lds(b, to + (k0 + dk) * 32, first + dk * row_bytes, 0);
-        }
-    }
-    unsigned int k_bytes;
-
-    // Whether there is another stage.
-    __device__ __forceinline__ bool have(const ProductArgs &a, const ProductTile &t) {
-        if constexpr (KIND == Product::kBackwardW)
-            return left > 0 || next_run(a, t);
-        else
-            return left > 0;
-    }
-    __device__ __forceinline__ void step(const ProductArgs &a) {
-        if constexpr (F::kXByK) xk += static_cast<size_t>(kStageK) * a.inner * 2;
-        if constexpr (F::kWByK) wk += static_cast<size_t>(kStageK) * a.cols * 2;
-        left -= F::kForward ? kStageBytes : kStageK;
-        ++s;
+        for (int j = 0; j < 2; ++j) copy_to_lds(b, to + (k0 + 16 * j) * 32, first + 16 * j * row_bytes, 0);
     }
 
-    // Asks for the next stage, if there is one, into `stage`; false if there is none.
-    // XCOPIES: 8 rows of X per wave and copy.
-    template <int XCOPIES>
-    __device__ __forceinline__ bool copy(const ProductArgs &a, const ProductTile &t, u32x4 *stage, int wave_cols) {
+    // Asks for the next stage, into `stage`.
+    __device__ __forceinline__ void copy(const ProductArgs &a, const ProductTile &t, u32x4 *stage) {
         const int lane = threadIdx.x & (kWave - 1);
-        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-        if (!have(a, t)) return false;
+        const int wave = uniform(static_cast<int>(threadIdx.x) / kWave);
         const unsigned int xb = static_cast<unsigned int>(a.inner) * F::kSize, cb = static_cast<unsigned int>(a.cols) * 2;
         unsigned int x_lane = xo, w_lane = wo;
         asm volatile("" : "+v"(x_lane), "+v"(w_lane));    // offsets are made here, not kept in a register each
+        const int rows = uniform(min(left, kStageK));     // of k, where the memory's rows are k
         if constexpr (F::kXByK) {
-            const int n = min(left, kStageK);
-            k_bytes = min(512u, xb - static_cast<unsigned int>(t.row0) * 2);
-            copy_k(xk, n, xb, x_lane, stage);
-            k_bytes = min(512u, cb - static_cast<unsigned int>(t.c0) * 2);
-            copy_k(wk, n, cb, w_lane, stage + kOperandVecs);
+            copy_k(x, rows, uniform(x_bytes), xb, x_lane, stage);
+            x += static_cast<size_t>(kStageK) * xb;
         } else {
             const int bytes = F::kForward ? left : 2 * left;      // of k, from this stage on
-            const unsigned int gone = static_cast<int>(lane_chunk(lane)) >= bytes ? kPastEnd : 0u;
+            const unsigned int gone = static_cast<int>(((lane & 3) ^ chunk_turn(lane / 4)) * 16) >= bytes ? kPastEnd : 0u;
+            const auto from = buffer_of(uniform(x), uniform(x_bytes));
 #pragma unroll
-            for (int j = 0; j < XCOPIES; ++j)
-                copy_to_lds(x, stage + (j * kGemmWaves + wave) * 64, (x_lane + j * kGemmWaves * 8 * xb) | gone, s * kStageBytes);
+            for (int j = 0; j < 2; ++j)
+                copy_to_lds(from, stage + (j * kGemmWaves + wave) * 64, (x_lane + j * kGemmWaves * 16 * xb) | gone, uniform(at));
             if constexpr (F::kForward) {
-                // 32 rows of the tile; gated, the second half of a wave's channels (wave_cols)
-                // are the up rows of the first
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    int row = wave * 32 + j * 8;
-                    bool is_up = false;
-                    if constexpr (kSplit) {
-                        const int half = wave_cols / 2, of = row / wave_cols * half, in = row % wave_cols;
-                        is_up = in >= half;
-                        row = of + in - (is_up ? half : 0);
-                    }
-                    copy_to_lds(is_up ? up : gate, stage + kOperandVecs + (wave * 4 + j) * 64, (w_lane + row * xb) | gone, s * kStageBytes);
-                }
-            } else {
-                k_bytes = min(512u, cb - static_cast<unsigned int>(t.c0) * 2);
-                copy_k(wk, min(left, kStageK), cb, w_lane, stage + kOperandVecs);
+                copy_to_lds(buffer_of(uniform(w), uniform(w_bytes)), stage + kOperandVecs + wave * 128, w_lane | gone, uniform(at));
+                copy_to_lds(buffer_of(uniform(w1), uniform(w1_bytes)), stage + kOperandVecs + wave * 128 + 64, w_lane | gone, uniform(at));
             }
+            at += kStageKBytes;
         }
-        step(a);
-        return true;
+        if constexpr (F::kWByK) {
+            copy_k(w, rows, uniform(w_bytes), cb, w_lane, stage + kOperandVecs);
+            w += static_cast<size_t>(kStageK) * cb;
+        }
+        left -= F::kForward ? kStageKBytes : kStageK;
+        if constexpr (KIND == Product::kBackwardW) {
+            if (a.seg_offset != nullptr) next_run(a, t);
+        }
     }
 };
+
+// Stages of a tile.
+template <Product KIND>
+__device__ __forceinline__ int stages_of(const ProductArgs &a, const ProductTile &t) {
+    if constexpr (Form<KIND>::kForward) return (a.inner * Form<KIND>::kSize + kStageKBytes - 1) / kStageKBytes;
+    if constexpr (KIND == Product::kBackwardX) return (a.inner + kStageK - 1) / kStageK;
+    int n = (t.end - t.first + kStageK - 1) / kStageK;
+    if (a.seg_offset != nullptr) {
+        const int lane = threadIdx.x & (kWave - 1), slots = a.R * a.B, epr = a.E / a.R;
+        int mine = 0;
+        for (int i = lane; i < slots; i += kWave)
+            if (a.slot_expert[i] == t.expert) {
+                const int seg = i / a.B * (epr + a.B) + epr + i % a.B;
+                mine += (a.seg_offset[seg + 1] - a.seg_offset[seg] + kStageK - 1) / kStageK;
+            }
+        n += __builtin_amdgcn_readlane(wave_inclusive_scan(mine), kWave - 1);
+    }
+    return uniform(n);
+}
 
 // 16-byte chunk c of row q of a plane in LDS lies at c ^ turn(q), against bank
 // conflicts: rows of CHUNKS chunks.
@@ -270,24 +291,25 @@ __device__ __forceinline__ void plane_put(u32x4 *plane, int q, int i, int g, f32
     reinterpret_cast<u32x2 *>(plane)[(q * CHUNKS + ((2 * i + (g >> 1)) ^ plane_turn<CHUNKS>(q))) * 2 + (g & 1)] = pack_bf16x4(v);
 }
 
-// Stores 32 rows of a plane: channels c0 .. of rows `row_bytes` apart, from row q0
+// Stores ROWS rows of a plane: channels c0 .. of rows `row_bytes` apart, from row q0
 // of `to`.  Rows outside the tile fall past the buffer's end, channels past `cols`
 // are sent there.
-template <int CHUNKS>
+template <int CHUNKS, int ROWS>
 __device__ __forceinline__ void plane_store(const u32x4 *plane, __amdgpu_buffer_rsrc_t to, unsigned int row_bytes, int q0, int c0, int cols) {
     const int lane = threadIdx.x & (kWave - 1);
     constexpr int kRows = kWave / CHUNKS;
 #pragma unroll
-    for (int j = 0; j < 32 / kRows; ++j) {
+    for (int j = 0; j < (ROWS + kRows - 1) / kRows; ++j) {
         const int q = j * kRows + lane / CHUNKS, c = lane % CHUNKS;
-        const u32x4 v = plane[q * CHUNKS + (c ^ plane_turn<CHUNKS>(q))];
-        const unsigned int at = c0 + c * 8 < cols ? (q0 + q) * row_bytes + 2u * (c0 + c * 8) : kPastEnd;
+        const bool mine = ROWS % kRows == 0 || q < ROWS;
+        const u32x4 v = plane[mine ? q * CHUNKS + (c ^ plane_turn<CHUNKS>(q)) : 0];
+        const unsigned int at = mine && c0 + c * 8 < cols ? (q0 + q) * row_bytes + 2u * (c0 + c * 8) : kPastEnd;
         __builtin_amdgcn_raw_buffer_store_b128(v, to, static_cast<int>(at), 0, kNonTemporal);
     }
 }
 
 // What is done with a wave's sums: TT tiles of 16 rows from row q0 of the tile, WT
-// tiles of 16 channels; n0: the first channel.  `mine`: 8 KB of LDS.
+// tiles of 16 channels; n0: the first channel.  `mine`: 4 KB of LDS.
 template <int TT, int WT, Product KIND, bool GATED>
 __device__ __forceinline__ void finish(const ProductArgs &a, const ProductTile &t, Acc<Form<KIND>::kI8> (&acc)[TT][WT], int q0, int n0,
                                        u32x4 *mine) {
@@ -319,21 +341,16 @@ __device__ __forceinline__ void finish(const ProductArgs &a, const ProductTile &
         const auto pre = buffer_of(static_cast<const char *>(a.pre_in) + first * row_bytes * 2, static_cast<unsigned int>(t.rows) * row_bytes * 2);
         const auto to = buffer_of(static_cast<char *>(a.out) + first * row_bytes * 2, static_cast<unsigned int>(t.rows) * row_bytes * 2);
 #pragma unroll
-        for (int m0 = 0; m0 < TT; m0 += 2) {
+        for (int m = 0; m < TT; ++m) {
 #pragma unroll
-            for (int m = m0; m < m0 + 2; ++m)
-#pragma unroll
-                for (int i = 0; i < WT; ++i) {
-                    const int q = (m - m0) * 16 + r;
-                    mine[q * kF + ((4 * i + g) ^ (r & (kF - 1)))] = __builtin_bit_cast(u32x4, acc[m][i]);
-                }
+            for (int i = 0; i < WT; ++i) mine[r * kF + ((4 * i + g) ^ (r & (kF - 1)))] = __builtin_bit_cast(u32x4, acc[m][i]);
             wave_lds_fence();
 #pragma unroll
-            for (int j = 0; j < 32 / kRowsAt; ++j) {
+            for (int j = 0; j < 16 / kRowsAt; ++j) {
                 const int q = j * kRowsAt + lane / (2 * WT), c = lane % (2 * WT);
-                const f32x4 lo = __builtin_bit_cast(f32x4, mine[q * kF + ((2 * c) ^ (q & 15 & (kF - 1)))]);
-                const f32x4 hi = __builtin_bit_cast(f32x4, mine[q * kF + ((2 * c + 1) ^ (q & 15 & (kF - 1)))]);
-                const unsigned int at = n0 + c * 8 < a.cols ? (q0 + m0 * 16 + q) * row_bytes * 2 + 2u * (n0 + c * 8) : kPastEnd;
+                const f32x4 lo = __builtin_bit_cast(f32x4, mine[q * kF + ((2 * c) ^ (q & (kF - 1)))]);
+                const f32x4 hi = __builtin_bit_cast(f32x4, mine[q * kF + ((2 * c + 1) ^ (q & (kF - 1)))]);
+                const unsigned int at = n0 + c * 8 < a.cols ? (q0 + m * 16 + q) * row_bytes * 2 + 2u * (n0 + c * 8) : kPastEnd;
                 const unsigned int at_up = at == kPastEnd ? kPastEnd : at + row_bytes;
                 const u32x4 gv = __builtin_amdgcn_raw_buffer_load_b128(pre, static_cast<int>(at), 0, 0);
                 const u32x4 uv = __builtin_amdgcn_raw_buffer_load_b128(pre, static_cast<int>(at_up), 0, 0);
@@ -369,10 +386,11 @@ __device__ __forceinline__ void finish(const ProductArgs &a, const ProductTile &
                 for (int e = 0; e < 4; ++e) ws[i][e] = from[c + e];
         }
     }
+    constexpr int kAtOnce = kSplit ? 1 : 2, kPlane = kAtOnce * 16 * kChunks;   // row tiles at a time
 #pragma unroll
-    for (int m0 = 0; m0 < TT; m0 += 2) {
+    for (int m0 = 0; m0 < TT; m0 += kAtOnce) {
 #pragma unroll
-        for (int m = m0; m < m0 + 2; ++m) {
+        for (int m = m0; m < m0 + kAtOnce; ++m) {
             const int q = (m - m0) * 16 + r;
             float xs = 0.0f;
             if constexpr (F::kI8) {
@@ -392,8 +410,8 @@ __device__ __forceinline__ void finish(const ProductArgs &a, const ProductTile &
                 }
                 if constexpr (kSplit) {
                     if (keep) {
-                        plane_put<kChunks>(mine + 32 * kChunks, q, i, g, v);
-                        plane_put<kChunks>(mine + 64 * kChunks, q, i, g, u);
+                        plane_put<kChunks>(mine + kPlane, q, i, g, v);
+                        plane_put<kChunks>(mine + 2 * kPlane, q, i, g, u);
                     }
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v[e] = silu(v[e]) * u[e];
@@ -402,30 +420,48 @@ __device__ __forceinline__ void finish(const ProductArgs &a, const ProductTile &
             }
         }
         wave_lds_fence();
-        plane_store<kChunks>(mine, to, row_bytes, q0 + m0 * 16, n0, a.cols);
+        plane_store<kChunks, kAtOnce * 16>(mine, to, row_bytes, q0 + m0 * 16, n0, a.cols);
         if (keep) {
-            plane_store<kChunks>(mine + 32 * kChunks, pre, 2 * row_bytes, q0 + m0 * 16, n0, a.cols);
+            plane_store<kChunks, kAtOnce * 16>(mine + kPlane, pre, 2 * row_bytes, q0 + m0 * 16, n0, a.cols);
             // up values lie `cols` channels further
             const auto pre_up = buffer_of(static_cast<char *>(a.pre) + first * row_bytes * 2 + row_bytes, static_cast<unsigned int>(t.rows) * row_bytes * 2 - row_bytes);
-            plane_store<kChunks>(mine + 64 * kChunks, pre_up, 2 * row_bytes, q0 + m0 * 16, n0, a.cols);
+            plane_store<kChunks, kAtOnce * 16>(mine + 2 * kPlane, pre_up, 2 * row_bytes, q0 + m0 * 16, n0, a.cols);
         }
         wave_lds_fence();
     }
 }
 
-// One tile whose first stage, if it has one, is on its way to stage 0.
-// next_first() asks for the next tile's, into the same place.
-template <int TT, int WT, Product KIND, bool GATED, typename NextFirst>
-__device__ __forceinline__ void run_tile(const ProductArgs &a, const ProductTile &t, Feed<KIND, GATED> &feed, bool any, u32x4 *stage0,
-                                         u32x4 *stage1, NextFirst &&next_first) {
+// Waits until at most N of the wave's global loads, copies and stores are in
+// flight.  Loads return in order, so that with N = 2 * kCopies all but the two
+// stages asked for last have arrived.
+template <int N>
+__device__ __forceinline__ void copies_arrived() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4 << 14));   // vmcnt(N)
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+}
+
+// One tile whose first three stages have arrived in the buffers 0 to 2; the next
+// tile's are asked for when its own are.  Its stages are taken in fours: past the
+// last one zeros are multiplied.  next_tile() makes `feed` the next tile's.
+//
+// The two waves of a SIMD take turns: while one group of four waves multiplies the
+// other reads its operands of the next stage from LDS and asks for copies.  Each
+// half step ends with a barrier of the workgroup; the second group begins half a
+// step later.
+template <int TT, int WT, Product KIND, bool GATED, typename NextTile>
+__device__ __forceinline__ void run_tile(const ProductArgs &a, const ProductTile &t, const ProductTile &nt, Feed<KIND, GATED> &feed, int groups,
+                                         u32x4 *b0, u32x4 *b1, u32x4 *b2, u32x4 *b3, NextTile &&next_tile) {
     using F = Form<KIND>;
     constexpr int kAcross = kTileCols / (16 * WT);                  // waves across the channels
-    constexpr int kX = (TT * (kGemmWaves / kAcross) * 2 + kGemmWaves - 1) / kGemmWaves;
     constexpr bool kSplit = F::kForward && GATED;
     int tid = threadIdx.x;
     asm volatile("" : "+v"(tid));   // what follows from it is made once per tile, not kept from tile to tile
     const int lane = tid & (kWave - 1);
-    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int wave = uniform(tid / kWave);
+    const bool second = wave >= kGemmWaves / 2;
     const int across = wave % kAcross, q0 = wave / kAcross * (16 * TT);
     const Reader<F::kXByK> xr(q0, lane);
     const Reader<F::kWByK> wr(across * 16 * WT, lane);
@@ -434,41 +470,44 @@ __device__ __forceinline__ void run_tile(const ProductArgs &a, const ProductTile
     for (int m = 0; m < TT; ++m)
 #pragma unroll
         for (int i = 0; i < WT; ++i) acc[m][i] = Acc<F::kI8>{0, 0, 0, 0};
-    const auto products = [&](const u32x4 *stage, int h) {
-        u32x4 w[WT];
+    // One stage; the stage three further on goes to the buffer that was read last.
+    // settled: the next stage has arrived already.
+    const auto stage = [&](const u32x4 *from, u32x4 *to, bool settled) {
+        u32x4 w[WT], x[TT];
 #pragma unroll
-        for (int i = 0; i < WT; ++i) w[i] = wr(stage + kOperandVecs, h, i);
+        for (int i = 0; i < WT; ++i) w[i] = wr(from + kOperandVecs, i);
 #pragma unroll
-        for (int m = 0; m < TT; ++m) {
-            const u32x4 x = xr(stage, h, m);
+        for (int m = 0; m < TT; ++m) x[m] = xr(from, m);
+        feed.copy(a, nt, to);
+        if (second && !settled) copies_arrived<2 * kCopies>();
+        barrier_after<63>();
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-            for (int i = 0; i < WT; ++i) acc[m][i] = multiply<F::kI8>(w[i], x, acc[m][i]);
-        }
-        // a step's products stay in their step: the compiler would move them,
-        // with their operands, behind the barriers
+        for (int m = 0; m < TT; ++m)
+#pragma unroll
+            for (int i = 0; i < WT; ++i) acc[m][i] = multiply<F::kI8>(w[i], x[m], acc[m][i]);
+        // a stage's products stay between their barriers
 #pragma unroll
         for (int m = 0; m < TT; ++m)
 #pragma unroll
             for (int i = 0; i < WT; ++i) asm volatile("" : "+v"(acc[m][i]));
+        __builtin_amdgcn_s_setprio(0);
+        if (!second && !settled) copies_arrived<2 * kCopies>();
+        barrier_after<63>();
     };
-    barrier_after<0>();                                            // stage 0 has arrived, stage 1 is free
-    bool even = any;
-    if (!even) next_first();
-    while (even) {
-        const bool odd = feed.template copy<kX>(a, t, stage1, 16 * WT);
-        products(stage0, 0);
-        products(stage0, 1);
-        barrier_after<0>();                                        // stage 1 has arrived, stage 0 is free
-        even = odd && feed.template copy<kX>(a, t, stage0, 16 * WT);
-        if (!even) next_first();
-        if (odd) {
-            products(stage1, 0);
-            products(stage1, 1);
-        }
-        if (even) barrier_after<0>();                              // stage 0 has arrived, stage 1 is free
-    }
-    barrier_after<63>();                                           // stage 1 is free
-    finish<TT, WT, KIND, GATED>(a, t, acc, q0, t.c0 + across * (kSplit ? 8 : 16) * WT, stage1 + wave * 512);
+    if (second) barrier_after<63>();
+    bool first = true;
+    do {
+        stage(b0, b3, first);
+        if (groups == 1) next_tile();
+        stage(b1, b0, first);
+        stage(b2, b1, false);
+        stage(b3, b2, false);
+        first = false;
+    } while (--groups > 0);
+    if (!second) barrier_after<63>();
+    copies_arrived<0>();
+    finish<TT, WT, KIND, GATED>(a, t, acc, q0, t.c0 + across * (kSplit ? 8 : 16) * WT, b3 + wave * 256);
 }
 
 template <Product KIND, bool GATED>
@@ -477,7 +516,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_product_tile(ProductArgs a,
     constexpr bool kSplit = F::kForward && GATED;
     constexpr int kOutCols = kSplit ? kTileCols / 2 : kTileCols;
     constexpr bool kW = KIND == Product::kBackwardW;
-    __shared__ u32x4 stage0[kPairVecs], stage1[kPairVecs];
+    __shared__ u32x4 b0[kPairVecs], b1[kPairVecs], b2[kPairVecs], b3[kPairVecs];
     __shared__ SegTable segs;
     __shared__ int2 s_scan[kGemmWaves];
     const int tid = threadIdx.x;
@@ -543,41 +582,44 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_product_tile(ProductArgs a,
             t = ProductTile{rt.row0, rt.rows, rt.expert, rt.ntile * kOutCols, 0, 0};
         }
         const int part_rows = kTileRows >> cut, skip = cut ? (((item - whole) & ((1 << cut) - 1)) * part_rows) : 0;
-        t.row0 += skip;
-        t.rows = __builtin_amdgcn_readfirstlane(min(t.rows - skip, part_rows));
+        t.rows = uniform(min(t.rows - skip, part_rows));
+        t.row0 = uniform(t.row0 + skip);
+        t.expert = uniform(t.expert);
+        t.c0 = uniform(t.c0);
+        if constexpr (kW) {
+            t.first = uniform(t.first);
+            t.end = uniform(t.end);
+        }
         return t.rows > 0;
     };
-    // channels of a wave
-    const auto cols_of = [](const ProductTile &t) { return t.rows > 128 ? 64 : 32; };
     ProductTile t;
     if (!tile_of(0, t)) return;                                    // the same for every wave
-    {
-        Feed<KIND, GATED> first;
-        first.start(a, t);
-        first.template copy<4>(a, t, stage0, cols_of(t));
-    }
+    Feed<KIND, GATED> feed;
+    feed.start(a, t);
+    feed.copy(a, t, b0);
+    feed.copy(a, t, b1);
+    feed.copy(a, t, b2);
+    copies_arrived<0>();
     for (int round = 1;; ++round) {
-        Feed<KIND, GATED> feed;
-        feed.start(a, t);
-        const bool any = feed.have(a, t);
-        if (any) feed.step(a);
-        ProductTile nt{};
+        const int groups = max((stages_of<KIND>(a, t) + 3) / 4, 1);
+        ProductTile nt = t;
         bool more = false;
-        const auto next_first = [&]() {
+        const auto next_tile = [&]() {
             more = tile_of(round, nt);
-            if (!more) return;
-            Feed<KIND, GATED> first;
-            first.start(a, nt);
-            first.template copy<4>(a, nt, stage0, cols_of(nt));
+            if (more)
+                feed.start(a, nt);
+            else
+                feed.stop();
         };
+        barrier_after<63>();                                       // every wave's copies are there, the last tile's buffer 3 is free
         if (t.rows > 128)
-            run_tile<8, 4, KIND, GATED>(a, t, feed, any, stage0, stage1, next_first);
+            run_tile<8, 4, KIND, GATED>(a, t, nt, feed, groups, b0, b1, b2, b3, next_tile);
         else if (t.rows > 64)
-            run_tile<8, 2, KIND, GATED>(a, t, feed, any, stage0, stage1, next_first);
+            run_tile<8, 2, KIND, GATED>(a, t, nt, feed, groups, b0, b1, b2, b3, next_tile);
         else if (t.rows > 32)
-            run_tile<4, 2, KIND, GATED>(a, t, feed, any, stage0, stage1, next_first);
+            run_tile<4, 2, KIND, GATED>(a, t, nt, feed, groups, b0, b1, b2, b3, next_tile);
         else
-            run_tile<2, 2, KIND, GATED>(a, t, feed, any, stage0, stage1, next_first);
+            run_tile<2, 2, KIND, GATED>(a, t, nt, feed, groups, b0, b1, b2, b3, next_tile);
         if (!more) return;
         t = nt;
     }
