@@ -625,38 +625,225 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_product_tile(ProductArgs a,
     }
 }
 
-int64_t grid_of(const ProductArgs &a, int &tiles_c, int64_t &tiles) {
-    const bool split = a.gated && a.kind != Product::kBackwardX;
-    const int out = split ? kTileCols / 2 : kTileCols;
-    tiles_c = (a.cols + out - 1) / out;
-    const int64_t rows = a.kind == Product::kBackwardW ? static_cast<int64_t>(a.E) * ((a.inner + kTileRows - 1) / kTileRows) : most_tiles(a, kTileRows);
-    tiles = rows * tiles_c;
-    return std::min<int64_t>(4 * tiles, kCus);               // a tile may be taken in four parts
+// ---------------------------------------------------------------------------
+// forward products of short segments
+// ---------------------------------------------------------------------------
+
+// 16 token rows by 32 weight rows; the four waves split the channels and join
+// their sums in LDS.  The weights' bytes are the work, each read once, so what
+// counts is to keep many of them in flight and to ask for whole lines: a unit
+// (128 bytes of k) of the 32 rows, 4 KB, is copied to the wave's own LDS in
+// instructions of 8 whole lines while the unit before it is multiplied, four
+// workgroups of four such waves per CU.  Tokens, few and shared by every workgroup
+// of the segment, go straight to registers.
+constexpr int kStreamRows = 16;
+constexpr int kStreamWaves = 4;
+constexpr int kWTiles = 2;                     // 16-row weight tiles (gated: a gate and an up tile)
+constexpr int kUnitBytes = 128;                // of k: two steps
+constexpr int kUnitVecs = kWTiles * 16 * 8;
+
+template <Product KIND, bool GATED, bool ONCE>
+__global__ __launch_bounds__(kStreamWaves * kWave, 4) void k_product_stream(ProductArgs a, int tiles_c) {
+    using F = Form<KIND>;
+    constexpr bool kI8 = F::kI8;
+    constexpr int kOutTiles = GATED ? kWTiles / 2 : kWTiles;
+    __shared__ u32x4 unit0[kStreamWaves][kUnitVecs], unit1[kStreamWaves][kUnitVecs];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = uniform(static_cast<int>(threadIdx.x) / kWave);
+    RowTile t;
+    if (!find_tile<kStreamRows>(a, blockIdx.x, tiles_c, t)) return;   // the same for every wave
+    t.row0 = uniform(t.row0);
+    t.rows = uniform(t.rows);
+    t.expert = uniform(t.expert);
+    t.ntile = uniform(t.ntile);
+    const int n0 = t.ntile * (kOutTiles * 16);
+    // lane = 16*g + r: row r of each operand, chunk g of a step
+    const int r = lane & 15, g = lane >> 4;
+    const unsigned int xb = static_cast<unsigned int>(a.inner) * F::kSize;
+    const unsigned int wrows = min(kOutTiles * 16, a.cols - n0);      // past them zeros are read
+    const char *const first = static_cast<const char *>(a.w) + (static_cast<size_t>(t.expert) * (GATED ? 2 : 1) * a.cols + n0) * xb;
+    const auto w_gate = buffer_of(first, wrows * xb), w_up = buffer_of(first + (GATED ? static_cast<size_t>(a.cols) * xb : 0), wrows * xb);
+    const auto xbuf = buffer_of(static_cast<const char *>(a.x) + static_cast<size_t>(t.row0) * xb, t.rows * xb);
+    const int units = (xb + kUnitBytes - 1) / kUnitBytes;
+    const int begin = units * wave / kStreamWaves, end = units * (wave + 1) / kStreamWaves;
+    // Copies of 8 weight rows: lane l's vector is row l/8, chunk c at place l%8;
+    // chunk c of row q lies at c ^ (q % 8).  Chunks past the row's end read zeros.
+    const unsigned int chunk = lane_chunk(lane);
+    const unsigned int wo = lane / 8 * xb + chunk;
+    const auto copy_unit = [&](int u, u32x4 *to) {
+        const unsigned int gone = u * kUnitBytes + chunk >= xb ? kPastEnd : 0u;
+#pragma unroll
+        for (int j = 0; j < kWTiles * 2; ++j) {
+            const int row = 8 * j;
+            const bool is_up = row >= kOutTiles * 16;
+            copy_to_lds<ONCE>(is_up ? w_up : w_gate, to + row * 8, (wo + (is_up ? row - kOutTiles * 16 : row) * xb) | gone, u * kUnitBytes);
+        }
+    };
+    Acc<kI8> acc[kWTiles];
+#pragma unroll
+    for (int i = 0; i < kWTiles; ++i) acc[i] = Acc<kI8>{0, 0, 0, 0};
+    struct Tokens {
+        u32x4 x[2];
+    };
+    const unsigned int xo = r * xb + g * 16;
+    const auto load_tokens = [&](int u) {
+        Tokens v;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const unsigned int at = static_cast<unsigned int>(u * kUnitBytes + h * 64);
+            v.x[h] = __builtin_amdgcn_raw_buffer_load_b128(xbuf, static_cast<int>(at + g * 16 >= xb ? kPastEnd : xo), static_cast<int>(min(at, xb - 1)), 0);
+        }
+        return v;
+    };
+    const auto products = [&](const u32x4 *from, const Tokens &tok) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < kWTiles; ++i) acc[i] = multiply<kI8>(from[(i * 16 + r) * 8 + ((h * 4 + g) ^ (r & 7))], tok.x[h], acc[i]);
+        // the unit is read before anything is copied over it
+#pragma unroll
+        for (int i = 0; i < kWTiles; ++i) asm volatile("" : "+v"(acc[i]) : : "memory");
+    };
+    if (begin < end) {
+        copy_unit(begin, unit0[wave]);
+        if (begin + 1 < end) copy_unit(begin + 1, unit1[wave]);
+        Tokens now = load_tokens(begin);
+        for (int u = begin; u < end; u += 2) {
+            Tokens next = now;
+            if (u + 1 < end) next = load_tokens(u + 1);
+            products(unit0[wave], now);
+            if (u + 2 < end) copy_unit(u + 2, unit0[wave]);
+            if (u + 1 < end) {
+                if (u + 2 < end) now = load_tokens(u + 2);
+                products(unit1[wave], next);
+                if (u + 3 < end) copy_unit(u + 3, unit1[wave]);
+            }
+        }
+    }
+    // the sums meet where the weights were
+    __syncthreads();
+    Acc<kI8>(*const part)[kWTiles][kWave] = reinterpret_cast<Acc<kI8>(*)[kWTiles][kWave]>(&unit0[0][0]);
+#pragma unroll
+    for (int i = 0; i < kWTiles; ++i) part[wave][i][lane] = acc[i];
+    __syncthreads();
+    for (int i = wave; i < kOutTiles; i += kStreamWaves) {
+        const int n = n0 + i * 16 + 4 * g;
+        const bool mine = r < t.rows && n < a.cols;
+        const size_t row = static_cast<size_t>(t.row0) + r;
+        const auto sum = [&](int tile, int up) {
+            Acc<kI8> v = part[0][tile][lane];
+#pragma unroll
+            for (int q = 1; q < kStreamWaves; ++q) v += part[q][tile][lane];
+            f32x4 f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                f[c] = static_cast<float>(v[c]);
+                if constexpr (kI8) {
+                    if (mine) f[c] = f[c] * a.xs[row] * a.ws[(static_cast<size_t>(t.expert) * (GATED ? 2 : 1) + up) * a.cols + n + c];
+                }
+            }
+            return f;
+        };
+        f32x4 v = sum(i, 0);
+        if constexpr (GATED) {
+            const f32x4 u = sum(kOutTiles + i, 1);
+            if (!kI8 && a.pre != nullptr && mine) {
+                unsigned short *const pre = static_cast<unsigned short *>(a.pre) + row * 2 * a.cols + n;
+                *reinterpret_cast<u32x2 *>(pre) = pack_bf16x4(v);
+                *reinterpret_cast<u32x2 *>(pre + a.cols) = pack_bf16x4(u);
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[c] = silu(v[c]) * u[c];
+        }
+        if (mine) *reinterpret_cast<u32x2 *>(static_cast<unsigned short *>(a.out) + row * a.cols + n) = pack_bf16x4(v);
+    }
+}
+
+bool forward(const ProductArgs &a) { return a.kind == Product::kForward || a.kind == Product::kForwardI8; }
+
+double weight_bytes(const ProductArgs &a) {
+    return used_segments(a) * (a.gated ? 2.0 : 1.0) * a.cols * a.inner * (a.kind == Product::kForwardI8 ? 1.0 : 2.0);
+}
+// Weights that the Infinity Cache (256 MB) does not hold from call to call are
+// read past the caches by the streaming kernel.
+bool weights_once(const ProductArgs &a) { return weight_bytes(a) > 320.0e6; }
+
+// The rule between a forward product's two kernels: the sooner by these estimates,
+// in microseconds.  Experts with a row: as many as a routing at random leaves with
+// one.  Steps are of 64 bytes of k.
+//   stream: a start of 4 us; a workgroup's work is one 16-row tile by 32 weight
+//     rows, 3300 steps of such a microsecond, or the weights at 7.0 TB/s.
+//   tile: a start of 6 us, then rounds of 256 workgroups one tile each, 0.38 us a
+//     step and 0.0018 more for each row of a tile, or of a part of it in the last
+//     round; or the weights at 5.5 TB/s.
+// Measured, stream / tile (us; E experts with m rows each, M weight rows; bf16):
+//   E=256 H=7168 M=2048  m=4 1066 / 1351  m=16 1664 / 1370
+//   E=256 H=1024 M=7168  m=4 561 / 642    E=256 H=2048 M=1536 m=16 356 / 354
+//   E=64  H=2048 M=2816  m=6 107 / 171    m=24 205 / 172
+//   E=8   H=7168 M=2048  m=2 30 / 87      m=8 34 / 88     m=32 55 / 97
+//   E=4   H=7168 M=512   m=32 17 / 95     m=128 33 / 97
+bool long_segments(const ProductArgs &a) {
+    if (!forward(a)) return true;
+    if (a.entries == 0) return false;
+    const double rows = static_cast<double>(a.entries), used = used_segments(a), weights = weight_bytes(a);
+    const double M = a.gated ? 2.0 * a.cols : a.cols, steps = a.inner * (a.kind == Product::kForwardI8 ? 1.0 : 2.0) / kStageKBytes;
+    const double stream_tiles = std::max(used, rows / kStreamRows + used / 2), row_tiles = std::max(used, rows / kTileRows + used / 2);
+    const double stream = 4 + std::max(stream_tiles * (M / (16 * kWTiles)) * steps / 3300, weights / 7.0e6);
+    const double tiles = row_tiles * std::ceil(M / kTileCols), whole = std::floor(tiles / kCus), rest = tiles - whole * kCus;
+    const double last_rows = rest * 4 <= kCus ? kTileRows / 4 : (rest * 2 <= kCus ? kTileRows / 2 : kTileRows);
+    const auto step_us = [](double tile_rows) { return 0.38 + 0.0018 * tile_rows; };
+    const double tile_rows = std::min(rows / used, static_cast<double>(kTileRows));
+    const double rounds_us = whole * step_us(tile_rows) + (rest > 0 ? step_us(std::min(tile_rows, last_rows)) : 0);
+    return 6 + std::max(steps * rounds_us, weights / 5.5e6) < stream;
+}
+
+struct Grid {
+    int tiles_c;
+    int64_t tiles;     // at most
+    int64_t blocks;
+};
+Grid grid_of(const ProductArgs &a) {
+    const bool tiles = long_segments(a), split = a.gated && forward(a);
+    const int cols = tiles ? kTileCols : kWTiles * 16, out = split ? cols / 2 : cols;
+    Grid g;
+    g.tiles_c = (a.cols + out - 1) / out;
+    const int64_t rows = a.kind == Product::kBackwardW ? static_cast<int64_t>(a.E) * ((a.inner + kTileRows - 1) / kTileRows)
+                                                       : most_tiles(a, tiles ? kTileRows : kStreamRows);
+    g.tiles = (rows * g.tiles_c + kXcds - 1) / kXcds * kXcds;
+    g.blocks = tiles ? std::min<int64_t>(4 * g.tiles, kCus) : g.tiles;   // a tile may be taken in four parts
+    return g;
 }
 
 }  // namespace
 
 bool product_grid_ok(const ProductArgs &a) {
-    int tiles_c;
-    int64_t tiles;
-    grid_of(a, tiles_c, tiles);
-    return tiles <= INT32_MAX - kCus;
+    const Grid g = grid_of(a);
+    return g.tiles <= INT32_MAX - kCus && g.blocks * std::max(kStreamWaves * kWave, kGemmThreads) <= kMaxLaunchThreads;
 }
 
 hipError_t launch_product(const ProductArgs &a, hipStream_t s) {
-    int tiles_c;
-    int64_t tiles;
-    const int64_t blocks = grid_of(a, tiles_c, tiles);
-    if (blocks == 0) return hipSuccess;
-    const dim3 grid(static_cast<unsigned>((blocks + kXcds - 1) / kXcds * kXcds)), block(kGemmThreads);
-#define MOE_PRODUCT(KIND, GATED) hipLaunchKernelGGL((k_product_tile<Product::KIND, GATED>), grid, block, 0, s, a, tiles_c)
+    const Grid g = grid_of(a);
+    if (g.blocks == 0) return hipSuccess;
+    const dim3 grid(static_cast<unsigned>(g.blocks)), tile_block(kGemmThreads), stream_block(kStreamWaves * kWave);
+    const bool tiles = long_segments(a), once = weights_once(a);
+#define MOE_TILE(KIND, GATED) hipLaunchKernelGGL((k_product_tile<Product::KIND, GATED>), grid, tile_block, 0, s, a, g.tiles_c)
+#define MOE_FORWARD(KIND, GATED)                                                                                              \
+    do {                                                                                                                      \
+        if (tiles)                                                                                                            \
+            MOE_TILE(KIND, GATED);                                                                                            \
+        else if (once)                                                                                                        \
+            hipLaunchKernelGGL((k_product_stream<Product::KIND, GATED, true>), grid, stream_block, 0, s, a, g.tiles_c);       \
+        else                                                                                                                  \
+            hipLaunchKernelGGL((k_product_stream<Product::KIND, GATED, false>), grid, stream_block, 0, s, a, g.tiles_c);      \
+    } while (0)
     switch (a.kind) {
-        case Product::kForward: if (a.gated) MOE_PRODUCT(kForward, true); else MOE_PRODUCT(kForward, false); break;
-        case Product::kForwardI8: if (a.gated) MOE_PRODUCT(kForwardI8, true); else MOE_PRODUCT(kForwardI8, false); break;
-        case Product::kBackwardX: if (a.gated) MOE_PRODUCT(kBackwardX, true); else MOE_PRODUCT(kBackwardX, false); break;
-        case Product::kBackwardW: MOE_PRODUCT(kBackwardW, false); break;
+        case Product::kForward: if (a.gated) MOE_FORWARD(kForward, true); else MOE_FORWARD(kForward, false); break;
+        case Product::kForwardI8: if (a.gated) MOE_FORWARD(kForwardI8, true); else MOE_FORWARD(kForwardI8, false); break;
+        case Product::kBackwardX: if (a.gated) MOE_TILE(kBackwardX, true); else MOE_TILE(kBackwardX, false); break;
+        case Product::kBackwardW: MOE_TILE(kBackwardW, false); break;
     }
-#undef MOE_PRODUCT
+#undef MOE_FORWARD
+#undef MOE_TILE
     return hipGetLastError();
 }
 
