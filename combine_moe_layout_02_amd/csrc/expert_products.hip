@@ -51,18 +51,22 @@ __device__ __forceinline__ void gated_gradient(float g, float u, float dh, float
 
 // A tile is up to 256 rows q by 256 channels c.  One workgroup of eight waves per
 // CU takes tile after tile; each wave holds 128 x 64 (128 accumulator registers),
-// or for at most 128 rows all of them by 32 channels.  A stage is 64 bytes of k of
-// every row (32 rows of k where those are the memory's rows), one matrix
-// instruction deep, 32 KB; four buffers: while one stage is multiplied the next
-// three are on their way, across tiles too.
+// or for at most 128 rows all of them by 32 channels.
+//
+// 128 bytes of k of every row (64 rows of k where those are the memory's rows), a
+// whole line each, make a pair of stages.  The first stage multiplies half of each
+// wave's rows q with its channels, the second the other half with the same
+// channels, which stay in registers: so X is needed in two halves, one a stage
+// later.  LDS holds two pairs, 128 KB: while one stage is multiplied what the next
+// three need is on its way, across tiles too.
 constexpr int kGemmWaves = 8;
 constexpr int kGemmThreads = kGemmWaves * kWave;
 constexpr int kTileCols = 256;
-constexpr int kOperandVecs = 1024;             // 16-byte vectors of one operand's stage
-constexpr int kPairVecs = 2 * kOperandVecs;    // X, then W
-constexpr int kStageKBytes = 64;               // bytes of k of a stage
-constexpr int kStageK = 32;                    // rows of k of a stage of a transposed operand
-constexpr int kCopies = 4;                     // copies of a wave and stage: two of X, two of W
+constexpr int kHalfVecs = 1024;                // 16-byte vectors of half of X of a pair
+constexpr int kWVecs = 2048;                   // of W
+constexpr int kPairBytes = 128;                // bytes of k of a pair
+constexpr int kPairK = 64;                     // rows of k of a pair of a transposed operand
+constexpr int kInFlight = 8;                   // a wave's copies of two stages: two of X, then two of X and four of W
 
 template <Product KIND>
 struct Form {
@@ -73,42 +77,40 @@ struct Form {
     static constexpr int kSize = kI8 ? 1 : 2;                       // bytes of an element
 };
 
-// Rows of k of a stage lie at a pitch of 512 bytes.  The transposing read's 16
-// lanes of one group take four rows of k (its lanes' quarter of each 32 bytes);
-// 32-byte block b of row k lies at b ^ turn(k), so that the eight rows that half a
-// wave reads are in eight different groups of banks.
+// Rows of k lie at a pitch of 512 bytes (W) or 256 (half of X).  The transposing
+// read's 16 lanes of one group take four rows of k (its lanes' quarter of each 32
+// bytes); 32-byte block b of row k lies at b ^ turn(k), so that the eight rows that
+// half a wave reads are in eight different groups of banks.
 __device__ __forceinline__ int k_turn(int k) { return (k & 3) | (k >> 1 & 4); }
 
-// K neighbours: rows lie at a pitch of 64 bytes, chunk c (16 bytes) of row q at
-// c ^ chunk_turn(q): eight and sixteen neighbouring rows' chunk c are in different
-// groups of banks.
-__device__ __forceinline__ int chunk_turn(int q) { return q >> 1 & 2; }
-
-// Where a lane's operands lie.  K neighbours: row i*16 + r of the wave's, chunk g.
-template <bool BY_K>
+// Where a lane's operands lie, of tiles of 16 rows (q or c) from `first` of the
+// buffer's, at step h of the pair.  K neighbours: row r, chunk 4h + g at
+// (4h + g) ^ (r % 8).
+template <bool BY_K, int PITCH>
 struct Reader {
-    int at;
+    int at[2];
     unsigned int base;
-    __device__ __forceinline__ Reader(int first, int lane) {   // the wave's first row (of 16 * a power of two)
+    __device__ __forceinline__ Reader(int first, int lane) {   // first: 16 * a multiple of the power of two of tiles
         const int r = lane & 15, g = lane >> 4;
         if constexpr (BY_K) {
             const int k = 8 * g + r / 4;
-            base = static_cast<unsigned int>(k * 512 + ((first / 16) ^ k_turn(k)) * 32 + (r & 3) * 8);
+            base = static_cast<unsigned int>(k * PITCH + ((first / 16) ^ k_turn(k)) * 32 + (r & 3) * 8);
         } else {
-            at = (first + r) * 4 + (g ^ chunk_turn(r));
+            at[0] = (first + r) * 8 + (g ^ (r & 7));
+            at[1] = (first + r) * 8 + ((4 + g) ^ (r & 7));
         }
     }
-    __device__ __forceinline__ u32x4 operator()(const u32x4 *stage, int i) const {
+    __device__ __forceinline__ u32x4 operator()(const u32x4 *buffer, int h, int i) const {
         if constexpr (BY_K) {
             typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-            const char *const p = reinterpret_cast<const char *>(stage) + (base ^ static_cast<unsigned int>(i * 32));
-            // rows 8g .. 8g+3 of the stage, then 8g+4 .. 8g+7
+            const char *const p = reinterpret_cast<const char *>(buffer) + (base ^ static_cast<unsigned int>(i * 32)) + h * 32 * PITCH;
+            // rows 8g .. 8g+3 of the step, then 8g+4 .. 8g+7
             const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p));
-            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 2048));
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 4 * PITCH));
             const u32x2 a = __builtin_bit_cast(u32x2, lo), b = __builtin_bit_cast(u32x2, hi);
             return u32x4{a[0], a[1], b[0], b[1]};
         } else {
-            return stage[at + i * 64];
+            return buffer[at[h] + i * 128];
         }
     }
 };
@@ -129,32 +131,34 @@ struct ProductTile {
     int first, end;    // kBackwardW: the expert's rows, but for its replicas'
 };
 
-// Asks for a tile's stages, one after the other; past the last one for zeros.
+// Asks for what a tile's stages need, pair by pair: W and the first half of X, then
+// the second half.  Past the tile's last k it asks for zeros.
 template <Product KIND, bool GATED>
 struct Feed {
     using F = Form<KIND>;
     static constexpr bool kSplit = F::kForward && GATED;
     unsigned int xo, wo;                 // this lane's first offsets
-    // K neighbours: X's first row, and of W the first row of each of the wave's two
-    // copies, with the bytes from there to the tile's end; rows of k: the next stage's
-    // first row and the tile's bytes of each row
+    // K neighbours: X's first row, and of W the first row of each half of the wave's
+    // copies, with the bytes from there to the tile's end; rows of k: the pair's first
+    // row and the tile's bytes of each row
     const char *x, *w, *w1;
     unsigned int x_bytes, w_bytes, w1_bytes;
-    int left;                            // rows of k, or bytes of k, not asked for yet
-    int at;                              // bytes of k asked for
+    int left;                            // rows of k, or bytes of k, from this pair on
+    int at;                              // bytes of k before this pair
     int slot;                            // kBackwardW, balanced: replica slots looked at
+    int row0, c0, expert;                // kBackwardW: of the tile
 
     // kBackwardW: rows first .. end-1 of the receive buffer
-    __device__ __forceinline__ void run(const ProductArgs &a, const ProductTile &t, int first, int end) {
+    __device__ __forceinline__ void run(const ProductArgs &a, int first, int end) {
         left = uniform(end - first);
-        x = static_cast<const char *>(a.x) + (static_cast<size_t>(uniform(first)) * a.inner + t.row0) * 2;
-        w = static_cast<const char *>(a.w) + (static_cast<size_t>(uniform(first)) * a.cols + t.c0) * 2;
+        x = static_cast<const char *>(a.x) + (static_cast<size_t>(uniform(first)) * a.inner + row0) * 2;
+        w = static_cast<const char *>(a.w) + (static_cast<size_t>(uniform(first)) * a.cols + c0) * 2;
     }
-    __device__ __forceinline__ void next_run(const ProductArgs &a, const ProductTile &t) {
+    __device__ __forceinline__ void next_run(const ProductArgs &a) {
         const int lane = threadIdx.x & (kWave - 1), slots = a.R * a.B;
         while (left <= 0 && slot < slots) {
             const int i = slot + lane;
-            const uint64_t mine = __ballot(i < slots && a.slot_expert[min(i, slots - 1)] == t.expert);
+            const uint64_t mine = __ballot(i < slots && a.slot_expert[min(i, slots - 1)] == expert);
             if (mine == 0) {
                 slot += kWave;
                 continue;
@@ -162,38 +166,44 @@ struct Feed {
             const int found = slot + __builtin_ctzll(mine);
             slot = found + 1;
             const int epr = a.E / a.R, seg = found / a.B * (epr + a.B) + epr + found % a.B;
-            run(a, t, a.seg_offset[seg], a.seg_offset[seg + 1]);
+            run(a, a.seg_offset[seg], a.seg_offset[seg + 1]);
         }
     }
 
-    // A tile's first stage comes next.
+    // A tile's first pair comes next.
     __device__ __forceinline__ void start(const ProductArgs &a, const ProductTile &t) {
         const int lane = threadIdx.x & (kWave - 1);
         const int wave = uniform(static_cast<int>(threadIdx.x) / kWave);
         const unsigned int xb = static_cast<unsigned int>(a.inner) * F::kSize, cb = static_cast<unsigned int>(a.cols) * 2;
-        // of 16 rows of k neighbours: row lane/4, its chunk; of two rows of k: row
-        // lane/32, its chunk (copy_k() has the rows that this wave takes)
-        const unsigned int chunk = ((lane & 3) ^ chunk_turn(lane / 4)) * 16;
+        // W's rows of k: of the wave's copies of two rows, row lane/32 of the first and
+        // its chunk
         const int k = 2 * (wave & 1) + 8 * (wave >> 1 & 1) + 4 * (wave >> 2) + lane / 32;
         const unsigned int k_chunk = ((lane & 31) ^ (2 * k_turn(k))) * 16;
         at = 0;
         slot = 0;
         if constexpr (KIND == Product::kBackwardW) {
-            xo = k * xb + k_chunk;
+            // half of X: two pieces of 128 bytes of each row of k, 256 apart; of the wave's
+            // copies of four rows, row lane/16 of the first
+            const int kx = 4 * wave + lane / 16, c = (lane & 15) ^ (2 * k_turn(kx));
+            xo = kx * xb + (c >> 3) * 256 + (c & 7) * 16;
             wo = k * cb + k_chunk;
             x_bytes = min(512u, xb - static_cast<unsigned int>(t.row0) * 2);
             w_bytes = min(512u, cb - static_cast<unsigned int>(t.c0) * 2);
-            run(a, t, t.first, t.end);
-            if (a.seg_offset != nullptr) next_run(a, t);
+            row0 = t.row0;
+            c0 = t.c0;
+            expert = t.expert;
+            run(a, t.first, t.end);
+            if (a.seg_offset != nullptr) next_run(a);
         } else {
             x = static_cast<const char *>(a.x) + static_cast<size_t>(t.row0) * xb;
             x_bytes = t.rows * xb;
-            xo = (wave * 16 + lane / 4) * xb + chunk;
+            // of copies of eight rows: row lane/8, its chunk
+            xo = (wave * 8 + lane / 8) * xb + lane_chunk(lane);
             if constexpr (F::kForward) {
                 left = static_cast<int>(xb);
-                // the wave copies 32 rows of W's place in LDS; gated, the second half of the
-                // rows that one wave multiplies (64, or 32 for at most 128 rows q) are the up
-                // weights of the first
+                // the wave copies 32 rows of W's place in LDS, in two halves of 16; gated, the
+                // second half of the rows that one wave multiplies (64, or 32 for at most 128
+                // rows q) are the up weights of the first
                 const bool wide = t.rows > 128;
                 const int row = !kSplit ? wave * 32 : (wide ? (wave >> 1) * 32 : wave * 16), row1 = kSplit && !wide ? row : row + 16;
                 const bool up = kSplit && wide && (wave & 1), up1 = kSplit && (!wide || (wave & 1));
@@ -203,7 +213,7 @@ struct Feed {
                 w1 = first + (static_cast<size_t>(up1 ? a.cols : 0) + row1) * xb;
                 w_bytes = max(rows - row, 0) * xb;
                 w1_bytes = max(rows - row1, 0) * xb;
-                wo = lane / 4 * xb + chunk;
+                wo = lane / 8 * xb + lane_chunk(lane);
             } else {
                 left = a.inner;
                 w_bytes = min(512u, cb - static_cast<unsigned int>(t.c0) * 2);
@@ -215,65 +225,86 @@ struct Feed {
     // No tile comes next: zeros.
     __device__ __forceinline__ void stop() { left = 0; }
 
-    // Rows of k `n` (at most 32) from `from`: the wave's copies take two rows each,
-    // with the same turn.  Rows past the last read zeros; `bytes` of the last row
-    // belong to the tile.
-    __device__ __forceinline__ static void copy_k(const char *from, int n, unsigned int bytes, unsigned int row_bytes, unsigned int first, u32x4 *to) {
-        const int wave = uniform(static_cast<int>(threadIdx.x) / kWave);
-        const auto b = buffer_of(uniform(from), n > 0 ? static_cast<unsigned int>(n - 1) * row_bytes + bytes : 0u);
-        const int k0 = 2 * (wave & 1) + 8 * (wave >> 1 & 1) + 4 * (wave >> 2);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) copy_to_lds(b, to + (k0 + 16 * j) * 32, first + 16 * j * row_bytes, 0);
+    // A buffer over `n` (at most 64) rows of k from `from`; `bytes` of the last row
+    // belong to the tile.  Rows past the last read zeros.
+    __device__ __forceinline__ static __amdgpu_buffer_rsrc_t rows_of_k(const char *from, int n, unsigned int bytes, unsigned int row_bytes) {
+        return buffer_of(uniform(from), n > 0 ? static_cast<unsigned int>(n - 1) * row_bytes + bytes : 0u);
+    }
+    // kPastEnd for the lanes whose chunk of the pair lies past the row's end.
+    __device__ __forceinline__ unsigned int gone() const {
+        const int bytes = F::kForward ? left : 2 * left;
+        return static_cast<int>(lane_chunk(threadIdx.x & (kWave - 1))) >= bytes ? kPastEnd : 0u;
     }
 
-    // Asks for the next stage, into `stage`.
-    __device__ __forceinline__ void copy(const ProductArgs &a, const ProductTile &t, u32x4 *stage) {
-        const int lane = threadIdx.x & (kWave - 1);
+    // Half `half` of the pair's X.
+    __device__ __forceinline__ void copy_x(const ProductArgs &a, u32x4 *to, int half) const {
         const int wave = uniform(static_cast<int>(threadIdx.x) / kWave);
-        const unsigned int xb = static_cast<unsigned int>(a.inner) * F::kSize, cb = static_cast<unsigned int>(a.cols) * 2;
-        unsigned int x_lane = xo, w_lane = wo;
-        asm volatile("" : "+v"(x_lane), "+v"(w_lane));    // offsets are made here, not kept in a register each
-        const int rows = uniform(min(left, kStageK));     // of k, where the memory's rows are k
+        const unsigned int xb = static_cast<unsigned int>(a.inner) * F::kSize;
+        unsigned int x_lane = xo;
+        asm volatile("" : "+v"(x_lane));                  // offsets are made here, not kept in a register each
         if constexpr (F::kXByK) {
-            copy_k(x, rows, uniform(x_bytes), xb, x_lane, stage);
-            x += static_cast<size_t>(kStageK) * xb;
-        } else {
-            const int bytes = F::kForward ? left : 2 * left;      // of k, from this stage on
-            const unsigned int gone = static_cast<int>(((lane & 3) ^ chunk_turn(lane / 4)) * 16) >= bytes ? kPastEnd : 0u;
-            const auto from = buffer_of(uniform(x), uniform(x_bytes));
+            const auto b = rows_of_k(x, uniform(min(left, kPairK)), uniform(x_bytes), xb);
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                copy_to_lds(from, stage + (j * kGemmWaves + wave) * 64, (x_lane + j * kGemmWaves * 16 * xb) | gone, uniform(at));
-            if constexpr (F::kForward) {
-                copy_to_lds(buffer_of(uniform(w), uniform(w_bytes)), stage + kOperandVecs + wave * 128, w_lane | gone, uniform(at));
-                copy_to_lds(buffer_of(uniform(w1), uniform(w1_bytes)), stage + kOperandVecs + wave * 128 + 64, w_lane | gone, uniform(at));
-            }
-            at += kStageKBytes;
+            for (int j = 0; j < 2; ++j) copy_to_lds(b, to + (j * 8 + wave) * 64, x_lane + j * 32 * xb + half * 128, 0);
+        } else {
+            // rows 0-63 and 128-191 of the tile, or those 64 further on
+            const auto b = buffer_of(uniform(x), uniform(x_bytes));
+            const unsigned int past = gone();
+#pragma unroll
+            for (int j = 0; j < 2; ++j) copy_to_lds(b, to + (j * 8 + wave) * 64, (x_lane + (j * 128 + half * 64) * xb) | past, uniform(at));
         }
+    }
+    // The pair's W.
+    __device__ __forceinline__ void copy_w(const ProductArgs &a, u32x4 *to) const {
+        const int wave = uniform(static_cast<int>(threadIdx.x) / kWave);
+        unsigned int w_lane = wo;
+        asm volatile("" : "+v"(w_lane));
         if constexpr (F::kWByK) {
-            copy_k(w, rows, uniform(w_bytes), cb, w_lane, stage + kOperandVecs);
-            w += static_cast<size_t>(kStageK) * cb;
+            const unsigned int cb = static_cast<unsigned int>(a.cols) * 2;
+            const auto b = rows_of_k(w, uniform(min(left, kPairK)), uniform(w_bytes), cb);
+            const int k0 = 2 * (wave & 1) + 8 * (wave >> 1 & 1) + 4 * (wave >> 2);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) copy_to_lds(b, to + (k0 + 16 * j) * 32, w_lane + 16 * j * cb, 0);
+        } else {
+            const unsigned int xb = static_cast<unsigned int>(a.inner) * F::kSize, past = gone();
+            const auto b = buffer_of(uniform(w), uniform(w_bytes)), b1 = buffer_of(uniform(w1), uniform(w1_bytes));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                copy_to_lds(b, to + (wave * 4 + j) * 64, (w_lane + j * 8 * xb) | past, uniform(at));
+                copy_to_lds(b1, to + (wave * 4 + 2 + j) * 64, (w_lane + j * 8 * xb) | past, uniform(at));
+            }
         }
-        left -= F::kForward ? kStageKBytes : kStageK;
+    }
+    // What a pair's first stage needs, then what its second does.
+    __device__ __forceinline__ void ask_first(const ProductArgs &a, u32x4 *x_to, u32x4 *w_to) const {
+        copy_x(a, x_to, 0);
+        copy_w(a, w_to);
+    }
+    __device__ __forceinline__ void ask_second(const ProductArgs &a, u32x4 *x_to) {
+        copy_x(a, x_to, 1);
+        if constexpr (F::kXByK) x += static_cast<size_t>(kPairK) * a.inner * 2;
+        if constexpr (F::kWByK) w += static_cast<size_t>(kPairK) * a.cols * 2;
+        at += kPairBytes;
+        left -= F::kForward ? kPairBytes : kPairK;
         if constexpr (KIND == Product::kBackwardW) {
-            if (a.seg_offset != nullptr) next_run(a, t);
+            if (a.seg_offset != nullptr) next_run(a);
         }
     }
 };
 
-// Stages of a tile.
+// Pairs of a tile.
 template <Product KIND>
-__device__ __forceinline__ int stages_of(const ProductArgs &a, const ProductTile &t) {
-    if constexpr (Form<KIND>::kForward) return (a.inner * Form<KIND>::kSize + kStageKBytes - 1) / kStageKBytes;
-    if constexpr (KIND == Product::kBackwardX) return (a.inner + kStageK - 1) / kStageK;
-    int n = (t.end - t.first + kStageK - 1) / kStageK;
+__device__ __forceinline__ int pairs_of(const ProductArgs &a, const ProductTile &t) {
+    if constexpr (Form<KIND>::kForward) return (a.inner * Form<KIND>::kSize + kPairBytes - 1) / kPairBytes;
+    if constexpr (KIND == Product::kBackwardX) return (a.inner + kPairK - 1) / kPairK;
+    int n = (t.end - t.first + kPairK - 1) / kPairK;
     if (a.seg_offset != nullptr) {
         const int lane = threadIdx.x & (kWave - 1), slots = a.R * a.B, epr = a.E / a.R;
         int mine = 0;
         for (int i = lane; i < slots; i += kWave)
             if (a.slot_expert[i] == t.expert) {
                 const int seg = i / a.B * (epr + a.B) + epr + i % a.B;
-                mine += (a.seg_offset[seg + 1] - a.seg_offset[seg] + kStageK - 1) / kStageK;
+                mine += (a.seg_offset[seg + 1] - a.seg_offset[seg] + kPairK - 1) / kPairK;
             }
         n += __builtin_amdgcn_readlane(wave_inclusive_scan(mine), kWave - 1);
     }
@@ -309,7 +340,7 @@ __device__ __forceinline__ void plane_store(const u32x4 *plane, __amdgpu_buffer_
 }
 
 // What is done with a wave's sums: TT tiles of 16 rows from row q0 of the tile, WT
-// tiles of 16 channels; n0: the first channel.  `mine`: 4 KB of LDS.
+// tiles of 16 channels; n0: the first channel.  `mine`: 2 KB of LDS.
 template <int TT, int WT, Product KIND, bool GATED>
 __device__ __forceinline__ void finish(const ProductArgs &a, const ProductTile &t, Acc<Form<KIND>::kI8> (&acc)[TT][WT], int q0, int n0,
                                        u32x4 *mine) {
@@ -335,45 +366,53 @@ __device__ __forceinline__ void finish(const ProductArgs &a, const ProductTile &
         }
     }
     if constexpr (KIND == Product::kBackwardX && GATED) {
-        // the sums pass LDS in fp32: a lane then has eight neighbouring channels of a
-        // row, and reads and writes 16 bytes of gate and up each
-        constexpr int kF = 4 * WT, kRowsAt = kWave / (2 * WT);
+        // the sums pass LDS in fp32, 32 channels at a time: a lane then has eight
+        // neighbouring channels of a row, and reads and writes 16 bytes of gate and up each
         const auto pre = buffer_of(static_cast<const char *>(a.pre_in) + first * row_bytes * 2, static_cast<unsigned int>(t.rows) * row_bytes * 2);
         const auto to = buffer_of(static_cast<char *>(a.out) + first * row_bytes * 2, static_cast<unsigned int>(t.rows) * row_bytes * 2);
+        const int q = lane / 4, c = lane & 3;
 #pragma unroll
         for (int m = 0; m < TT; ++m) {
+            u32x4 gv[WT / 2], uv[WT / 2];
+            unsigned int at[WT / 2], at_up[WT / 2];
 #pragma unroll
-            for (int i = 0; i < WT; ++i) mine[r * kF + ((4 * i + g) ^ (r & (kF - 1)))] = __builtin_bit_cast(u32x4, acc[m][i]);
-            wave_lds_fence();
+            for (int p = 0; p < WT / 2; ++p) {
+                const int n = n0 + p * 32 + c * 8;
+                at[p] = n < a.cols ? (q0 + m * 16 + q) * row_bytes * 2 + 2u * n : kPastEnd;
+                at_up[p] = n < a.cols ? at[p] + row_bytes : kPastEnd;
+                gv[p] = __builtin_amdgcn_raw_buffer_load_b128(pre, static_cast<int>(at[p]), 0, 0);
+                uv[p] = __builtin_amdgcn_raw_buffer_load_b128(pre, static_cast<int>(at_up[p]), 0, 0);
+            }
 #pragma unroll
-            for (int j = 0; j < 16 / kRowsAt; ++j) {
-                const int q = j * kRowsAt + lane / (2 * WT), c = lane % (2 * WT);
-                const f32x4 lo = __builtin_bit_cast(f32x4, mine[q * kF + ((2 * c) ^ (q & (kF - 1)))]);
-                const f32x4 hi = __builtin_bit_cast(f32x4, mine[q * kF + ((2 * c + 1) ^ (q & (kF - 1)))]);
-                const unsigned int at = n0 + c * 8 < a.cols ? (q0 + m * 16 + q) * row_bytes * 2 + 2u * (n0 + c * 8) : kPastEnd;
-                const unsigned int at_up = at == kPastEnd ? kPastEnd : at + row_bytes;
-                const u32x4 gv = __builtin_amdgcn_raw_buffer_load_b128(pre, static_cast<int>(at), 0, 0);
-                const u32x4 uv = __builtin_amdgcn_raw_buffer_load_b128(pre, static_cast<int>(at_up), 0, 0);
+            for (int p = 0; p < WT / 2; ++p) {
+                // eight chunks to the row
+#pragma unroll
+                for (int i = 0; i < 2; ++i) mine[r * 8 + ((4 * i + g) ^ (r & 7))] = __builtin_bit_cast(u32x4, acc[m][2 * p + i]);
+                wave_lds_fence();
+                const f32x4 lo = __builtin_bit_cast(f32x4, mine[q * 8 + ((2 * c) ^ (q & 7))]);
+                const f32x4 hi = __builtin_bit_cast(f32x4, mine[q * 8 + ((2 * c + 1) ^ (q & 7))]);
+                wave_lds_fence();
                 f32x4 dg[2], du[2];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float gf = e & 1 ? bf16_hi(gv[e / 2]) : bf16_lo(gv[e / 2]), uf = e & 1 ? bf16_hi(uv[e / 2]) : bf16_lo(uv[e / 2]);
+                    const unsigned int gw = gv[p][e / 2], uw = uv[p][e / 2];
                     float x, y;
-                    gated_gradient(gf, uf, e < 4 ? lo[e & 3] : hi[e & 3], x, y);
+                    gated_gradient(e & 1 ? bf16_hi(gw) : bf16_lo(gw), e & 1 ? bf16_hi(uw) : bf16_lo(uw), e < 4 ? lo[e & 3] : hi[e & 3], x, y);
                     dg[e / 4][e & 3] = x;
                     du[e / 4][e & 3] = y;
                 }
                 const u32x2 a0 = pack_bf16x4(dg[0]), a1 = pack_bf16x4(dg[1]), b0 = pack_bf16x4(du[0]), b1 = pack_bf16x4(du[1]);
-                __builtin_amdgcn_raw_buffer_store_b128(u32x4{a0[0], a0[1], a1[0], a1[1]}, to, static_cast<int>(at), 0, 0);
-                __builtin_amdgcn_raw_buffer_store_b128(u32x4{b0[0], b0[1], b1[0], b1[1]}, to, static_cast<int>(at_up), 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b128(u32x4{a0[0], a0[1], a1[0], a1[1]}, to, static_cast<int>(at[p]), 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b128(u32x4{b0[0], b0[1], b1[0], b1[1]}, to, static_cast<int>(at_up[p]), 0, 0);
             }
-            wave_lds_fence();
         }
         return;
     }
     const auto to = buffer_of(static_cast<char *>(a.out) + first * row_bytes, static_cast<unsigned int>(t.rows) * row_bytes);
     const bool keep = kSplit && !F::kI8 && a.pre != nullptr;
     const auto pre = keep ? buffer_of(static_cast<char *>(a.pre) + first * row_bytes * 2, static_cast<unsigned int>(t.rows) * row_bytes * 2) : to;
+    // up values lie `cols` channels further
+    const auto pre_up = keep ? buffer_of(static_cast<char *>(a.pre) + first * row_bytes * 2 + row_bytes, static_cast<unsigned int>(t.rows) * row_bytes * 2 - row_bytes) : to;
     f32x4 ws[F::kI8 ? WT : 1];
     if constexpr (F::kI8) {
 #pragma unroll
@@ -386,54 +425,54 @@ __device__ __forceinline__ void finish(const ProductArgs &a, const ProductTile &
                 for (int e = 0; e < 4; ++e) ws[i][e] = from[c + e];
         }
     }
-    constexpr int kAtOnce = kSplit ? 1 : 2, kPlane = kAtOnce * 16 * kChunks;   // row tiles at a time
+    constexpr int kPlane = 16 * kChunks;
 #pragma unroll
-    for (int m0 = 0; m0 < TT; m0 += kAtOnce) {
+    for (int m = 0; m < TT; ++m) {
+        const unsigned int row = static_cast<unsigned int>(q0 + m * 16);
+        float xs = 0.0f;
+        if constexpr (F::kI8) {
+            if (static_cast<int>(row) + r < t.rows) xs = a.xs[first + row + r];
+        }
+        const auto sums = [&](int i) {
+            f32x4 v;
 #pragma unroll
-        for (int m = m0; m < m0 + kAtOnce; ++m) {
-            const int q = (m - m0) * 16 + r;
-            float xs = 0.0f;
-            if constexpr (F::kI8) {
-                if (q0 + m * 16 + r < t.rows) xs = a.xs[first + q0 + m * 16 + r];
+            for (int e = 0; e < 4; ++e) {
+                v[e] = static_cast<float>(acc[m][i][e]);
+                if constexpr (F::kI8) v[e] = v[e] * xs * ws[i][e];
             }
+            return v;
+        };
+        if constexpr (kSplit) {
+            if (keep) {
 #pragma unroll
-            for (int i = 0; i < kOut; ++i) {
-                f32x4 v, u;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    v[e] = static_cast<float>(acc[m][i][e]);
-                    u[e] = static_cast<float>(acc[m][kSplit ? i + kOut : i][e]);
-                    if constexpr (F::kI8) {
-                        v[e] = v[e] * xs * ws[i][e];
-                        u[e] = u[e] * xs * ws[kSplit ? i + kOut : i][e];
-                    }
+                for (int i = 0; i < kOut; ++i) {
+                    plane_put<kChunks>(mine, r, i, g, sums(i));
+                    plane_put<kChunks>(mine + kPlane, r, i, g, sums(i + kOut));
                 }
-                if constexpr (kSplit) {
-                    if (keep) {
-                        plane_put<kChunks>(mine + kPlane, q, i, g, v);
-                        plane_put<kChunks>(mine + 2 * kPlane, q, i, g, u);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = silu(v[e]) * u[e];
-                }
-                plane_put<kChunks>(mine, q, i, g, v);
+                wave_lds_fence();
+                plane_store<kChunks, 16>(mine, pre, 2 * row_bytes, row, n0, a.cols);
+                plane_store<kChunks, 16>(mine + kPlane, pre_up, 2 * row_bytes, row, n0, a.cols);
+                wave_lds_fence();
             }
+        }
+#pragma unroll
+        for (int i = 0; i < kOut; ++i) {
+            f32x4 v = sums(i);
+            if constexpr (kSplit) {
+                const f32x4 u = sums(i + kOut);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = silu(v[e]) * u[e];
+            }
+            plane_put<kChunks>(mine, r, i, g, v);
         }
         wave_lds_fence();
-        plane_store<kChunks, kAtOnce * 16>(mine, to, row_bytes, q0 + m0 * 16, n0, a.cols);
-        if (keep) {
-            plane_store<kChunks, kAtOnce * 16>(mine + kPlane, pre, 2 * row_bytes, q0 + m0 * 16, n0, a.cols);
-            // up values lie `cols` channels further
-            const auto pre_up = buffer_of(static_cast<char *>(a.pre) + first * row_bytes * 2 + row_bytes, static_cast<unsigned int>(t.rows) * row_bytes * 2 - row_bytes);
-            plane_store<kChunks, kAtOnce * 16>(mine + 2 * kPlane, pre_up, 2 * row_bytes, q0 + m0 * 16, n0, a.cols);
-        }
+        plane_store<kChunks, 16>(mine, to, row_bytes, row, n0, a.cols);
         wave_lds_fence();
     }
 }
 
 // Waits until at most N of the wave's global loads, copies and stores are in
-// flight.  Loads return in order, so that with N = 2 * kCopies all but the two
-// stages asked for last have arrived.
+// flight.  They finish in order.
 template <int N>
 __device__ __forceinline__ void copies_arrived() {
     asm volatile("" ::: "memory");
@@ -443,71 +482,94 @@ __device__ __forceinline__ void copies_arrived() {
     asm volatile("" ::: "memory");
 }
 
-// One tile whose first three stages have arrived in the buffers 0 to 2; the next
-// tile's are asked for when its own are.  Its stages are taken in fours: past the
-// last one zeros are multiplied.  next_tile() makes `feed` the next tile's.
+// The buffers of the two pairs.
+struct Pairs {
+    u32x4 *xa0, *xb0, *w0, *xa1, *xb1, *w1;
+};
+
+// One tile.  Its first pair and the first stage of its second have arrived; the next
+// tile's are asked for when its own are.  Its pairs are taken two at a time: past
+// the last one zeros are multiplied.  next_tile() makes `feed` the next tile's.
 //
 // The two waves of a SIMD take turns: while one group of four waves multiplies the
 // other reads its operands of the next stage from LDS and asks for copies.  Each
 // half step ends with a barrier of the workgroup; the second group begins half a
 // step later.
-template <int TT, int WT, Product KIND, bool GATED, typename NextTile>
-__device__ __forceinline__ void run_tile(const ProductArgs &a, const ProductTile &t, const ProductTile &nt, Feed<KIND, GATED> &feed, int groups,
-                                         u32x4 *b0, u32x4 *b1, u32x4 *b2, u32x4 *b3, NextTile &&next_tile) {
+template <int TT, int WT, Product KIND, bool GATED, typename NextTile, typename Ended>
+__device__ __forceinline__ void run_tile(const ProductArgs &a, const ProductTile &t, Feed<KIND, GATED> &feed, int groups,
+                                         const Pairs &lds, NextTile &&next_tile, Ended &&ended) {
     using F = Form<KIND>;
     constexpr int kAcross = kTileCols / (16 * WT);                  // waves across the channels
     constexpr bool kSplit = F::kForward && GATED;
+    constexpr int kXT = TT < 4 ? TT : 4;                            // tiles of a half of X
     int tid = threadIdx.x;
     asm volatile("" : "+v"(tid));   // what follows from it is made once per tile, not kept from tile to tile
     const int lane = tid & (kWave - 1);
     const int wave = uniform(tid / kWave);
     const bool second = wave >= kGemmWaves / 2;
-    const int across = wave % kAcross, q0 = wave / kAcross * (16 * TT);
-    const Reader<F::kXByK> xr(q0, lane);
-    const Reader<F::kWByK> wr(across * 16 * WT, lane);
+    const int across = wave % kAcross, half = wave / kAcross, q0 = half * (16 * TT);
+    const Reader<F::kXByK, 256> xr(half * 64, lane);
+    const Reader<F::kWByK, 512> wr(across * 16 * WT, lane);
     Acc<F::kI8> acc[TT][WT];
 #pragma unroll
     for (int m = 0; m < TT; ++m)
 #pragma unroll
         for (int i = 0; i < WT; ++i) acc[m][i] = Acc<F::kI8>{0, 0, 0, 0};
-    // One stage; the stage three further on goes to the buffer that was read last.
-    // settled: the next stage has arrived already.
-    const auto stage = [&](const u32x4 *from, u32x4 *to, bool settled) {
-        u32x4 w[WT], x[TT];
+    u32x4 w[2][WT];
+    // One stage: rows of the tiles m0 and on, from `x`.  settled: what the next stage
+    // needs has arrived already.
+    const auto stage = [&](const u32x4 *x_from, const u32x4 *w_from, auto m0_, bool settled, auto &&ask) {
+        constexpr int m0 = decltype(m0_)::value;
+        u32x4 x[2][kXT];
+        if constexpr (m0 == 0) {
 #pragma unroll
-        for (int i = 0; i < WT; ++i) w[i] = wr(from + kOperandVecs, i);
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int m = 0; m < TT; ++m) x[m] = xr(from, m);
-        feed.copy(a, nt, to);
-        if (second && !settled) copies_arrived<2 * kCopies>();
+                for (int i = 0; i < WT; ++i) w[h][i] = wr(w_from, h, i);
+        }
+        if constexpr (m0 < TT) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int m = 0; m < kXT; ++m) x[h][m] = xr(x_from, h, m);
+        }
+        ask();
+        if (second && !settled) copies_arrived<kInFlight>();
         barrier_after<63>();
-        __builtin_amdgcn_s_setprio(1);
+        if constexpr (m0 < TT) {
+            __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-        for (int m = 0; m < TT; ++m)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int i = 0; i < WT; ++i) acc[m][i] = multiply<F::kI8>(w[i], x[m], acc[m][i]);
-        // a stage's products stay between their barriers
+                for (int m = 0; m < kXT; ++m)
 #pragma unroll
-        for (int m = 0; m < TT; ++m)
+                    for (int i = 0; i < WT; ++i) acc[m0 + m][i] = multiply<F::kI8>(w[h][i], x[h][m], acc[m0 + m][i]);
+            // a stage's products stay between their barriers
 #pragma unroll
-            for (int i = 0; i < WT; ++i) asm volatile("" : "+v"(acc[m][i]));
-        __builtin_amdgcn_s_setprio(0);
-        if (!second && !settled) copies_arrived<2 * kCopies>();
+            for (int m = 0; m < kXT; ++m)
+#pragma unroll
+                for (int i = 0; i < WT; ++i) asm volatile("" : "+v"(acc[m0 + m][i]));
+            __builtin_amdgcn_s_setprio(0);
+        }
+        if (!second && !settled) copies_arrived<kInFlight>();
         barrier_after<63>();
     };
+    using First = std::integral_constant<int, 0>;
+    using Second = std::integral_constant<int, 4>;
     if (second) barrier_after<63>();
-    bool first = true;
+    bool begun = false;
     do {
-        stage(b0, b3, first);
+        stage(lds.xa0, lds.w0, First{}, !begun, [&]() { feed.ask_second(a, lds.xb1); });
         if (groups == 1) next_tile();
-        stage(b1, b0, first);
-        stage(b2, b1, false);
-        stage(b3, b2, false);
-        first = false;
+        stage(lds.xb0, lds.w0, Second{}, !begun, [&]() { feed.ask_first(a, lds.xa0, lds.w0); });
+        stage(lds.xa1, lds.w1, First{}, false, [&]() { feed.ask_second(a, lds.xb0); });
+        stage(lds.xb1, lds.w1, Second{}, false, [&]() { feed.ask_first(a, lds.xa1, lds.w1); });
+        begun = true;
     } while (--groups > 0);
     if (!second) barrier_after<63>();
     copies_arrived<0>();
-    finish<TT, WT, KIND, GATED>(a, t, acc, q0, t.c0 + across * (kSplit ? 8 : 16) * WT, b3 + wave * 256);
+    ended();
+    finish<TT, WT, KIND, GATED>(a, t, acc, q0, t.c0 + across * (kSplit ? 8 : 16) * WT, lds.xb1 + wave * 128);
 }
 
 template <Product KIND, bool GATED>
@@ -516,7 +578,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_product_tile(ProductArgs a,
     constexpr bool kSplit = F::kForward && GATED;
     constexpr int kOutCols = kSplit ? kTileCols / 2 : kTileCols;
     constexpr bool kW = KIND == Product::kBackwardW;
-    __shared__ u32x4 b0[kPairVecs], b1[kPairVecs], b2[kPairVecs], b3[kPairVecs];
+    __shared__ u32x4 xa0[kHalfVecs], xb0[kHalfVecs], w0[kWVecs], xa1[kHalfVecs], xb1[kHalfVecs], w1[kWVecs];
     __shared__ SegTable segs;
     __shared__ int2 s_scan[kGemmWaves];
     const int tid = threadIdx.x;
@@ -594,34 +656,40 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_product_tile(ProductArgs a,
     };
     ProductTile t;
     if (!tile_of(0, t)) return;                                    // the same for every wave
+    ProductTile nt = t;
+    bool more = tile_of(1, nt);
+    const Pairs lds{xa0, xb0, w0, xa1, xb1, w1};
     Feed<KIND, GATED> feed;
     feed.start(a, t);
-    feed.copy(a, t, b0);
-    feed.copy(a, t, b1);
-    feed.copy(a, t, b2);
+    feed.ask_first(a, xa0, w0);
+    feed.ask_second(a, xb0);
+    feed.ask_first(a, xa1, w1);
     copies_arrived<0>();
-    for (int round = 1;; ++round) {
-        const int groups = max((stages_of<KIND>(a, t) + 3) / 4, 1);
-        ProductTile nt = t;
-        bool more = false;
+    for (int round = 2;; ++round) {
+        const int groups = max((pairs_of<KIND>(a, t) + 1) / 2, 1);
         const auto next_tile = [&]() {
-            more = tile_of(round, nt);
             if (more)
                 feed.start(a, nt);
             else
                 feed.stop();
         };
-        barrier_after<63>();                                       // every wave's copies are there, the last tile's buffer 3 is free
+        // the tile after the next one, before the stores, for which its search would wait
+        ProductTile later = nt;
+        bool more_later = false;
+        const auto ended = [&]() { more_later = more && tile_of(round, later); };
+        barrier_after<63>();                                       // every wave's copies are there, the last tile's results have left LDS
         if (t.rows > 128)
-            run_tile<8, 4, KIND, GATED>(a, t, nt, feed, groups, b0, b1, b2, b3, next_tile);
+            run_tile<8, 4, KIND, GATED>(a, t, feed, groups, lds, next_tile, ended);
         else if (t.rows > 64)
-            run_tile<8, 2, KIND, GATED>(a, t, nt, feed, groups, b0, b1, b2, b3, next_tile);
+            run_tile<8, 2, KIND, GATED>(a, t, feed, groups, lds, next_tile, ended);
         else if (t.rows > 32)
-            run_tile<4, 2, KIND, GATED>(a, t, nt, feed, groups, b0, b1, b2, b3, next_tile);
+            run_tile<4, 2, KIND, GATED>(a, t, feed, groups, lds, next_tile, ended);
         else
-            run_tile<2, 2, KIND, GATED>(a, t, nt, feed, groups, b0, b1, b2, b3, next_tile);
+            run_tile<2, 2, KIND, GATED>(a, t, feed, groups, lds, next_tile, ended);
         if (!more) return;
         t = nt;
+        nt = later;
+        more = more_later;
     }
 }
 
@@ -786,7 +854,7 @@ bool long_segments(const ProductArgs &a) {
     if (!forward(a)) return true;
     if (a.entries == 0) return false;
     const double rows = static_cast<double>(a.entries), used = used_segments(a), weights = weight_bytes(a);
-    const double M = a.gated ? 2.0 * a.cols : a.cols, steps = a.inner * (a.kind == Product::kForwardI8 ? 1.0 : 2.0) / kStageKBytes;
+    const double M = a.gated ? 2.0 * a.cols : a.cols, steps = a.inner * (a.kind == Product::kForwardI8 ? 1.0 : 2.0) / 64;
     const double stream_tiles = std::max(used, rows / kStreamRows + used / 2), row_tiles = std::max(used, rows / kTileRows + used / 2);
     const double stream = 4 + std::max(stream_tiles * (M / (16 * kWTiles)) * steps / 3300, weights / 7.0e6);
     const double tiles = row_tiles * std::ceil(M / kTileCols), whole = std::floor(tiles / kCus), rest = tiles - whole * kCus;
