@@ -222,8 +222,14 @@ struct Feed {
             }
         }
     }
-    // No tile comes next: zeros.
-    __device__ __forceinline__ void stop() { left = 0; }
+    // The same, or zeros where no tile comes next.  (Without a branch: the two sides'
+    // last stores would be joined, and what they store to kept in memory.)
+    __device__ __forceinline__ void start_or_stop(const ProductArgs &a, const ProductTile &t) {
+        start(a, t);
+        const bool none = t.rows <= 0;
+        left = none ? 0 : left;
+        slot = none ? kMaxBalanceSlots : slot;
+    }
 
     // A buffer over `n` (at most 64) rows of k from `from`; `bytes` of the last row
     // belong to the tile.  Rows past the last read zeros.
@@ -620,10 +626,11 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_product_tile(ProductArgs a,
     const int whole = total / kCus * kCus, rest = total - whole;
     const int halvings = rest * 4 <= kCus ? 2 : (rest * 2 <= kCus ? 1 : 0), items = whole + (rest << halvings);
     const int place = static_cast<int>(blockIdx.x) / kXcds, xcd = static_cast<int>(blockIdx.x) % kXcds;
-    // What this workgroup takes in a round; false: nothing, then or later.
-    const auto tile_of = [&](int round, ProductTile &t) {
+    // What this workgroup takes in a round; nothing, then or later, where it has no rows.
+    const auto tile_of = [&](int round) {
+        ProductTile t{};                                           // rows 0: no tile
         const int left = min(items - round * kCus, kCus), run = (left + kXcds - 1) / kXcds, at = xcd * run + place;
-        if (place >= run || at >= left) return false;
+        if (place >= run || at >= left) return t;
         const int item = round * kCus + at, cut = item < whole ? 0 : halvings;
         const int tile = item - (cut ? item - whole - ((item - whole) >> cut) : 0);
         if constexpr (kW) {
@@ -652,12 +659,11 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_product_tile(ProductArgs a,
             t.first = uniform(t.first);
             t.end = uniform(t.end);
         }
-        return t.rows > 0;
+        return t;
     };
-    ProductTile t;
-    if (!tile_of(0, t)) return;                                    // the same for every wave
-    ProductTile nt = t;
-    bool more = tile_of(1, nt);
+    ProductTile t = tile_of(0);
+    if (t.rows <= 0) return;                                       // the same for every wave
+    ProductTile nt = tile_of(1);
     const Pairs lds{xa0, xb0, w0, xa1, xb1, w1};
     Feed<KIND, GATED> feed;
     feed.start(a, t);
@@ -667,16 +673,10 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_product_tile(ProductArgs a,
     copies_arrived<0>();
     for (int round = 2;; ++round) {
         const int groups = max((pairs_of<KIND>(a, t) + 1) / 2, 1);
-        const auto next_tile = [&]() {
-            if (more)
-                feed.start(a, nt);
-            else
-                feed.stop();
-        };
+        const auto next_tile = [&]() { feed.start_or_stop(a, nt); };
         // the tile after the next one, before the stores, for which its search would wait
-        ProductTile later = nt;
-        bool more_later = false;
-        const auto ended = [&]() { more_later = more && tile_of(round, later); };
+        ProductTile later{};
+        const auto ended = [&]() { later = tile_of(round); };
         barrier_after<63>();                                       // every wave's copies are there, the last tile's results have left LDS
         if (t.rows > 128)
             run_tile<8, 4, KIND, GATED>(a, t, feed, groups, lds, next_tile, ended);
@@ -686,10 +686,9 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_product_tile(ProductArgs a,
             run_tile<4, 2, KIND, GATED>(a, t, feed, groups, lds, next_tile, ended);
         else
             run_tile<2, 2, KIND, GATED>(a, t, feed, groups, lds, next_tile, ended);
-        if (!more) return;
+        if (nt.rows <= 0) return;
         t = nt;
         nt = later;
-        more = more_later;
     }
 }
 
