@@ -144,7 +144,7 @@ class _Descriptor:
     """A frozen descriptor; its C struct is built once and is no part of its state."""
 
     def __getstate__(self):
-        return {k: v for k, v in self.__dict__.items() if k != "_ref"}
+        return {k: v for k, v in self.__dict__.items() if k not in ("_ref", "_rows")}
 
 
 @dataclasses.dataclass(frozen=True)
@@ -873,9 +873,10 @@ def moe_expert_gemm_mx4(desc: LayoutDesc, layout: Layout, x: torch.Tensor, x_sca
 
 def _check_segments(desc: LayoutDesc, layout: Layout, balance: Optional[Balance], slots_per_rank: int, device):
     """The layout's arrays that a product reads, as C structs (layout, balance or None)."""
-    _check(layout.tokens_per_expert, "layout.tokens_per_expert", torch.int32, (desc.E,), device)
-    _check(layout.expert_offset, "layout.expert_offset", torch.int32, (desc.E + 1,), device)
-    b = moe_layout_bufs(layout.tokens_per_expert.data_ptr(), None, layout.expert_offset.data_ptr())
+    count, offset, E = layout.tokens_per_expert, layout.expert_offset, desc.E
+    _check(count, "layout.tokens_per_expert", torch.int32, (E,), device)
+    _check(offset, "layout.expert_offset", torch.int32, (E + 1,), device)
+    b = moe_layout_bufs(count.data_ptr(), None, offset.data_ptr())
     if balance is None:
         return ctypes.byref(b), None
     _check(balance.seg_offset, "balance.seg_offset", torch.int32, (desc.E + desc.R * slots_per_rank + 1,), device)
@@ -884,16 +885,24 @@ def _check_segments(desc: LayoutDesc, layout: Layout, balance: Optional[Balance]
 
 
 def _product_rows(desc: LayoutDesc, what: str) -> int:
-    rows = int(_lib.moe_max_recv_rows(_made_once(desc)))
-    if rows < 0:
-        raise MoeError(MOE_ERR_SHAPE, what)
+    """moe_max_recv_rows, worked out once per descriptor."""
+    rows = desc.__dict__.get("_rows")
+    if rows is None:
+        rows = int(_lib.moe_max_recv_rows(_made_once(desc)))
+        if rows < 0:
+            raise MoeError(MOE_ERR_SHAPE, what)
+        desc.__dict__["_rows"] = rows
     return rows
 
 
 def _check_rows(t: torch.Tensor, name: str, dtype, rows: int, width: int, device):
     """A row buffer [at least `rows`, width]."""
-    _check(t, name, dtype, None, device)
     shape = t.shape
+    # the usual case in one line
+    if t.is_cuda and t.dtype is dtype and t.is_contiguous() and len(shape) == 2 and shape[1] == width and shape[0] >= rows and \
+            t.device == device:
+        return
+    _check(t, name, dtype, None, device)
     if len(shape) != 2 or shape[1] != width or shape[0] < rows:
         raise ValueError(f"{name}: shape {tuple(shape)}, expected [at least {rows}, {width}]")
 

@@ -89,8 +89,25 @@ __global__ __launch_bounds__(kMaxWaves * kWave) void k_combine_backward(CombineB
     }
 }
 
+// Rows of y and d_y that the caches do not keep are read in one launch and written
+// in another: the memory turns from the one to the other less often, and d_out, the
+// smaller part, is read twice.  One launch / two (us; S tokens, H channels, K rows
+// each): S=256 H=7168 K=8, 29 MB, 13.9 / 15.5; S=1024 H=2048 K=6, 25 MB, 12.4 / 14.8;
+// S=512 H=7168 K=8, 59 MB, 28.1 / 25.9; S=4096, 470 MB, 189 / 171; S=16384 H=2048
+// K=6, 403 MB, 155 / 149.
+bool in_two(const CombineBackwardArgs &a) { return 2.0 * a.S * a.K * a.H > 40.0e6; }
+
 template <int K>
 void launch(const CombineBackwardArgs &a, dim3 grid, dim3 block, hipStream_t s) {
+    if (a.d_y != nullptr && a.d_w != nullptr && in_two(a)) {
+        // d_y may be y: what reads it goes first
+        CombineBackwardArgs weights = a, rows = a;
+        weights.d_y = nullptr;
+        rows.d_w = nullptr;
+        launch<K>(weights, grid, block, s);
+        launch<K>(rows, grid, block, s);
+        return;
+    }
     if (a.d_y == nullptr)
         hipLaunchKernelGGL((k_combine_backward<K, false, true>), grid, block, 0, s, a);
     else if (a.d_w == nullptr)

@@ -500,7 +500,8 @@ struct Pairs {
 // The two waves of a SIMD take turns: while one group of four waves multiplies the
 // other reads its operands of the next stage from LDS and asks for copies.  Each
 // half step ends with a barrier of the workgroup; the second group begins half a
-// step later.
+// step later.  Tiles of at most 64 rows have no second half of X and little to
+// multiply: they take a pair at a time, every wave at once, with half the barriers.
 template <int TT, int WT, Product KIND, bool GATED, typename NextTile, typename Ended>
 __device__ __forceinline__ void run_tile(const ProductArgs &a, const ProductTile &t, Feed<KIND, GATED> &feed, int groups,
                                          const Pairs &lds, NextTile &&next_tile, Ended &&ended) {
@@ -560,10 +561,47 @@ __device__ __forceinline__ void run_tile(const ProductArgs &a, const ProductTile
         if (!second && !settled) copies_arrived<kInFlight>();
         barrier_after<63>();
     };
+    bool begun = false;
+    if constexpr (TT <= 4) {
+        const auto pair = [&](u32x4 *x_from, u32x4 *w_from, u32x4 *second_to, bool settled, bool last) {
+            u32x4 x[2][kXT];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int i = 0; i < WT; ++i) w[h][i] = wr(w_from, h, i);
+#pragma unroll
+                for (int m = 0; m < kXT; ++m) x[h][m] = xr(x_from, h, m);
+            }
+            barrier_after<63>();                                   // the pair is in registers
+            feed.ask_second(a, second_to);
+            if (last) next_tile();
+            feed.ask_first(a, x_from, w_from);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int m = 0; m < kXT; ++m)
+#pragma unroll
+                    for (int i = 0; i < WT; ++i) acc[m][i] = multiply<F::kI8>(w[h][i], x[h][m], acc[m][i]);
+#pragma unroll
+            for (int m = 0; m < kXT; ++m)
+#pragma unroll
+                for (int i = 0; i < WT; ++i) asm volatile("" : "+v"(acc[m][i]));
+            if (!settled) copies_arrived<kInFlight>();
+            barrier_after<63>();
+        };
+        do {
+            pair(lds.xa0, lds.w0, lds.xb1, !begun, groups == 1);
+            pair(lds.xa1, lds.w1, lds.xb0, false, false);
+            begun = true;
+        } while (--groups > 0);
+        copies_arrived<0>();
+        ended();
+        finish<TT, WT, KIND, GATED>(a, t, acc, q0, t.c0 + across * (kSplit ? 8 : 16) * WT, lds.xb1 + wave * 128);
+        return;
+    }
     using First = std::integral_constant<int, 0>;
     using Second = std::integral_constant<int, 4>;
     if (second) barrier_after<63>();
-    bool begun = false;
     do {
         stage(lds.xa0, lds.w0, First{}, !begun, [&]() { feed.ask_second(a, lds.xb1); });
         if (groups == 1) next_tile();
@@ -663,13 +701,13 @@ __global__ __launch_bounds__(kGemmThreads, 2) void k_product_tile(ProductArgs a,
     };
     ProductTile t = tile_of(0);
     if (t.rows <= 0) return;                                       // the same for every wave
-    ProductTile nt = tile_of(1);
     const Pairs lds{xa0, xb0, w0, xa1, xb1, w1};
     Feed<KIND, GATED> feed;
     feed.start(a, t);
     feed.ask_first(a, xa0, w0);
     feed.ask_second(a, xb0);
     feed.ask_first(a, xa1, w1);
+    ProductTile nt = tile_of(1);
     copies_arrived<0>();
     for (int round = 2;; ++round) {
         const int groups = max((pairs_of<KIND>(a, t) + 1) / 2, 1);

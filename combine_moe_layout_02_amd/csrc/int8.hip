@@ -26,28 +26,60 @@ __device__ __forceinline__ unsigned int wave_max(unsigned int m) {
     return m;
 }
 
-// Four codes of the channels in two words of bf16 pairs.
-__device__ __forceinline__ unsigned int codes4(unsigned int lo, unsigned int hi, float scale) {
-    const float f[4] = {bf16_lo(lo), bf16_hi(lo), bf16_lo(hi), bf16_hi(hi)};
-    unsigned int c = 0u;
+// Codes of 16 channels.  The definition's quotient x / scale is a division, about
+// ten instructions, and would bound the conversion (98304 rows of 1408: 106 us).
+// With inv = 1/scale, fma(x, inv, 1.5 * 2^23) is x * inv rounded to an integer, ties
+// to even, in the sum's low bits.  x * inv is within 2^-24 of itself of the exact
+// quotient and the rounded quotient within as much, below 127 * 2^-23 together: where
+// x * inv is further than 2^-14 from the middle of two integers both round alike.
+// The others, one in 8000, are divided.  `exact`: a scale whose inverse is not to
+// be had so well, below 2^-100, divides too.
+__device__ __forceinline__ u32x4 codes16(u32x4 lo, u32x4 hi, float scale, float inv, bool exact) {
+    constexpr float kShift = 12582912.0f;
+    float f[16], t[16], far = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        // a scale below fp32's normal range is rounded: its quotient may pass 127
-        const float q = fminf(fmaxf(__builtin_rintf(f[i] / scale), -127.0f), 127.0f);
-        c |= (static_cast<unsigned int>(static_cast<int>(q)) & 255u) << (8 * i);
+        f[2 * i] = bf16_lo(lo[i]);
+        f[2 * i + 1] = bf16_hi(lo[i]);
+        f[8 + 2 * i] = bf16_lo(hi[i]);
+        f[9 + 2 * i] = bf16_hi(hi[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        t[i] = __builtin_fmaf(f[i], inv, kShift);
+        far = fmaxf(far, __builtin_fabsf(__builtin_fmaf(f[i], inv, kShift - t[i])));
+    }
+    if (exact || far > 0.5f - 0x1p-14f) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            // a scale below fp32's normal range is rounded: its quotient may pass 127
+            t[i] = fminf(fmaxf(__builtin_rintf(f[i] / scale), -127.0f), 127.0f) + kShift;
+    }
+    u32x4 c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const unsigned int a = __float_as_uint(t[4 * i]), b = __float_as_uint(t[4 * i + 1]), d = __float_as_uint(t[4 * i + 2]), e = __float_as_uint(t[4 * i + 3]);
+        c[i] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(e, d, 0x0C0C0400u), __builtin_amdgcn_perm(b, a, 0x0C0C0400u), 0x05040100u);
     }
     return c;
 }
 
-__device__ __forceinline__ u32x4 codes16(u32x4 lo, u32x4 hi, float scale) {
-    return u32x4{codes4(lo[0], lo[1], scale), codes4(lo[2], lo[3], scale), codes4(hi[0], hi[1], scale), codes4(hi[2], hi[3], scale)};
+// The largest of the workgroup's waves' values.
+__device__ __forceinline__ unsigned int join_waves(unsigned int m) {
+    __shared__ unsigned int part[kMaxWaves];
+    const int waves = blockDim.x / kWave;
+    if (waves == 1) return m;
+    if ((threadIdx.x & (kWave - 1)) == 0) part[threadIdx.x / kWave] = m;
+    __syncthreads();
+    for (int w = 0; w < waves; ++w) m = max(m, part[w]);
+    return m;
 }
 
 // Quantises one row of H channels with the whole workgroup; store(g, codes) for
-// each group g of 16 channels that the lane owns.  Returns the row's scale.
-template <typename Store>
+// each group g of 16 channels that the lane owns.  Returns the row's scale.  ONCE:
+// the row is read past the caches.
+template <bool ONCE, typename Store>
 __device__ __forceinline__ float quantize_row(const u32x4 *__restrict__ x, int H, Store &&store) {
-    __shared__ unsigned int part[kMaxWaves];
     const int n16 = H / 16, threads = blockDim.x, tid = threadIdx.x;
     u32x4 lo[kHeld], hi[kHeld];
     unsigned int m = 0u;
@@ -56,29 +88,25 @@ __device__ __forceinline__ float quantize_row(const u32x4 *__restrict__ x, int H
         const int g = j * threads + tid;
         lo[j] = hi[j] = u32x4{0u, 0u, 0u, 0u};
         if (g < n16) {
-            lo[j] = x[2 * g];
-            hi[j] = x[2 * g + 1];
+            lo[j] = ONCE ? __builtin_nontemporal_load(x + 2 * g) : x[2 * g];
+            hi[j] = ONCE ? __builtin_nontemporal_load(x + 2 * g + 1) : x[2 * g + 1];
         }
     }
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) m = max(m, max(mx4_absmax(lo[j]), mx4_absmax(hi[j])));
     for (int g = kHeld * threads + tid; g < n16; g += threads) m = max(m, max(mx4_absmax(x[2 * g]), mx4_absmax(x[2 * g + 1])));
-    m = wave_max(m);
-    if (threads > kWave) {
-        if ((tid & (kWave - 1)) == 0) part[tid / kWave] = m;
-        __syncthreads();
-        for (int w = 0; w < threads / kWave; ++w) m = max(m, part[w]);
-    }
+    m = join_waves(wave_max(m));
     const bool broken = m >= 0x7F80u;
     const float scale = broken ? __uint_as_float(0x7FC00000u) : __uint_as_float(m << 16) / 127.0f;
-    const bool none = broken || m == 0u;
+    const float inv = 1.0f / scale;
+    const bool none = broken || m == 0u, exact = !(scale >= 0x1p-100f);
     const u32x4 zero = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) {
         const int g = j * threads + tid;
-        if (g < n16) store(g, none ? zero : codes16(lo[j], hi[j], scale));
+        if (g < n16) store(g, none ? zero : codes16(lo[j], hi[j], scale, inv, exact));
     }
-    for (int g = kHeld * threads + tid; g < n16; g += threads) store(g, none ? zero : codes16(x[2 * g], x[2 * g + 1], scale));
+    for (int g = kHeld * threads + tid; g < n16; g += threads) store(g, none ? zero : codes16(x[2 * g], x[2 * g + 1], scale, inv, exact));
     return scale;
 }
 
@@ -93,7 +121,7 @@ __global__ __launch_bounds__(kMaxWaves * kWave) void k_quantize_i8(QuantizeI8Arg
     const int64_t row = row_of_block();
     if (row >= a.rows || (a.src != nullptr && a.src[row] < 0)) return;
     u32x4 *__restrict__ codes = static_cast<u32x4 *>(a.codes) + row * (a.H / 16);
-    const float scale = quantize_row(static_cast<const u32x4 *>(a.x) + row * (a.H / 8), a.H, [&](int g, u32x4 c) { codes[g] = c; });
+    const float scale = quantize_row<true>(static_cast<const u32x4 *>(a.x) + row * (a.H / 8), a.H, [&](int g, u32x4 c) { codes[g] = c; });
     if (threadIdx.x == 0) a.scales[row] = scale;
 }
 
@@ -130,7 +158,7 @@ __global__ __launch_bounds__(kMaxWaves * kWave) void k_dispatch_i8(DispatchI8Arg
 #pragma unroll
     for (int k = 0; k < K; ++k) p[k] = a.pos[static_cast<size_t>(t) * K + k];
     u32x4 *__restrict__ recv = static_cast<u32x4 *>(a.recv);
-    const float scale = quantize_row(static_cast<const u32x4 *>(a.hidden) + static_cast<size_t>(t) * (a.H / 8), a.H, [&](int g, u32x4 c) {
+    const float scale = quantize_row<false>(static_cast<const u32x4 *>(a.hidden) + static_cast<size_t>(t) * (a.H / 8), a.H, [&](int g, u32x4 c) {
 #pragma unroll
         for (int k = 0; k < K; ++k)
             if (p[k] >= 0) __builtin_nontemporal_store(c, recv + static_cast<size_t>(p[k]) * n16 + g);
