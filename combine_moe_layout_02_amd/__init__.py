@@ -113,8 +113,8 @@ def _load():
     L.moe_dispatch_mx4.argtypes = [D, B, P, I, P, P, P, P, P]
     L.moe_expert_gemm_mx4.argtypes = [D, B, ctypes.POINTER(moe_balance_bufs), I, P, P, I, P, P, I, I, P, P]
     BB = ctypes.POINTER(moe_balance_bufs)
-    L.moe_expert_gemm.argtypes = [D, B, BB, I, P, I, P, I, I, P, P, P]
-    L.moe_expert_gemm_backward_x.argtypes = [D, B, BB, I, P, I, P, I, P, P, P]
+    L.moe_expert_gemm.argtypes = [D, B, BB, I, P, I, P, I, I, P, I, P, P]
+    L.moe_expert_gemm_backward_x.argtypes = [D, B, BB, I, P, I, P, I, P, I, P, P]
     L.moe_expert_gemm_backward_w.argtypes = [D, B, BB, I, P, I, P, I, I, P, P]
     L.moe_combine_backward.argtypes = [D, B, P, I, P, P, P, P, P]
     L.moe_quantize_i8.argtypes = [P, I64, I, P, P, P, P]
@@ -896,7 +896,7 @@ def _product_rows(desc: LayoutDesc, what: str) -> int:
 
 
 def _check_rows(t: torch.Tensor, name: str, dtype, rows: int, width: int, device):
-    """A row buffer [at least `rows`, width]."""
+    """A row buffer [at least `rows`, width] of `dtype` (or of one of them)."""
     shape = t.shape
     # the usual case in one line
     if t.is_cuda and t.dtype is dtype and t.is_contiguous() and len(shape) == 2 and shape[1] == width and shape[0] >= rows and \
@@ -919,21 +919,28 @@ def _gemm_shape(desc: LayoutDesc, x: torch.Tensor, w: torch.Tensor, act: int, dt
     return H, (M // 2 if act == MOE_ACT_SWIGLU else M), M
 
 
+_PRE_TYPES = (torch.float32, torch.bfloat16)
+
+
+def _pre_type(pre) -> int:
+    return MOE_BF16 if pre is not None and pre.dtype is torch.bfloat16 else MOE_F32
+
+
 def moe_expert_gemm(desc: LayoutDesc, layout: Layout, x: torch.Tensor, w: torch.Tensor, act: int = MOE_ACT_NONE, out=None,
                     pre=None, balance: Optional[Balance] = None, slots_per_rank: int = 0, stream=None) -> torch.Tensor:
     """Every expert's bf16 rows times its weights: out [max_recv,N] bf16.
 
     x [max_recv,H]; w [E,M,H], M = N, or 2N with MOE_ACT_SWIGLU (N gate rows,
-    then N up rows).  ``pre`` [max_recv,2N] (SWIGLU only) receives the gate's
-    and up's values before the activation, for moe_expert_gemm_backward_x.
-    Rows that hold no entry are neither read nor written."""
+    then N up rows).  ``pre`` [max_recv,2N] (SWIGLU only; fp32, or bf16 for half the
+    bytes and gradients off by its rounding) receives the gate's and up's values
+    before the activation, for moe_expert_gemm_backward_x.  Rows that hold no entry are neither read nor written."""
     dev, rows = x.device, _product_rows(desc, "moe_expert_gemm")
     H, N, M = _gemm_shape(desc, x, w, act, torch.bfloat16, "moe_expert_gemm")
     _check_rows(x, "x", torch.bfloat16, rows, H, dev)
     if pre is not None:
         if act != MOE_ACT_SWIGLU:
             raise MoeError(MOE_ERR_SHAPE, "moe_expert_gemm")
-        _check_rows(pre, "pre", torch.bfloat16, rows, M, dev)
+        _check_rows(pre, "pre", _PRE_TYPES, rows, M, dev)
     if out is None:
         with _alloc_on(stream):
             out = torch.empty(rows, N, dtype=torch.bfloat16, device=dev)
@@ -942,7 +949,7 @@ def moe_expert_gemm(desc: LayoutDesc, layout: Layout, x: torch.Tensor, w: torch.
     b, bal = _check_segments(desc, layout, balance, slots_per_rank, dev)
     with _on_device(dev):
         rc = _lib.moe_expert_gemm(_made_once(desc), b, bal, slots_per_rank, x.data_ptr(), H, w.data_ptr(), N, act, _ptr(pre),
-                                  out.data_ptr(), _stream(stream, dev))
+                                  _pre_type(pre), out.data_ptr(), _stream(stream, dev))
     if rc != MOE_OK:
         raise MoeError(rc, "moe_expert_gemm")
     return out
@@ -953,8 +960,8 @@ def moe_expert_gemm_backward_x(desc: LayoutDesc, layout: Layout, d_out: torch.Te
     """Gradient of a product's rows: d_out [max_recv,N] times w [E,N,H] -> [max_recv,H] bf16.
 
     With ``pre`` [max_recv,2H], of the SWIGLU product that made those rows, the
-    gradient goes on through the activation to pre: [max_recv,2H] (which may be
-    pre itself).  Rows that hold no entry are neither read nor written."""
+    gradient goes on through the activation to pre: [max_recv,2H] (which may be a
+    bf16 pre itself).  Rows that hold no entry are neither read nor written."""
     dev, rows = d_out.device, _product_rows(desc, "moe_expert_gemm_backward_x")
     N = d_out.shape[-1]
     _check_rows(d_out, "d_out", torch.bfloat16, rows, N, dev)
@@ -965,7 +972,7 @@ def moe_expert_gemm_backward_x(desc: LayoutDesc, layout: Layout, d_out: torch.Te
     width = H
     if pre is not None:
         width = 2 * H
-        _check_rows(pre, "pre", torch.bfloat16, rows, width, dev)
+        _check_rows(pre, "pre", _PRE_TYPES, rows, width, dev)
     if out is None:
         with _alloc_on(stream):
             out = torch.empty(rows, width, dtype=torch.bfloat16, device=dev)
@@ -974,7 +981,7 @@ def moe_expert_gemm_backward_x(desc: LayoutDesc, layout: Layout, d_out: torch.Te
     b, bal = _check_segments(desc, layout, balance, slots_per_rank, dev)
     with _on_device(dev):
         rc = _lib.moe_expert_gemm_backward_x(_made_once(desc), b, bal, slots_per_rank, d_out.data_ptr(), N, w.data_ptr(), H,
-                                             _ptr(pre), out.data_ptr(), _stream(stream, dev))
+                                             _ptr(pre), _pre_type(pre), out.data_ptr(), _stream(stream, dev))
     if rc != MOE_OK:
         raise MoeError(rc, "moe_expert_gemm_backward_x")
     return out
@@ -1172,9 +1179,9 @@ class _DispatchFunction(torch.autograd.Function):
 
 class _ExpertFfnFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w_in, w_out, desc, layout, balance, slots):
+    def forward(ctx, x, w_in, w_out, desc, layout, balance, slots, pre_dtype):
         rows, M = _product_rows(desc, "expert_ffn"), w_in.shape[1]
-        pre = torch.empty(rows, M, dtype=torch.bfloat16, device=x.device)
+        pre = torch.empty(rows, M, dtype=pre_dtype, device=x.device)
         h = moe_expert_gemm(desc, layout, x, w_in, MOE_ACT_SWIGLU, pre=pre, balance=balance, slots_per_rank=slots)
         y = moe_expert_gemm(desc, layout, h, w_out, balance=balance, slots_per_rank=slots)
         moe_zero_padding(desc, layout, y)
@@ -1203,7 +1210,7 @@ class _ExpertFfnFunction(torch.autograd.Function):
         if want_x:
             dx = moe_expert_gemm_backward_x(ctx.desc, layout, d_pre, w_in, **at)
             moe_zero_padding(ctx.desc, layout, dx)
-        return dx, dw_in, dw_out, None, None, None, None
+        return dx, dw_in, dw_out, None, None, None, None, None
 
 
 class _CombineFunction(torch.autograd.Function):
@@ -1245,16 +1252,20 @@ def dispatch(desc: LayoutDesc, layout: Layout, hidden: torch.Tensor) -> torch.Te
 
 
 def expert_ffn(desc: LayoutDesc, layout: Layout, x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor,
-               balance: Optional[Balance] = None, slots_per_rank: int = 0) -> torch.Tensor:
+               balance: Optional[Balance] = None, slots_per_rank: int = 0, pre_dtype=torch.float32) -> torch.Tensor:
     """The experts' gated feed-forward block as an autograd function of its rows
     x [max_recv,H] and of the weights w_in [E,2N,H] (N gate rows, then N up rows) and
     w_out [E,H',N], all bf16: moe_expert_gemm twice.  Rows that hold no entry are
-    zero, in the result and in x's gradient."""
+    zero, in the result and in x's gradient.  The activation's arguments are kept
+    for the backward pass in ``pre_dtype``: fp32, or bf16 for half the memory and
+    gradients off by its rounding."""
     _no_capture("expert_ffn")
+    if pre_dtype not in _PRE_TYPES:
+        raise TypeError(f"pre_dtype {pre_dtype}, expected float32 or bfloat16")
     _check(x, "x", torch.bfloat16, (_product_rows(desc, "expert_ffn"), x.shape[-1]))
     _check(layout.src, "layout.src", torch.int32, (x.shape[0],), x.device)
     with _on_device(x.device):
-        return _ExpertFfnFunction.apply(x, w_in, w_out, desc, layout, balance, slots_per_rank)
+        return _ExpertFfnFunction.apply(x, w_in, w_out, desc, layout, balance, slots_per_rank, pre_dtype)
 
 
 def combine(desc: LayoutDesc, layout: Layout, expert_out: torch.Tensor, w=None, shared_out=None) -> torch.Tensor:

@@ -472,8 +472,8 @@ bool channels_ok(int32_t n, int32_t multiple) { return n >= multiple && n % mult
 moe_status run_product(const moe_layout_desc *desc, const moe_layout_bufs *layout, const moe_balance_bufs *bal,
                        int32_t slots_per_rank, moe::ProductArgs &a, void *stream) {
     // a tile's 256 rows of out lie within 32-bit offsets of each other
-    const bool wide = a.gated || a.out_f32;
-    if (wide && a.cols > moe::kMaxGemmChannels / 2) return MOE_ERR_SHAPE;
+    const bool wide = a.gated || a.out_f32, widest = a.gated && a.pre_f32;
+    if (a.cols > moe::kMaxGemmChannels / (widest ? 4 : (wide ? 2 : 1))) return MOE_ERR_SHAPE;
     if (!segments_of(desc, bal, slots_per_rank, a) || !moe::product_grid_ok(a)) return MOE_ERR_SHAPE;
     const bool i8 = a.kind == moe::Product::kForwardI8, weights = a.kind == moe::Product::kBackwardW;
     if (desc->S == 0 && !weights) return MOE_OK;
@@ -600,10 +600,10 @@ moe_status moe_expert_gemm_mx4(const moe_layout_desc *desc, const moe_layout_buf
 
 moe_status moe_expert_gemm(const moe_layout_desc *desc, const moe_layout_bufs *layout, const moe_balance_bufs *bal,
                            int32_t slots_per_rank, const void *x, int32_t H, const void *w, int32_t N, int32_t act, void *pre,
-                           void *out, void *stream) {
+                           int32_t pre_type, void *out, void *stream) {
     if (desc == nullptr || layout == nullptr) return MOE_ERR_NULL;
     if (!channels_ok(H, 8) || !channels_ok(N, 8) || (act != MOE_ACT_NONE && act != MOE_ACT_SWIGLU)) return MOE_ERR_SHAPE;
-    if (act == MOE_ACT_NONE && pre != nullptr) return MOE_ERR_SHAPE;
+    if (pre != nullptr && (act == MOE_ACT_NONE || (pre_type != MOE_F32 && pre_type != MOE_BF16))) return MOE_ERR_SHAPE;
     moe::ProductArgs a{};
     a.kind = moe::Product::kForward;
     a.gated = act == MOE_ACT_SWIGLU;
@@ -612,15 +612,17 @@ moe_status moe_expert_gemm(const moe_layout_desc *desc, const moe_layout_bufs *l
     a.x = x;
     a.w = w;
     a.pre = pre;
+    a.pre_f32 = pre != nullptr && pre_type == MOE_F32;
     a.out = out;
     return run_product(desc, layout, bal, slots_per_rank, a, stream);
 }
 
 moe_status moe_expert_gemm_backward_x(const moe_layout_desc *desc, const moe_layout_bufs *layout, const moe_balance_bufs *bal,
                                       int32_t slots_per_rank, const void *d_out, int32_t N, const void *w, int32_t H,
-                                      const void *pre, void *dx, void *stream) {
+                                      const void *pre, int32_t pre_type, void *dx, void *stream) {
     if (desc == nullptr || layout == nullptr) return MOE_ERR_NULL;
     if (!channels_ok(H, 8) || !channels_ok(N, 8)) return MOE_ERR_SHAPE;
+    if (pre != nullptr && ((pre_type != MOE_F32 && pre_type != MOE_BF16) || (pre_type == MOE_F32 && pre == dx))) return MOE_ERR_SHAPE;
     moe::ProductArgs a{};
     a.kind = moe::Product::kBackwardX;
     a.gated = pre != nullptr;
@@ -629,6 +631,7 @@ moe_status moe_expert_gemm_backward_x(const moe_layout_desc *desc, const moe_lay
     a.x = d_out;
     a.w = w;
     a.pre_in = pre;
+    a.pre_f32 = pre != nullptr && pre_type == MOE_F32;
     a.out = dx;
     return run_product(desc, layout, bal, slots_per_rank, a, stream);
 }

@@ -21,12 +21,13 @@ struct ProductArgs : Segments {
     Product kind;
     bool gated;              // forward: w holds `cols` gate rows, then `cols` up rows; kBackwardX: with pre_in
     bool out_f32;            // kBackwardW
+    bool pre_f32;            // of pre_in and pre; bf16 otherwise
     int32_t inner;           // channels of a row of x: summed over, but for kBackwardW (its n)
     int32_t cols;            // channels of a row of out (c)
     const void *x, *w;
     const float *xs, *ws;    // kForwardI8: [max_recv], [E, cols or 2*cols]
-    const void *pre_in;      // kBackwardX: [max_recv, 2*cols] bf16 or null
-    void *pre;               // kForward, gated: [max_recv, 2*cols] bf16 or null
+    const void *pre_in;      // kBackwardX: [max_recv, 2*cols] or null
+    void *pre;               // kForward, gated: [max_recv, 2*cols] or null
     void *out;               // rows of `cols`; of 2*cols for kBackwardX with pre_in
 };
 

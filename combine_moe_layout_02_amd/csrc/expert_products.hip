@@ -328,17 +328,17 @@ __device__ __forceinline__ void plane_put(u32x4 *plane, int q, int i, int g, f32
     reinterpret_cast<u32x2 *>(plane)[(q * CHUNKS + ((2 * i + (g >> 1)) ^ plane_turn<CHUNKS>(q))) * 2 + (g & 1)] = pack_bf16x4(v);
 }
 
-// Stores ROWS rows of a plane: channels c0 .. of rows `row_bytes` apart, from row q0
-// of `to`.  Rows outside the tile fall past the buffer's end, channels past `cols`
-// are sent there.
-template <int CHUNKS, int ROWS>
+// Stores the 16 rows of a plane: channels c0 .. of rows `row_bytes` apart, from row
+// q0 of `to`.  Rows outside the tile fall past the buffer's end, channels past
+// `cols` are sent there.
+template <int CHUNKS>
 __device__ __forceinline__ void plane_store(const u32x4 *plane, __amdgpu_buffer_rsrc_t to, unsigned int row_bytes, int q0, int c0, int cols) {
     const int lane = threadIdx.x & (kWave - 1);
     constexpr int kRows = kWave / CHUNKS;
 #pragma unroll
-    for (int j = 0; j < (ROWS + kRows - 1) / kRows; ++j) {
+    for (int j = 0; j < (15 + kRows) / kRows; ++j) {
         const int q = j * kRows + lane / CHUNKS, c = lane % CHUNKS;
-        const bool mine = ROWS % kRows == 0 || q < ROWS;
+        const bool mine = kRows <= 16 || q < 16;
         const u32x4 v = plane[mine ? q * CHUNKS + (c ^ plane_turn<CHUNKS>(q)) : 0];
         const unsigned int at = mine && c0 + c * 8 < cols ? (q0 + q) * row_bytes + 2u * (c0 + c * 8) : kPastEnd;
         __builtin_amdgcn_raw_buffer_store_b128(v, to, static_cast<int>(at), 0, kNonTemporal);
@@ -373,52 +373,66 @@ __device__ __forceinline__ void finish(const ProductArgs &a, const ProductTile &
     }
     if constexpr (KIND == Product::kBackwardX && GATED) {
         // the sums pass LDS in fp32, 32 channels at a time: a lane then has eight
-        // neighbouring channels of a row, and reads and writes 16 bytes of gate and up each
-        const auto pre = buffer_of(static_cast<const char *>(a.pre_in) + first * row_bytes * 2, static_cast<unsigned int>(t.rows) * row_bytes * 2);
+        // neighbouring channels of a row, and reads and writes whole 16 bytes of gate and up
         const auto to = buffer_of(static_cast<char *>(a.out) + first * row_bytes * 2, static_cast<unsigned int>(t.rows) * row_bytes * 2);
         const int q = lane / 4, c = lane & 3;
+        const auto all_rows = [&](auto pre_f32_) {
+            constexpr unsigned int kWide = decltype(pre_f32_)::value ? 2 : 1;   // vectors of eight channels of pre
+            const unsigned int pre_bytes = row_bytes * 2 * kWide;
+            const auto pre = buffer_of(static_cast<const char *>(a.pre_in) + first * pre_bytes, static_cast<unsigned int>(t.rows) * pre_bytes);
 #pragma unroll
-        for (int m = 0; m < TT; ++m) {
-            u32x4 gv[WT / 2], uv[WT / 2];
-            unsigned int at[WT / 2], at_up[WT / 2];
+            for (int m = 0; m < TT; ++m) {
+                u32x4 gv[WT / 2][kWide], uv[WT / 2][kWide];
+                unsigned int at[WT / 2], at_up[WT / 2];
 #pragma unroll
-            for (int p = 0; p < WT / 2; ++p) {
-                const int n = n0 + p * 32 + c * 8;
-                at[p] = n < a.cols ? (q0 + m * 16 + q) * row_bytes * 2 + 2u * n : kPastEnd;
-                at_up[p] = n < a.cols ? at[p] + row_bytes : kPastEnd;
-                gv[p] = __builtin_amdgcn_raw_buffer_load_b128(pre, static_cast<int>(at[p]), 0, 0);
-                uv[p] = __builtin_amdgcn_raw_buffer_load_b128(pre, static_cast<int>(at_up[p]), 0, 0);
-            }
+                for (int p = 0; p < WT / 2; ++p) {
+                    const int n = n0 + p * 32 + c * 8;
+                    at[p] = n < a.cols ? (q0 + m * 16 + q) * row_bytes * 2 + 2u * n : kPastEnd;
+                    at_up[p] = n < a.cols ? at[p] + row_bytes : kPastEnd;
 #pragma unroll
-            for (int p = 0; p < WT / 2; ++p) {
-                // eight chunks to the row
-#pragma unroll
-                for (int i = 0; i < 2; ++i) mine[r * 8 + ((4 * i + g) ^ (r & 7))] = __builtin_bit_cast(u32x4, acc[m][2 * p + i]);
-                wave_lds_fence();
-                const f32x4 lo = __builtin_bit_cast(f32x4, mine[q * 8 + ((2 * c) ^ (q & 7))]);
-                const f32x4 hi = __builtin_bit_cast(f32x4, mine[q * 8 + ((2 * c + 1) ^ (q & 7))]);
-                wave_lds_fence();
-                f32x4 dg[2], du[2];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const unsigned int gw = gv[p][e / 2], uw = uv[p][e / 2];
-                    float x, y;
-                    gated_gradient(e & 1 ? bf16_hi(gw) : bf16_lo(gw), e & 1 ? bf16_hi(uw) : bf16_lo(uw), e < 4 ? lo[e & 3] : hi[e & 3], x, y);
-                    dg[e / 4][e & 3] = x;
-                    du[e / 4][e & 3] = y;
+                    for (unsigned int e = 0; e < kWide; ++e) {
+                        gv[p][e] = __builtin_amdgcn_raw_buffer_load_b128(pre, static_cast<int>(n < a.cols ? at[p] * kWide + e * 16 : kPastEnd), 0, 0);
+                        uv[p][e] = __builtin_amdgcn_raw_buffer_load_b128(pre, static_cast<int>(n < a.cols ? at_up[p] * kWide + e * 16 : kPastEnd), 0, 0);
+                    }
                 }
-                const u32x2 a0 = pack_bf16x4(dg[0]), a1 = pack_bf16x4(dg[1]), b0 = pack_bf16x4(du[0]), b1 = pack_bf16x4(du[1]);
-                __builtin_amdgcn_raw_buffer_store_b128(u32x4{a0[0], a0[1], a1[0], a1[1]}, to, static_cast<int>(at[p]), 0, 0);
-                __builtin_amdgcn_raw_buffer_store_b128(u32x4{b0[0], b0[1], b1[0], b1[1]}, to, static_cast<int>(at_up[p]), 0, 0);
+#pragma unroll
+                for (int p = 0; p < WT / 2; ++p) {
+                    // eight chunks to the row
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) mine[r * 8 + ((4 * i + g) ^ (r & 7))] = __builtin_bit_cast(u32x4, acc[m][2 * p + i]);
+                    wave_lds_fence();
+                    const f32x4 lo = __builtin_bit_cast(f32x4, mine[q * 8 + ((2 * c) ^ (q & 7))]);
+                    const f32x4 hi = __builtin_bit_cast(f32x4, mine[q * 8 + ((2 * c + 1) ^ (q & 7))]);
+                    wave_lds_fence();
+                    const auto value = [&](const u32x4(&v)[kWide], int e) {
+                        if constexpr (kWide == 2) return __builtin_bit_cast(f32x4, v[e / 4])[e & 3];
+                        return e & 1 ? bf16_hi(v[0][e / 2]) : bf16_lo(v[0][e / 2]);
+                    };
+                    f32x4 dg[2], du[2];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float x, y;
+                        gated_gradient(value(gv[p], e), value(uv[p], e), e < 4 ? lo[e & 3] : hi[e & 3], x, y);
+                        dg[e / 4][e & 3] = x;
+                        du[e / 4][e & 3] = y;
+                    }
+                    const u32x2 a0 = pack_bf16x4(dg[0]), a1 = pack_bf16x4(dg[1]), b0 = pack_bf16x4(du[0]), b1 = pack_bf16x4(du[1]);
+                    __builtin_amdgcn_raw_buffer_store_b128(u32x4{a0[0], a0[1], a1[0], a1[1]}, to, static_cast<int>(at[p]), 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b128(u32x4{b0[0], b0[1], b1[0], b1[1]}, to, static_cast<int>(at_up[p]), 0, 0);
+                }
             }
-        }
+        };
+        if (a.pre_f32)
+            all_rows(std::true_type{});
+        else
+            all_rows(std::false_type{});
         return;
     }
     const auto to = buffer_of(static_cast<char *>(a.out) + first * row_bytes, static_cast<unsigned int>(t.rows) * row_bytes);
     const bool keep = kSplit && !F::kI8 && a.pre != nullptr;
-    const auto pre = keep ? buffer_of(static_cast<char *>(a.pre) + first * row_bytes * 2, static_cast<unsigned int>(t.rows) * row_bytes * 2) : to;
-    // up values lie `cols` channels further
-    const auto pre_up = keep ? buffer_of(static_cast<char *>(a.pre) + first * row_bytes * 2 + row_bytes, static_cast<unsigned int>(t.rows) * row_bytes * 2 - row_bytes) : to;
+    const unsigned int pre_up_at = row_bytes * (a.pre_f32 ? 2 : 1), pre_bytes = pre_up_at * 2;   // up values lie `cols` channels further
+    const auto pre = keep ? buffer_of(static_cast<char *>(a.pre) + first * pre_bytes, static_cast<unsigned int>(t.rows) * pre_bytes) : to;
+    const auto pre_up = keep ? buffer_of(static_cast<char *>(a.pre) + first * pre_bytes + pre_up_at, static_cast<unsigned int>(t.rows) * pre_bytes - pre_up_at) : to;
     f32x4 ws[F::kI8 ? WT : 1];
     if constexpr (F::kI8) {
 #pragma unroll
@@ -449,15 +463,24 @@ __device__ __forceinline__ void finish(const ProductArgs &a, const ProductTile &
             return v;
         };
         if constexpr (kSplit) {
-            if (keep) {
+            if (keep && a.pre_f32) {
+                // 16 bytes of one row per lane; a row's neighbours follow in the next store
+#pragma unroll
+                for (int i = 0; i < kOut; ++i) {
+                    const int c = n0 + i * 16 + 4 * g;
+                    const int at = static_cast<int>(c < a.cols ? (row + r) * pre_bytes + 4u * c : kPastEnd);
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, sums(i)), pre, at, 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, sums(i + kOut)), pre_up, at, 0, 0);
+                }
+            } else if (keep) {
 #pragma unroll
                 for (int i = 0; i < kOut; ++i) {
                     plane_put<kChunks>(mine, r, i, g, sums(i));
                     plane_put<kChunks>(mine + kPlane, r, i, g, sums(i + kOut));
                 }
                 wave_lds_fence();
-                plane_store<kChunks, 16>(mine, pre, 2 * row_bytes, row, n0, a.cols);
-                plane_store<kChunks, 16>(mine + kPlane, pre_up, 2 * row_bytes, row, n0, a.cols);
+                plane_store<kChunks>(mine, pre, pre_bytes, row, n0, a.cols);
+                plane_store<kChunks>(mine + kPlane, pre_up, pre_bytes, row, n0, a.cols);
                 wave_lds_fence();
             }
         }
@@ -472,7 +495,7 @@ __device__ __forceinline__ void finish(const ProductArgs &a, const ProductTile &
             plane_put<kChunks>(mine, r, i, g, v);
         }
         wave_lds_fence();
-        plane_store<kChunks, 16>(mine, to, row_bytes, row, n0, a.cols);
+        plane_store<kChunks>(mine, to, row_bytes, row, n0, a.cols);
         wave_lds_fence();
     }
 }
@@ -853,9 +876,16 @@ __global__ __launch_bounds__(kStreamWaves * kWave, 4) void k_product_stream(Prod
         if constexpr (GATED) {
             const f32x4 u = sum(kOutTiles + i, 1);
             if (!kI8 && a.pre != nullptr && mine) {
-                unsigned short *const pre = static_cast<unsigned short *>(a.pre) + row * 2 * a.cols + n;
-                *reinterpret_cast<u32x2 *>(pre) = pack_bf16x4(v);
-                *reinterpret_cast<u32x2 *>(pre + a.cols) = pack_bf16x4(u);
+                const size_t at = row * 2 * a.cols + n;
+                if (a.pre_f32) {
+                    float *const pre = static_cast<float *>(a.pre) + at;
+                    *reinterpret_cast<f32x4 *>(pre) = v;
+                    *reinterpret_cast<f32x4 *>(pre + a.cols) = u;
+                } else {
+                    unsigned short *const pre = static_cast<unsigned short *>(a.pre) + at;
+                    *reinterpret_cast<u32x2 *>(pre) = pack_bf16x4(v);
+                    *reinterpret_cast<u32x2 *>(pre + a.cols) = pack_bf16x4(u);
+                }
             }
 #pragma unroll
             for (int c = 0; c < 4; ++c) v[c] = silu(v[c]) * u[c];

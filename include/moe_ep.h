@@ -460,8 +460,11 @@ moe_status moe_expert_gemm_mx4(const moe_layout_desc *desc, const moe_layout_buf
  * MOE_ACT_SWIGLU with its gate and up weights, MOE_ACT_NONE with its down weights.
  *   x         [max_recv,H], H % 8 == 0.
  *   w         [E,M,H], M = N or (SWIGLU) 2*N; N % 8 == 0.
- *   pre       [max_recv,2*N] or NULL, with SWIGLU only: bf16(g), then bf16(u) of
- *             every row, as moe_expert_gemm_backward_x takes them.
+ *   pre       [max_recv,2*N] or NULL, with SWIGLU only: g, then u of every row,
+ *             as moe_expert_gemm_backward_x takes them; fp32 or bf16 (pre_type).
+ *             With fp32 the gradients see the activation's own arguments; bf16
+ *             takes half the bytes, and its rounding of them (2^-8) passes into
+ *             the gradients.  N at most 2^20 with fp32.
  *   out       [max_recv,N].
  *   layout, bal, slots_per_rank as for moe_expert_gemm_mx4.
  * H and M are at most 2^22; all row arrays 16-byte aligned.  Rows that hold no
@@ -471,7 +474,7 @@ moe_status moe_expert_gemm_mx4(const moe_layout_desc *desc, const moe_layout_buf
  * row) * ceil(M/32) at most 2^23 - 8. */
 moe_status moe_expert_gemm(const moe_layout_desc *desc, const moe_layout_bufs *layout, const moe_balance_bufs *bal,
                            int32_t slots_per_rank, const void *x, int32_t H, const void *w, int32_t N, int32_t act, void *pre,
-                           void *out, void *stream);
+                           int32_t pre_type, void *out, void *stream);
 
 /* Gradient of a product with respect to its rows, from d_out [max_recv,N] bf16
  * and the weights w [E,N,H] of the MOE_ACT_NONE product (of a SWIGLU one: N
@@ -481,11 +484,12 @@ moe_status moe_expert_gemm(const moe_layout_desc *desc, const moe_layout_bufs *l
  *             gradient goes on through the activation to pre itself.  With d the
  *             sum above in fp32, g = pre[r,h], u = pre[r,H+h], s = 1/(1+exp(-g)):
  *             dx[r,h] = bf16( d*u*s*(1 + g*(1-s)) ), dx[r,H+h] = bf16( d*g*s ),
- *             dx [max_recv,2*H], H at most 2^21; it may be pre's own buffer.
+ *             dx [max_recv,2*H], H at most 2^21 (2^20 with fp32); it may be the
+ *             buffer of a bf16 pre itself (pre_type), not of an fp32 one.
  * The values at g = -inf or +inf are NaN.  Arguments otherwise as above. */
 moe_status moe_expert_gemm_backward_x(const moe_layout_desc *desc, const moe_layout_bufs *layout, const moe_balance_bufs *bal,
                                       int32_t slots_per_rank, const void *d_out, int32_t N, const void *w, int32_t H,
-                                      const void *pre, void *dx, void *stream);
+                                      const void *pre, int32_t pre_type, void *dx, void *stream);
 
 /* Gradient of a product with respect to its weights:
  *   dw[e,n,h] = sum over the rows r of expert e, replicas' rows too, of

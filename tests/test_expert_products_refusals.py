@@ -32,7 +32,7 @@ CALLS = ("forward", "backward_x", "backward_w", "int8")
 
 
 def call(moe, which, desc=None, layout=None, bal=None, slots=0, H=64, N=64, act=0, x=FAKE, w=FAKE, out=FAKE, pre=None, xs=FAKE,
-         ws=FAKE, dtype=0):
+         ws=FAKE, dtype=0, pre_type=1):
     L = moe.lib()
     desc = moe.LayoutDesc(64, 2, 8, 2) if desc is None else desc
     layout = bufs(moe) if layout is None else layout
@@ -40,9 +40,9 @@ def call(moe, which, desc=None, layout=None, bal=None, slots=0, H=64, N=64, act=
     b = None if layout == "null" else ctypes.byref(layout)
     bal = None if bal is None else ctypes.byref(bal)
     if which == "forward":
-        return L.moe_expert_gemm(d, b, bal, slots, P(x), H, P(w), N, act, P(pre), P(out), None)
+        return L.moe_expert_gemm(d, b, bal, slots, P(x), H, P(w), N, act, P(pre), pre_type, P(out), None)
     if which == "backward_x":
-        return L.moe_expert_gemm_backward_x(d, b, bal, slots, P(x), N, P(w), H, P(pre), P(out), None)
+        return L.moe_expert_gemm_backward_x(d, b, bal, slots, P(x), N, P(w), H, P(pre), pre_type, P(out), None)
     if which == "backward_w":
         return L.moe_expert_gemm_backward_w(d, b, bal, slots, P(x), N, P(w), H, dtype, P(out), None)
     return L.moe_expert_gemm_i8(d, b, bal, slots, P(x), P(xs), H, P(w), P(ws), N, act, P(out), None)
@@ -80,6 +80,9 @@ def test_what_only_some_take(moe):
     assert call(moe, "forward", pre=FAKE) == moe.MOE_ERR_SHAPE          # only with the activation
     assert call(moe, "forward", act=1, pre=FAKE + 8) == moe.MOE_ERR_ALIGN
     assert call(moe, "backward_x", pre=FAKE + 8) == moe.MOE_ERR_ALIGN
+    assert call(moe, "forward", act=1, pre=FAKE, pre_type=2) == moe.MOE_ERR_SHAPE
+    assert call(moe, "backward_x", pre=FAKE, pre_type=-1) == moe.MOE_ERR_SHAPE
+    assert call(moe, "backward_x", pre=FAKE, pre_type=0, out=FAKE) == moe.MOE_ERR_SHAPE     # fp32: not into itself
     assert call(moe, "backward_w", dtype=2) == moe.MOE_ERR_SHAPE
     # rows of more than 2^23 bytes of results
     most = 1 << 21
@@ -88,6 +91,11 @@ def test_what_only_some_take(moe):
         assert call(moe, which, out=None, **kw) == moe.MOE_ERR_NULL
         size = "N" if "N" in kw else "H"
         assert call(moe, which, out=None, **{**kw, size: most + 8}) == moe.MOE_ERR_SHAPE
+    for which, kw in (("forward", dict(N=most // 2, act=1)), ("backward_x", dict(H=most // 2))):
+        kw.update(pre=FAKE, pre_type=0)
+        assert call(moe, which, out=None, **kw) == moe.MOE_ERR_NULL
+        size = "N" if "N" in kw else "H"
+        assert call(moe, which, out=None, **{**kw, size: most // 2 + 8}) == moe.MOE_ERR_SHAPE
     assert call(moe, "backward_w", H=1 << 22, dtype=1, out=None) == moe.MOE_ERR_NULL
     assert call(moe, "int8", H=72) == moe.MOE_ERR_SHAPE
     assert call(moe, "int8", H=131072) == moe.MOE_ERR_SHAPE             # 131072 * 128 * 128 passes 32 bits

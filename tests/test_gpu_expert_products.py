@@ -154,6 +154,13 @@ def check_gated(moe, c, rng, H, N):
     again = c.out(N)
     moe.moe_expert_gemm(c.desc, c.lay, c.poisoned(xb), dev_bf16(wb, DEV), act=moe.MOE_ACT_SWIGLU, out=again, **c.kw)
     assert torch.equal(out, again)
+    # the values before the activation in fp32
+    pre = torch.full((c.rows, 2 * N), 7.0, device=DEV)
+    moe.moe_expert_gemm(c.desc, c.lay, c.poisoned(xb), dev_bf16(wb, DEV), act=moe.MOE_ACT_SWIGLU, out=again, pre=pre, **c.kw)
+    assert torch.equal(out, again)
+    got = pre.cpu().numpy().astype(np.float64)
+    assert np.array_equal(got[c.held], y)
+    assert (got[~c.held] == 7).all()
 
 
 def check_backward_x(moe, c, rng, H, N):
@@ -174,6 +181,17 @@ def check_backward_x(moe, c, rng, H, N):
     want = np.concatenate([dh * u * ref64.silu_slope(g), dh * ref64.silu(g)], 1)
     bound = np.concatenate([np.abs(dh * u) * slope_bound(g), np.abs(dh) * silu_bound(g, np.ones_like(g))], 1)
     within(c.result(out), want, bound)
+    # the same values of pre in fp32
+    pre32, out32 = torch.where(torch.from_numpy(c.held).to(DEV)[:, None], pre.float(), float("nan")), c.out(2 * H)
+    moe.moe_expert_gemm_backward_x(c.desc, c.lay, c.poisoned(db), dev_bf16(wb, DEV), pre=pre32, out=out32, **c.kw)
+    assert torch.equal(out, out32)
+    p = rng.standard_normal((c.rows, 2 * H)).astype(np.float32) * 2
+    moe.moe_expert_gemm_backward_x(c.desc, c.lay, c.poisoned(db), dev_bf16(wb, DEV), pre=torch.from_numpy(p).to(DEV), out=out32, **c.kw)
+    p = p[c.held].astype(np.float64)
+    g, u = p[:, :H], p[:, H:]
+    want = np.concatenate([dh * u * ref64.silu_slope(g), dh * ref64.silu(g)], 1)
+    bound = np.concatenate([np.abs(dh * u) * slope_bound(g), np.abs(dh) * silu_bound(g, np.ones_like(g))], 1)
+    within(c.result(out32), want, bound)
     # into pre itself
     moe.moe_expert_gemm_backward_x(c.desc, c.lay, c.poisoned(db), dev_bf16(wb, DEV), pre=pre, out=pre, **c.kw)
     assert np.array_equal(host_bits(pre)[c.held], c.result(out))
