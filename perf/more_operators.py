@@ -205,7 +205,7 @@ def _own_ffn(s):
     if not s["case"]["train"]:
         h = moe.moe_expert_gemm(desc, lay, x, w_in, act=moe.MOE_ACT_SWIGLU)
         return moe.moe_expert_gemm(desc, lay, h, w_out, out=s["y"][:rows])
-    pre = torch.empty((rows, w_in.shape[1]), dtype=torch.bfloat16, device=x.device)
+    pre = torch.empty((rows, w_in.shape[1]), dtype=torch.float32, device=x.device)
     h = moe.moe_expert_gemm(desc, lay, x, w_in, act=moe.MOE_ACT_SWIGLU, pre=pre)
     y = moe.moe_expert_gemm(desc, lay, h, w_out, out=s["y"][:rows])
     d_pre = moe.moe_expert_gemm_backward_x(desc, lay, s["dy"], w_out, pre=pre)
