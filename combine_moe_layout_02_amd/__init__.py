@@ -1181,7 +1181,7 @@ class _ExpertFfnFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w_in, w_out, desc, layout, balance, slots, pre_dtype):
         rows, M = _product_rows(desc, "expert_ffn"), w_in.shape[1]
-        pre = torch.empty(rows, M, dtype=pre_dtype, device=x.device)
+        pre = None if pre_dtype is None else torch.empty(rows, M, dtype=pre_dtype, device=x.device)
         h = moe_expert_gemm(desc, layout, x, w_in, MOE_ACT_SWIGLU, pre=pre, balance=balance, slots_per_rank=slots)
         y = moe_expert_gemm(desc, layout, h, w_out, balance=balance, slots_per_rank=slots)
         moe_zero_padding(desc, layout, y)
@@ -1257,15 +1257,16 @@ def expert_ffn(desc: LayoutDesc, layout: Layout, x: torch.Tensor, w_in: torch.Te
     x [max_recv,H] and of the weights w_in [E,2N,H] (N gate rows, then N up rows) and
     w_out [E,H',N], all bf16: moe_expert_gemm twice.  Rows that hold no entry are
     zero, in the result and in x's gradient.  The activation's arguments are kept
-    for the backward pass in ``pre_dtype``: fp32, or bf16 for half the memory and
-    gradients off by its rounding."""
+    for the gradients of x and w_in in ``pre_dtype``: fp32, or bf16 for half the
+    memory and gradients off by its rounding."""
     _no_capture("expert_ffn")
     if pre_dtype not in _PRE_TYPES:
         raise TypeError(f"pre_dtype {pre_dtype}, expected float32 or bfloat16")
     _check(x, "x", torch.bfloat16, (_product_rows(desc, "expert_ffn"), x.shape[-1]))
     _check(layout.src, "layout.src", torch.int32, (x.shape[0],), x.device)
+    kept = pre_dtype if torch.is_grad_enabled() and (x.requires_grad or w_in.requires_grad) else None
     with _on_device(x.device):
-        return _ExpertFfnFunction.apply(x, w_in, w_out, desc, layout, balance, slots_per_rank, pre_dtype)
+        return _ExpertFfnFunction.apply(x, w_in, w_out, desc, layout, balance, slots_per_rank, kept)
 
 
 def combine(desc: LayoutDesc, layout: Layout, expert_out: torch.Tensor, w=None, shared_out=None) -> torch.Tensor:

@@ -200,3 +200,21 @@ def test_host_tensors(moe):
                lambda: moe.moe_expert_gemm_i8(desc, lay, q, s, torch.zeros((2, 16, 16), dtype=torch.int8), torch.zeros((2, 16)))):
         with pytest.raises(ValueError, match="device tensor"):
             go()
+
+
+def test_outputs_over_inputs(moe):
+    """An output that is an input's own buffer is refused where the call does not allow it."""
+    other = [FAKE + (1 << 20) * i for i in range(1, 8)]
+    for which in CALLS:
+        for kw in (dict(x=other[0], w=other[1], out=other[0]), dict(x=other[0], w=other[1], out=other[1])):
+            assert call(moe, which, xs=other[2], ws=other[3], **kw) == moe.MOE_ERR_SHAPE, (which, kw)
+    for same in other[:3]:
+        assert call(moe, "forward", act=1, x=other[0], w=other[1], out=other[2], pre=same, pre_type=0) == moe.MOE_ERR_SHAPE
+    assert call(moe, "backward_x", x=other[0], w=other[1], out=other[2], pre=other[2], pre_type=0) == moe.MOE_ERR_SHAPE
+    L, a, b, c, d = moe.lib(), *other[:4]
+    assert L.moe_quantize_i8(P(a), 4, 16, None, P(a), P(b), None) == moe.MOE_ERR_SHAPE
+    assert L.moe_dequantize_i8(P(a), P(b), 4, 16, None, P(a), None) == moe.MOE_ERR_SHAPE
+    desc, layout = ctypes.byref(moe.LayoutDesc(64, 2, 8, 2).c()), ctypes.byref(bufs(moe))
+    assert L.moe_dispatch_i8(desc, layout, P(a), 16, None, P(a), P(b), None, None) == moe.MOE_ERR_SHAPE
+    assert L.moe_combine_backward(desc, layout, P(a), 16, P(b), P(c), P(a), P(d), None) == moe.MOE_ERR_SHAPE
+    assert L.moe_combine_backward(desc, layout, P(a), 16, P(b), P(c), P(d), P(c), None) == moe.MOE_ERR_SHAPE

@@ -343,5 +343,14 @@ def test_what_is_kept_of_the_activation(moe):
     # h or d_pre, and the result: each rounded once
     for got, ref in zip(a[1:], want):
         assert float((got.double() - ref).norm()) <= 2 * 2.0 ** -8 * float(ref.norm())
+    # nothing is kept where no gradient needs it
+    assert torch.equal(moe.expert_ffn(c.desc, c.lay, x.detach(), w_in.detach(), w_out), a[0])
+    y = moe.expert_ffn(c.desc, c.lay, x.detach(), w_in.detach(), w_out)
+    assert torch.equal(torch.autograd.grad(y, w_out, d)[0], a[3])
+    with torch.no_grad():
+        before = torch.cuda.memory_allocated()
+        y = moe.expert_ffn(c.desc, c.lay, x, w_in, w_out)
+        assert torch.equal(y, a[0]) and not y.requires_grad
+        assert torch.cuda.memory_allocated() - before <= c.rows * 96 * 2 + 2048
     with pytest.raises(TypeError):
         moe.expert_ffn(c.desc, c.lay, x, w_in, w_out, pre_dtype=torch.float16)
