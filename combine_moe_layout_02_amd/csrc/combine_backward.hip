@@ -1,8 +1,9 @@
 // Gradient of combine: of out[t] = sum over k of w[t,k] * y[pos[t,k]] (+ shared),
 //   d_y[pos[t,k]] = bf16(w[t,k] * d_out[t]),
 //   d_w[t,k] = sum over channels of d_out[t,c] * y[pos[t,k],c], 0 where pos is -1
-// (d_shared is d_out itself).  Every row of d_out and y is read once and every
-// row of d_y written once: HBM bounds it.
+// (d_shared is d_out itself).  Every row of y is read once, every row of d_y written
+// once, d_out read once or (in_two) twice: HBM bounds it, 4096 tokens of 7168 with
+// eight rows each 171 us, 6.2 TB/s.
 //
 // One workgroup per token; a wave takes every W-th chunk of 512 channels, 16
 // bytes per lane, with all K gathers in flight before the first product, as in
