@@ -922,6 +922,10 @@ def _gemm_shape(desc: LayoutDesc, x: torch.Tensor, w: torch.Tensor, act: int, dt
 _PRE_TYPES = (torch.float32, torch.bfloat16)
 
 
+def _check_pre(pre: torch.Tensor, rows: int, width: int, device):
+    _check_rows(pre, "pre", pre.dtype if pre.dtype in _PRE_TYPES else _PRE_TYPES, rows, width, device)
+
+
 def _pre_type(pre) -> int:
     return MOE_BF16 if pre is not None and pre.dtype is torch.bfloat16 else MOE_F32
 
@@ -940,7 +944,7 @@ def moe_expert_gemm(desc: LayoutDesc, layout: Layout, x: torch.Tensor, w: torch.
     if pre is not None:
         if act != MOE_ACT_SWIGLU:
             raise MoeError(MOE_ERR_SHAPE, "moe_expert_gemm")
-        _check_rows(pre, "pre", _PRE_TYPES, rows, M, dev)
+        _check_pre(pre, rows, M, dev)
     if out is None:
         with _alloc_on(stream):
             out = torch.empty(rows, N, dtype=torch.bfloat16, device=dev)
@@ -972,7 +976,7 @@ def moe_expert_gemm_backward_x(desc: LayoutDesc, layout: Layout, d_out: torch.Te
     width = H
     if pre is not None:
         width = 2 * H
-        _check_rows(pre, "pre", _PRE_TYPES, rows, width, dev)
+        _check_pre(pre, rows, width, dev)
     if out is None:
         with _alloc_on(stream):
             out = torch.empty(rows, width, dtype=torch.bfloat16, device=dev)
