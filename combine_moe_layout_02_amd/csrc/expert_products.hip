@@ -146,6 +146,12 @@ __device__ __forceinline__ const char *uniform(const char *p) {
     return reinterpret_cast<const char *>(hi << 32 | lo);
 }
 
+// A buffer over `n` (at most 64) rows of k from `from`; `bytes` of the last row
+// belong to the tile.  Rows past the last read zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of_k(const char *from, int n, unsigned int bytes, unsigned int row_bytes) {
+    return buffer_of(uniform(from), n > 0 ? static_cast<unsigned int>(n - 1) * row_bytes + bytes : 0u);
+}
+
 struct ProductTile {
     int row0, rows;    // rows q: of the receive buffer, or (kBackwardW) n
     int expert;
@@ -253,11 +259,6 @@ struct Feed {
         slot = none ? kMaxBalanceSlots : slot;
     }
 
-    // A buffer over `n` (at most 64) rows of k from `from`; `bytes` of the last row
-    // belong to the tile.  Rows past the last read zeros.
-    __device__ __forceinline__ static __amdgpu_buffer_rsrc_t rows_of_k(const char *from, int n, unsigned int bytes, unsigned int row_bytes) {
-        return buffer_of(uniform(from), n > 0 ? static_cast<unsigned int>(n - 1) * row_bytes + bytes : 0u);
-    }
     // kPastEnd for the lanes whose chunk of the pair lies past the row's end.
     __device__ __forceinline__ unsigned int gone() const {
         const int bytes = F::kForward ? left : 2 * left;
@@ -918,20 +919,147 @@ __global__ __launch_bounds__(kStreamWaves * kWave, 4) void k_product_stream(Prod
     }
 }
 
+// ---------------------------------------------------------------------------
+// the rows' gradient of short segments
+// ---------------------------------------------------------------------------
+
+// The same for W's rows of k: 16 rows by 64 channels, a whole line of each of W's
+// rows; a unit is 32 of those.  32-byte block b of row k lies at b ^ back_turn(k), so
+// that the eight rows that half a wave's transposing read takes, 128 bytes apart,
+// lie in eight different groups of banks.  A tile's workgroup walks all of k alone, in
+// steps as long as a copy takes: with few rows there are too few of those for the
+// chip (16 tokens, 16 experts, 2048 x 704: 25 us, here 9).  256 experts, 2048 x 7168
+// weights, four rows each: 1164 us, 6.4 TB/s of weights.
+constexpr int kBackTiles = 4;
+constexpr int kBackCols = 16 * kBackTiles;
+constexpr int kBackUnit = 32;                  // rows of k
+static_assert(kBackUnit * 8 == kUnitVecs && kStreamWaves == kBackTiles, "a unit as long as the forward's; a wave joins a tile");
+__device__ __forceinline__ int back_turn(int k) { return (k >> 1 & 1) | (k >> 2 & 2); }
+
+template <bool GATED, bool ONCE>
+__global__ __launch_bounds__(kStreamWaves * kWave, 4) void k_product_stream_back(ProductArgs a, int tiles_c) {
+    __shared__ u32x4 unit0[kStreamWaves][kUnitVecs], unit1[kStreamWaves][kUnitVecs];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = uniform(static_cast<int>(threadIdx.x) / kWave);
+    RowTile t;
+    if (!find_tile<kStreamRows>(a, blockIdx.x, tiles_c, t)) return;   // the same for every wave
+    t.row0 = uniform(t.row0);
+    t.rows = uniform(t.rows);
+    t.expert = uniform(t.expert);
+    t.ntile = uniform(t.ntile);
+    const int n0 = t.ntile * kBackCols;
+    const int r = lane & 15, g = lane >> 4;
+    const unsigned int xb = static_cast<unsigned int>(a.inner) * 2, cb = static_cast<unsigned int>(a.cols) * 2;
+    const char *const first = static_cast<const char *>(a.w) + (static_cast<size_t>(t.expert) * a.inner * a.cols + n0) * 2;
+    const unsigned int bytes = min(2u * kBackCols, cb - 2u * n0);
+    const auto xbuf = buffer_of(static_cast<const char *>(a.x) + static_cast<size_t>(t.row0) * xb, t.rows * xb);
+    const int units = (a.inner + kBackUnit - 1) / kBackUnit;
+    const int begin = units * wave / kStreamWaves, end = units * (wave + 1) / kStreamWaves;
+    // Copies of 8 rows of k: lane l's vector is of row l/8, place l%8.  Channels past the
+    // last one read what follows them, and count for nothing.
+    const unsigned int row = lane / 8 * cb, chunk = (((lane & 7) >> 1 ^ back_turn(lane / 8)) * 2 + (lane & 1)) * 16;
+    const auto copy_unit = [&](int u, u32x4 *to) {
+        const auto b = rows_of_k(first + static_cast<size_t>(u) * kBackUnit * cb, u < end ? min(a.inner - u * kBackUnit, kBackUnit) : 0, bytes, cb);
+#pragma unroll
+        for (int j = 0; j < kBackUnit / 8; ++j) copy_to_lds<ONCE>(b, to + j * 64, row + j * 8 * cb + (j & 1 ? chunk ^ 64u : chunk), 0);
+    };
+    f32x4 acc[kBackTiles];
+#pragma unroll
+    for (int i = 0; i < kBackTiles; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const unsigned int xo = r * xb + g * 16;
+    const auto load_rows = [&](int u) {
+        const unsigned int at = static_cast<unsigned int>(u) * kBackUnit * 2;
+        return __builtin_amdgcn_raw_buffer_load_b128(xbuf, static_cast<int>(u >= end || at + g * 16 >= xb ? kPastEnd : xo), static_cast<int>(min(at, xb - 1)), 0);
+    };
+    // of tile i: rows 8g .. 8g+3 of k, then 8g+4 .. 8g+7
+    const int k = 8 * g + r / 4;
+    const unsigned int read = static_cast<unsigned int>(k * 128 + back_turn(k) * 32 + (r & 3) * 8);
+    const auto products = [&](const u32x4 *from, u32x4 x) {
+        typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+#pragma unroll
+        for (int i = 0; i < kBackTiles; ++i) {
+            const char *const p = reinterpret_cast<const char *>(from) + (read ^ static_cast<unsigned int>(i * 32));
+            const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p)));
+            const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 4 * 128)));
+            acc[i] = multiply<false>(u32x4{lo[0], lo[1], hi[0], hi[1]}, x, acc[i]);
+        }
+        // the unit is read before anything is copied over it
+#pragma unroll
+        for (int i = 0; i < kBackTiles; ++i) asm volatile("" : "+v"(acc[i]) : : "memory");
+    };
+    // Past the wave's last unit zeros are copied and multiplied: without branches the
+    // loads in flight are counted.  Before a unit's products its copies are there:
+    // in flight are the next one's four and its row's load.
+    if (begin < end) {
+        copy_unit(begin, unit0[wave]);
+        u32x4 now = load_rows(begin);
+        copy_unit(begin + 1, unit1[wave]);
+        for (int u = begin; u < end; u += 2) {
+            const u32x4 next = load_rows(u + 1);
+            copies_arrived<kBackUnit / 8 + 1>();
+            products(unit0[wave], now);
+            copy_unit(u + 2, unit0[wave]);
+            now = load_rows(u + 2);
+            copies_arrived<kBackUnit / 8 + 1>();
+            products(unit1[wave], next);
+            copy_unit(u + 3, unit1[wave]);
+        }
+        copies_arrived<0>();
+    }
+    // the sums meet where the weights were
+    __syncthreads();
+    f32x4(*const part)[kBackTiles][kWave] = reinterpret_cast<f32x4(*)[kBackTiles][kWave]>(&unit0[0][0]);
+#pragma unroll
+    for (int i = 0; i < kBackTiles; ++i) part[wave][i][lane] = acc[i];
+    __syncthreads();
+    const int n = n0 + wave * 16 + 4 * g;
+    if (r >= t.rows || n >= a.cols) return;
+    f32x4 d = part[0][wave][lane];
+#pragma unroll
+    for (int q = 1; q < kStreamWaves; ++q) d += part[q][wave][lane];
+    const size_t out_row = (static_cast<size_t>(t.row0) + r) * (GATED ? 2 : 1) * a.cols + n;
+    unsigned short *const out = static_cast<unsigned short *>(a.out) + out_row;
+    if constexpr (GATED) {
+        f32x4 gate, up, dg, du;
+        if (a.pre_f32) {
+            const float *const pre = static_cast<const float *>(a.pre_in) + out_row;
+            gate = *reinterpret_cast<const f32x4 *>(pre);
+            up = *reinterpret_cast<const f32x4 *>(pre + a.cols);
+        } else {
+            const unsigned short *const pre = static_cast<const unsigned short *>(a.pre_in) + out_row;
+            const u32x2 gw = *reinterpret_cast<const u32x2 *>(pre), uw = *reinterpret_cast<const u32x2 *>(pre + a.cols);
+            gate = f32x4{bf16_lo(gw[0]), bf16_hi(gw[0]), bf16_lo(gw[1]), bf16_hi(gw[1])};
+            up = f32x4{bf16_lo(uw[0]), bf16_hi(uw[0]), bf16_lo(uw[1]), bf16_hi(uw[1])};
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float x, y;
+            gated_gradient(gate[e], up[e], d[e], x, y);
+            dg[e] = x;
+            du[e] = y;
+        }
+        *reinterpret_cast<u32x2 *>(out) = pack_bf16x4(dg);
+        *reinterpret_cast<u32x2 *>(out + a.cols) = pack_bf16x4(du);
+    } else {
+        *reinterpret_cast<u32x2 *>(out) = pack_bf16x4(d);
+    }
+}
+
 bool forward(const ProductArgs &a) { return a.kind == Product::kForward || a.kind == Product::kForwardI8; }
 
 double weight_bytes(const ProductArgs &a) {
-    return used_segments(a) * (a.gated ? 2.0 : 1.0) * a.cols * a.inner * (a.kind == Product::kForwardI8 ? 1.0 : 2.0);
+    return used_segments(a) * (a.gated && forward(a) ? 2.0 : 1.0) * a.cols * a.inner * (a.kind == Product::kForwardI8 ? 1.0 : 2.0);
 }
 // Weights that the Infinity Cache (256 MB) does not hold from call to call are
 // read past the caches by the streaming kernel.
 bool weights_once(const ProductArgs &a) { return weight_bytes(a) > 320.0e6; }
 
-// The rule between a forward product's two kernels: the sooner by these estimates,
-// in microseconds.  Experts with a row: as many as a routing at random leaves with
+// The rule between the two kernels of a forward product, or of the rows' gradient: the
+// sooner by these estimates, in microseconds.  Experts with a row: as many as a routing at random leaves with
 // one.  Steps are of 64 bytes of k.
 //   stream: a start of 4 us; a workgroup's work is one 16-row tile by 32 weight
-//     rows, 3300 steps of such a microsecond, or the weights at 7.0 TB/s.
+//     rows (gradient: 64 channels), 3300 steps of such (1650) a microsecond, or the
+//     weights at 7.0 TB/s.
 //   tile: a start of 6 us, then rounds of 256 workgroups one tile each, 0.38 us a
 //     step and 0.0018 more for each row of a tile, or of a part of it in the last
 //     round; or the weights at 5.5 TB/s.
@@ -941,11 +1069,22 @@ bool weights_once(const ProductArgs &a) { return weight_bytes(a) > 320.0e6; }
 //   E=64  H=2048 M=2816  m=6 107 / 171    m=24 205 / 172
 //   E=8   H=7168 M=2048  m=2 30 / 87      m=8 34 / 88     m=32 55 / 97
 //   E=4   H=7168 M=512   m=32 17 / 95     m=128 33 / 97
+// The gradient of K channels with respect to H (m as a mean, routed at random):
+//   E=256 K=7168 H=1024  m=4 603 / 565    K=2048 H=7168 m=4 1164 / 1225
+//   E=64  K=2048 H=1408  m=6 60 / 76      m=24 127 / 82
+//   E=64  K=2816 H=2048  m=6 127 / 123    m=24 231 / 126
+//   E=16  K=512  H=264   m=32 9 / 13      K=528 H=512 m=32 7.6 / 12
+//   E=16  K=2048 H=704   m=2 9 / 25       K=1024 H=704 m=64 14 / 20
+//   E=8   K=7168 H=2048  m=4 38 / 70      K=4096 H=7168 m=4 95 / 83
+//   E=4   K=4096 H=512   m=32 11 / 49     m=128 20 / 49
 bool long_segments(const ProductArgs &a) {
-    if (!forward(a)) return true;
+    const bool back = a.kind == Product::kBackwardX;
+    if (a.kind == Product::kBackwardW) return true;
     if (a.entries == 0) return false;
+    // a grid of tiles can always be numbered
+    if (back && most_tiles(a, kStreamRows) * ((a.cols + kBackCols - 1) / kBackCols) > 1 << 20) return true;
     const double rows = static_cast<double>(a.entries), used = used_segments(a), weights = weight_bytes(a);
-    const double M = a.gated ? 2.0 * a.cols : a.cols, steps = a.inner * (a.kind == Product::kForwardI8 ? 1.0 : 2.0) / 64;
+    const double M = a.gated && !back ? 2.0 * a.cols : a.cols, steps = a.inner * (a.kind == Product::kForwardI8 ? 1.0 : 2.0) / 64;
     const double stream_tiles = std::max(used, rows / kStreamRows + used / 2), row_tiles = std::max(used, rows / kTileRows + used / 2);
     const double stream = 4 + std::max(stream_tiles * (M / (16 * kWTiles)) * steps / 3300, weights / 7.0e6);
     const double tiles = row_tiles * std::ceil(M / kTileCols), whole = std::floor(tiles / kCus), rest = tiles - whole * kCus;
@@ -963,7 +1102,7 @@ struct Grid {
 };
 Grid grid_of(const ProductArgs &a) {
     const bool tiles = long_segments(a), split = a.gated && forward(a);
-    const int cols = tiles ? kTileCols : kWTiles * 16, out = split ? cols / 2 : cols;
+    const int cols = tiles ? kTileCols : (a.kind == Product::kBackwardX ? kBackCols : kWTiles * 16), out = split ? cols / 2 : cols;
     Grid g;
     g.tiles_c = (a.cols + out - 1) / out;
     const int64_t rows = a.kind == Product::kBackwardW ? static_cast<int64_t>(a.E) * ((a.inner + kTileRows - 1) / kTileRows)
@@ -995,12 +1134,22 @@ hipError_t launch_product(const ProductArgs &a, hipStream_t s) {
         else                                                                                                                  \
             hipLaunchKernelGGL((k_product_stream<Product::KIND, GATED, false>), grid, stream_block, 0, s, a, g.tiles_c);      \
     } while (0)
+#define MOE_BACK(GATED)                                                                                                       \
+    do {                                                                                                                      \
+        if (tiles)                                                                                                            \
+            MOE_TILE(kBackwardX, GATED);                                                                                      \
+        else if (once)                                                                                                        \
+            hipLaunchKernelGGL((k_product_stream_back<GATED, true>), grid, stream_block, 0, s, a, g.tiles_c);                 \
+        else                                                                                                                  \
+            hipLaunchKernelGGL((k_product_stream_back<GATED, false>), grid, stream_block, 0, s, a, g.tiles_c);                \
+    } while (0)
     switch (a.kind) {
         case Product::kForward: if (a.gated) MOE_FORWARD(kForward, true); else MOE_FORWARD(kForward, false); break;
         case Product::kForwardI8: if (a.gated) MOE_FORWARD(kForwardI8, true); else MOE_FORWARD(kForwardI8, false); break;
-        case Product::kBackwardX: if (a.gated) MOE_TILE(kBackwardX, true); else MOE_TILE(kBackwardX, false); break;
+        case Product::kBackwardX: if (a.gated) MOE_BACK(true); else MOE_BACK(false); break;
         case Product::kBackwardW: MOE_TILE(kBackwardW, false); break;
     }
+#undef MOE_BACK
 #undef MOE_FORWARD
 #undef MOE_TILE
     return hipGetLastError();
