@@ -824,7 +824,7 @@ __global__ __launch_bounds__(kStreamWaves * kWave, 4) void k_product_stream(Prod
     const unsigned int chunk = lane_chunk(lane);
     const unsigned int wo = lane / 8 * xb + chunk;
     const auto copy_unit = [&](int u, u32x4 *to) {
-        const unsigned int gone = u * kUnitBytes + chunk >= xb ? kPastEnd : 0u;
+        const unsigned int gone = u >= end || u * kUnitBytes + chunk >= xb ? kPastEnd : 0u;
 #pragma unroll
         for (int j = 0; j < kWTiles * 2; ++j) {
             const int row = 8 * j;
@@ -844,7 +844,7 @@ __global__ __launch_bounds__(kStreamWaves * kWave, 4) void k_product_stream(Prod
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const unsigned int at = static_cast<unsigned int>(u * kUnitBytes + h * 64);
-            v.x[h] = __builtin_amdgcn_raw_buffer_load_b128(xbuf, static_cast<int>(at + g * 16 >= xb ? kPastEnd : xo), static_cast<int>(min(at, xb - 1)), 0);
+            v.x[h] = __builtin_amdgcn_raw_buffer_load_b128(xbuf, static_cast<int>(u >= end || at + g * 16 >= xb ? kPastEnd : xo), static_cast<int>(min(at, xb - 1)), 0);
         }
         return v;
     };
@@ -857,21 +857,24 @@ __global__ __launch_bounds__(kStreamWaves * kWave, 4) void k_product_stream(Prod
 #pragma unroll
         for (int i = 0; i < kWTiles; ++i) asm volatile("" : "+v"(acc[i]) : : "memory");
     };
+    // Past the wave's last unit zeros are copied and multiplied: without branches the
+    // loads in flight are counted.  Before a unit's products its copies are there:
+    // in flight are the next one's four and its tokens' two loads.
     if (begin < end) {
         copy_unit(begin, unit0[wave]);
-        if (begin + 1 < end) copy_unit(begin + 1, unit1[wave]);
         Tokens now = load_tokens(begin);
+        copy_unit(begin + 1, unit1[wave]);
         for (int u = begin; u < end; u += 2) {
-            Tokens next = now;
-            if (u + 1 < end) next = load_tokens(u + 1);
+            const Tokens next = load_tokens(u + 1);
+            copies_arrived<kWTiles * 2 + 2>();
             products(unit0[wave], now);
-            if (u + 2 < end) copy_unit(u + 2, unit0[wave]);
-            if (u + 1 < end) {
-                if (u + 2 < end) now = load_tokens(u + 2);
-                products(unit1[wave], next);
-                if (u + 3 < end) copy_unit(u + 3, unit1[wave]);
-            }
+            copy_unit(u + 2, unit0[wave]);
+            now = load_tokens(u + 2);
+            copies_arrived<kWTiles * 2 + 2>();
+            products(unit1[wave], next);
+            copy_unit(u + 3, unit1[wave]);
         }
+        copies_arrived<0>();
     }
     // the sums meet where the weights were
     __syncthreads();
