@@ -229,18 +229,14 @@ struct Feed {
             xo = (wave * 8 + lane / 8) * xb + lane_chunk(lane);
             if constexpr (F::kForward) {
                 left = static_cast<int>(xb);
-                // the wave copies 32 rows of W's place in LDS, in two halves of 16; gated, the
-                // second half of the rows that one wave multiplies (64, or 32 for at most 128
-                // rows q) are the up weights of the first
                 const bool wide = t.rows > 128;
-                const int row = !kSplit ? wave * 32 : (wide ? (wave >> 1) * 32 : wave * 16), row1 = kSplit && !wide ? row : row + 16;
-                const bool up = kSplit && wide && (wave & 1), up1 = kSplit && (!wide || (wave & 1));
+                const WeightRows half = weight_rows(kSplit, wide, wave, 0), half1 = weight_rows(kSplit, wide, wave, 1);
                 const int rows = min(kSplit ? kTileCols / 2 : kTileCols, a.cols - t.c0);
                 const char *const first = static_cast<const char *>(a.w) + (static_cast<size_t>(t.expert) * (kSplit ? 2 : 1) * a.cols + t.c0) * xb;
-                w = first + (static_cast<size_t>(up ? a.cols : 0) + row) * xb;
-                w1 = first + (static_cast<size_t>(up1 ? a.cols : 0) + row1) * xb;
-                w_bytes = max(rows - row, 0) * xb;
-                w1_bytes = max(rows - row1, 0) * xb;
+                w = first + (static_cast<size_t>(half.up ? a.cols : 0) + half.first) * xb;
+                w1 = first + (static_cast<size_t>(half1.up ? a.cols : 0) + half1.first) * xb;
+                w_bytes = bytes_from(half.first, rows, xb);
+                w1_bytes = bytes_from(half1.first, rows, xb);
                 wo = lane / 8 * xb + lane_chunk(lane);
             } else {
                 left = a.inner;
@@ -261,8 +257,7 @@ struct Feed {
 
     // kPastEnd for the lanes whose chunk of the pair lies past the row's end.
     __device__ __forceinline__ unsigned int gone() const {
-        const int bytes = F::kForward ? left : 2 * left;
-        return static_cast<int>(lane_chunk(threadIdx.x & (kWave - 1))) >= bytes ? kPastEnd : 0u;
+        return past_row(F::kForward ? left : 2 * left, threadIdx.x & (kWave - 1));
     }
 
     // Half `half` of the pair's X.
@@ -279,8 +274,9 @@ struct Feed {
             // rows 0-63 and 128-191 of the tile, or those 64 further on
             const auto b = buffer_of(uniform(x), uniform(x_bytes));
             const unsigned int past = gone();
+            const int shared = uniform(shared_offset(at, left, x_bytes));
 #pragma unroll
-            for (int j = 0; j < 2; ++j) copy_to_lds(b, to + (j * 8 + wave) * 64, (x_lane + (j * 128 + half * 64) * xb) | past, uniform(at));
+            for (int j = 0; j < 2; ++j) copy_to_lds(b, to + (j * 8 + wave) * 64, (x_lane + (j * 128 + half * 64) * xb) | past, shared);
         }
     }
     // The pair's W.
@@ -297,10 +293,11 @@ struct Feed {
         } else {
             const unsigned int xb = static_cast<unsigned int>(a.inner) * F::kSize, past = gone();
             const auto b = buffer_of(uniform(w), uniform(w_bytes)), b1 = buffer_of(uniform(w1), uniform(w1_bytes));
+            const int shared = uniform(shared_offset(at, left, w_bytes)), shared1 = uniform(shared_offset(at, left, w1_bytes));
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                copy_to_lds(b, to + (wave * 4 + j) * 64, (w_lane + j * 8 * xb) | past, uniform(at));
-                copy_to_lds(b1, to + (wave * 4 + 2 + j) * 64, (w_lane + j * 8 * xb) | past, uniform(at));
+                copy_to_lds(b, to + (wave * 4 + j) * 64, (w_lane + j * 8 * xb) | past, shared);
+                copy_to_lds(b1, to + (wave * 4 + 2 + j) * 64, (w_lane + j * 8 * xb) | past, shared1);
             }
         }
     }
@@ -824,12 +821,13 @@ __global__ __launch_bounds__(kStreamWaves * kWave, 4) void k_product_stream(Prod
     const unsigned int chunk = lane_chunk(lane);
     const unsigned int wo = lane / 8 * xb + chunk;
     const auto copy_unit = [&](int u, u32x4 *to) {
-        const unsigned int gone = u >= end || u * kUnitBytes + chunk >= xb ? kPastEnd : 0u;
+        const int left = u < end ? static_cast<int>(xb) - u * kUnitBytes : 0, shared = shared_offset(u * kUnitBytes, left, wrows * xb);
+        const unsigned int gone = past_row(left, lane);
 #pragma unroll
         for (int j = 0; j < kWTiles * 2; ++j) {
             const int row = 8 * j;
             const bool is_up = row >= kOutTiles * 16;
-            copy_to_lds<ONCE>(is_up ? w_up : w_gate, to + row * 8, (wo + (is_up ? row - kOutTiles * 16 : row) * xb) | gone, u * kUnitBytes);
+            copy_to_lds<ONCE>(is_up ? w_up : w_gate, to + row * 8, (wo + (is_up ? row - kOutTiles * 16 : row) * xb) | gone, shared);
         }
     };
     Acc<kI8> acc[kWTiles];

@@ -128,8 +128,10 @@ __device__ __forceinline__ u32x2 pack_bf16x4(f32x4 v) {
     return __builtin_bit_cast(u32x2, __builtin_convertvector(v, bf16x4));
 }
 
-// A raw buffer over `bytes` bytes: loads read zeros, stores write nothing, where a
-// lane's 32-bit offset and the one that all lanes share together lie past the end.
+// A raw buffer over `bytes` bytes: loads take a 32-bit offset per lane and read
+// zeros, stores write nothing, where it lies past the end.  An offset that all
+// lanes share is always smaller than `bytes`, or 0: whether the end is found there
+// too does not matter then.
 constexpr int kBufferRsrcWord3 = 0x00020000;
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, unsigned int bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, static_cast<int>(bytes), kBufferRsrcWord3);
