@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <initializer_list>
 #include <vector>
 
 #include "combine_backward.h"
@@ -465,6 +466,15 @@ moe_status segment_arrays(const moe_layout_bufs *layout, const moe_balance_bufs 
     return MOE_OK;
 }
 
+// Whether an output is the buffer of something that the call reads, or of another of
+// its outputs: other workgroups may still read what one has written.
+bool shares_buffer(std::initializer_list<const void *> outputs, std::initializer_list<const void *> inputs) {
+    for (auto o = outputs.begin(); o != outputs.end(); ++o)
+        if (*o != nullptr && (std::find(inputs.begin(), inputs.end(), *o) != inputs.end() || std::find(outputs.begin(), o, *o) != o))
+            return true;
+    return false;
+}
+
 bool channels_ok(int32_t n, int32_t multiple) { return n >= multiple && n % multiple == 0 && n <= moe::kMaxGemmChannels; }
 
 // A bf16 or 8-bit product whose formats and channels are in `a` and were found
@@ -484,8 +494,8 @@ moe_status run_product(const moe_layout_desc *desc, const moe_layout_bufs *layou
     if (!aligned(a.x, 16) || !aligned(a.w, 16) || !aligned(a.out, 16) || !aligned(a.pre, 16) || !aligned(a.pre_in, 16) ||
         !aligned(a.xs, 4) || !aligned(a.ws, 4))
         return MOE_ERR_ALIGN;
-    // other workgroups still read what one has done with
-    if (a.out == a.x || a.out == a.w || (a.pre != nullptr && (a.pre == a.x || a.pre == a.w || a.pre == a.out))) return MOE_ERR_SHAPE;
+    // (out may be pre_in: a lane reads the channels that it writes)
+    if (shares_buffer({a.out, a.pre}, {a.x, a.w, a.xs, a.ws, a.count, a.offset, a.seg_offset, a.slot_expert})) return MOE_ERR_SHAPE;
     return moe::launch_product(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
@@ -678,7 +688,7 @@ moe_status moe_quantize_i8(const void *x, int64_t rows, int32_t H, const int32_t
     if (rows == 0) return MOE_OK;
     if (x == nullptr || codes == nullptr || scales == nullptr) return MOE_ERR_NULL;
     if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(src, 4) || !aligned(scales, 4)) return MOE_ERR_ALIGN;
-    if (x == codes) return MOE_ERR_SHAPE;
+    if (shares_buffer({codes, scales}, {x, src})) return MOE_ERR_SHAPE;
     const moe::QuantizeI8Args a{x, rows, H, src, codes, scales};
     return moe::launch_quantize_i8(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
@@ -689,7 +699,7 @@ moe_status moe_dequantize_i8(const void *codes, const float *scales, int64_t row
     if (rows == 0) return MOE_OK;
     if (codes == nullptr || scales == nullptr || out == nullptr) return MOE_ERR_NULL;
     if (!aligned(codes, 16) || !aligned(out, 16) || !aligned(src, 4) || !aligned(scales, 4)) return MOE_ERR_ALIGN;
-    if (out == codes) return MOE_ERR_SHAPE;
+    if (shares_buffer({out}, {codes, scales, src})) return MOE_ERR_SHAPE;
     const moe::DequantizeI8Args a{codes, scales, rows, H, src, out};
     return moe::launch_dequantize_i8(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
@@ -703,7 +713,7 @@ moe_status moe_dispatch_i8(const moe_layout_desc *desc, const moe_layout_bufs *l
     if (!aligned(hidden, 16) || !aligned(recv, 16) || !aligned(recv_scales, 4) || !aligned(topk_w, 4) || !aligned(recv_w, 4) ||
         !aligned(layout->pos, 4))
         return MOE_ERR_ALIGN;
-    if (hidden == recv) return MOE_ERR_SHAPE;
+    if (shares_buffer({recv, recv_scales, topk_w != nullptr ? recv_w : nullptr}, {hidden, topk_w, layout->pos})) return MOE_ERR_SHAPE;
     const moe::DispatchI8Args a{hidden, desc->S, H, desc->K, layout->pos, topk_w, recv, recv_scales, recv_w};
     return moe::launch_dispatch_i8(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
@@ -718,7 +728,8 @@ moe_status moe_combine_backward(const moe_layout_desc *desc, const moe_layout_bu
     if (!aligned(d_out, 16) || !aligned(expert_out, 16) || !aligned(d_expert_out, 16) || !aligned(w, 4) || !aligned(d_w, 4) ||
         !aligned(layout->pos, 4))
         return MOE_ERR_ALIGN;
-    if (d_expert_out == d_out || (d_w != nullptr && d_w == w)) return MOE_ERR_SHAPE;
+    // (the rows may be expert_out, of which a lane reads the channels that it writes)
+    if (shares_buffer({d_expert_out, d_w}, {d_out, w, layout->pos}) || shares_buffer({d_w}, {expert_out})) return MOE_ERR_SHAPE;
     const moe::CombineBackwardArgs a{d_out, desc->S, H, desc->K, layout->pos, expert_out, w, d_expert_out, d_w};
     return moe::launch_combine_backward(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }

@@ -472,8 +472,9 @@ moe_status moe_expert_gemm_mx4(const moe_layout_desc *desc, const moe_layout_buf
  * shape alone: MOE_ERR_SHAPE where a launch cannot number it (this holds for
  * the calls below too); it always can with (S*K/16 + segments that can hold a
  * row) * ceil(M/32) at most 2^23 - 8.
- * No output of this call or of those below may overlap an input, unless it says
- * so: MOE_ERR_SHAPE where it is the input's own buffer. */
+ * No output of this call or of those below may overlap an input (the arrays of the
+ * layout that the call reads among them) or another output, unless it says so:
+ * MOE_ERR_SHAPE where it is the same buffer, beginning at the same address. */
 moe_status moe_expert_gemm(const moe_layout_desc *desc, const moe_layout_bufs *layout, const moe_balance_bufs *bal,
                            int32_t slots_per_rank, const void *x, int32_t H, const void *w, int32_t N, int32_t act, void *pre,
                            int32_t pre_type, void *out, void *stream);
