@@ -670,11 +670,24 @@ def moe_router_backward(desc: RouterDesc, logits: torch.Tensor, router: Router, 
     return d_logits
 
 
-def _no_capture(what: str):
+# What an autograd function calls forward and backward: a graph can hold these.
+_CAPTURABLE = {
+    "router": (("moe_router",), ("moe_router_backward",)),
+    "balance_loss": (("moe_balance_loss",), ("moe_router_backward",)),
+    "dispatch": (("moe_dispatch", "moe_zero_padding"), ("moe_combine",)),
+    "expert_ffn": (("moe_expert_gemm", "moe_zero_padding"),
+                   ("moe_expert_gemm_backward_x", "moe_expert_gemm_backward_w", "moe_zero_padding")),
+    "combine": (("moe_combine",), ("moe_combine_backward", "moe_zero_padding")),
+}
+
+
+def _no_capture(name: str, backward: bool = False):
     # autograd joins the streams of the leaves that live outside the capture
     if torch.cuda.is_current_stream_capturing():
-        raise RuntimeError(f"{what} cannot be captured into a graph: capture moe_router / moe_balance_loss and "
-                           "moe_router_backward instead")
+        calls = _CAPTURABLE[name]
+        calls = calls[1] if backward else tuple(dict.fromkeys(calls[0] + calls[1]))
+        what = f"the backward pass of {name}" if backward else name
+        raise RuntimeError(f"{what} cannot be captured into a graph: capture {', '.join(calls)} instead")
 
 
 class _RouterFunction(torch.autograd.Function):
@@ -695,7 +708,7 @@ class _RouterFunction(torch.autograd.Function):
         if d_loss is None and d_w is None:
             return None, None, None, None
         logits, token_mask, idx, w, coef = ctx.saved_tensors
-        _no_capture("the backward pass of router / balance_loss")
+        _no_capture("balance_loss" if ctx.given else "router", backward=True)
         d = moe_router_backward(ctx.desc, logits, Router(idx, w, None, coef, None), None if d_w is None else d_w.contiguous(),
                                 None if d_loss is None else d_loss.contiguous(), token_mask)
         return d, None, None, None
@@ -1176,7 +1189,7 @@ class _DispatchFunction(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, d):
-        _no_capture("the backward pass of dispatch")
+        _no_capture("dispatch", backward=True)
         pos, = ctx.saved_tensors
         return moe_combine(ctx.desc, _only(pos=pos), d.contiguous()), None, None
 
@@ -1197,7 +1210,7 @@ class _ExpertFfnFunction(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        _no_capture("the backward pass of expert_ffn")
+        _no_capture("expert_ffn", backward=True)
         x, w_in, w_out, h, pre, count, offset, src, seg, slot_expert = ctx.saved_tensors
         layout = _only(tokens_per_expert=count, expert_offset=offset, src=src)
         balance = Balance(seg, slot_expert, None) if ctx.balanced else None
@@ -1227,7 +1240,7 @@ class _CombineFunction(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, d):
-        _no_capture("the backward pass of combine")
+        _no_capture("combine", backward=True)
         expert_out, w, pos, src = ctx.saved_tensors
         want_y, want_w, want_shared = ctx.needs_input_grad[:3]
         d = d.contiguous()
