@@ -722,8 +722,8 @@ moe_status moe_combine_backward(const moe_layout_desc *desc, const moe_layout_bu
                                 const void *expert_out, const float *w, void *d_expert_out, float *d_w, void *stream) {
     if (desc == nullptr || layout == nullptr) return MOE_ERR_NULL;
     if (!desc_ok(desc) || max_rows(desc) < 0 || !channels_ok(H, 8) || !moe::combine_backward_grid_ok(desc->S)) return MOE_ERR_SHAPE;
+    if (desc->S == 0) return MOE_OK;   // both outputs may be empty arrays, whose addresses are NULL
     if (d_expert_out == nullptr && d_w == nullptr) return MOE_ERR_NULL;
-    if (desc->S == 0) return MOE_OK;
     if (d_out == nullptr || layout->pos == nullptr || (d_w != nullptr && expert_out == nullptr)) return MOE_ERR_NULL;
     if (!aligned(d_out, 16) || !aligned(expert_out, 16) || !aligned(d_expert_out, 16) || !aligned(w, 4) || !aligned(d_w, 4) ||
         !aligned(layout->pos, 4))

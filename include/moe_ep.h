@@ -510,7 +510,7 @@ moe_status moe_expert_gemm_backward_w(const moe_layout_desc *desc, const moe_lay
  *                 it may be expert_out's own buffer.
  *   d_w           [S,K] fp32 or NULL: sum_c d_out[t,c] * expert_out[pos[t,k],c] in
  *                 fp32, 0 where pos[t,k] is -1; needs expert_out.
- * At least one of the two.  d_out [S,H] bf16 (it is shared_out's gradient too);
+ * At least one of the two, unless S = 0.  d_out [S,H] bf16 (it is shared_out's gradient too);
  * w [S,K] fp32 or NULL for weight 1; H % 8 == 0, at most 2^22; S below 2^23.  Rows that hold
  * no entry are neither read nor written.  (The gradient of moe_dispatch's rows
  * with respect to hidden is moe_combine of them with w = NULL.) */
