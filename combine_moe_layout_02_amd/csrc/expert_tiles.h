@@ -213,7 +213,7 @@ inline int64_t most_tiles(const Segments &a, int BM) {
     return std::min(a.entries / BM + used, used * ((a.max_count + BM - 1) / BM));
 }
 
-// Segments with a row, if the routing is at random, and the bytes of their weights.
+// Segments with a row, if the routing is at random.
 inline double used_segments(const Segments &a) {
     return std::max(1.0, a.nseg * -std::expm1(-static_cast<double>(a.entries) / a.nseg));
 }

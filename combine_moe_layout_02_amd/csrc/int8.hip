@@ -10,10 +10,11 @@
 // over the wave by lane swaps and over the waves in LDS.
 //
 // HBM bounds them: 98304 rows of 1408 81 us (5.1 TB/s), 32768 of 7168 117 us (6.0) and
-// back 97 us (7.3), the dispatch of 4096 tokens of 7168 to eight rows each 51 us (5.8).
-// Of a layout's 32768 rows with 1024 in use 14 us, most of it workgroups that find
-// nothing to do; two to eight rows a workgroup, 17 to 30, and a wave for each row of
-// a plain array were slower.
+// back 125 us (5.6; 98 where the same call before left its codes in the Infinity Cache),
+// the dispatch of 4096 tokens of 7168 to eight rows each 51 us (5.8).  Of a layout's
+// 32768 rows with 1024 in use 14 us, back 10, most of it workgroups that find nothing to
+// do; two to eight rows a workgroup took 17 to 30, back 9 to 12 (and 99 to 102, not 98,
+// with every row in use), and a wave for each row of a plain array was slower.
 #include "int8.h"
 #include "mx4.h"   // mx4_absmax
 
