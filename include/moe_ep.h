@@ -456,7 +456,8 @@ moe_status moe_expert_gemm_mx4(const moe_layout_desc *desc, const moe_layout_buf
  *   MOE_ACT_NONE    out[r,n] = bf16( sum_h x[r,h] * w[e,n,h] ),  n < N
  *   MOE_ACT_SWIGLU  out[r,n] = bf16( silu(g) * u ), g = sum_h x[r,h] * w[e,n,h],
  *                   u = sum_h x[r,h] * w[e,N+n,h]
- * with fp32 sums.  The two make an expert's gated feed-forward block:
+ * with fp32 sums; silu(g) is 0 from g = -87.4 on down, where it is below 10^-36 in
+ * magnitude, and NaN at -inf.  The two make an expert's gated feed-forward block:
  * MOE_ACT_SWIGLU with its gate and up weights, MOE_ACT_NONE with its down weights.
  *   x         [max_recv,H], H % 8 == 0.
  *   w         [E,M,H], M = N or (SWIGLU) 2*N; N % 8 == 0.
@@ -489,7 +490,8 @@ moe_status moe_expert_gemm(const moe_layout_desc *desc, const moe_layout_bufs *l
  *             dx[r,h] = bf16( d*u*s*(1 + g*(1-s)) ), dx[r,H+h] = bf16( d*g*s ),
  *             dx [max_recv,2*H], H at most 2^21 (2^20 with fp32); it may be the
  *             buffer of a bf16 pre itself (pre_type), not of an fp32 one.
- * The values at g = -inf or +inf are NaN.  Arguments otherwise as above. */
+ * At g = -inf both values are NaN, at +inf the first is.  silu and its slope are as
+ * in moe_expert_gemm where they are small.  Arguments otherwise as above. */
 moe_status moe_expert_gemm_backward_x(const moe_layout_desc *desc, const moe_layout_bufs *layout, const moe_balance_bufs *bal,
                                       int32_t slots_per_rank, const void *d_out, int32_t N, const void *w, int32_t H,
                                       const void *pre, int32_t pre_type, void *dx, void *stream);
